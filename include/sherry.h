@@ -69,6 +69,20 @@ typedef enum {
     SHERRY_ERR_WORKSPACE = 6          /* the call needs more workspace than sherry_reserve set aside */
 } sherry_status;
 
+/* Element types of the tensors of the feed-forward entry points. */
+typedef enum { SHERRY_F32 = 0, SHERRY_BF16 = 1, SHERRY_F16 = 2 } sherry_dtype;
+
+/* Activations of the feed-forward entry points (Phi: the normal distribution
+ * function). */
+typedef enum {
+    SHERRY_ACT_NONE = 0,
+    SHERRY_ACT_RELU = 1,      /* max(z, 0) */
+    SHERRY_ACT_RELU2 = 2,     /* max(z, 0)^2 */
+    SHERRY_ACT_SILU = 3,      /* z / (1 + e^-z) */
+    SHERRY_ACT_GELU = 4,      /* z Phi(z) */
+    SHERRY_ACT_GELU_TANH = 5  /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+} sherry_act;
+
 /* Short English text for a status value; never NULL. */
 const char* sherry_status_string(int status);
 
@@ -402,6 +416,135 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
                      const float* scale, float* y, int64_t M, int64_t N, int64_t K,
                      void* stream);
 
+/* ===========================================================================
+ * Feed-forward operators: the linear layer with its epilogue, the gated pair
+ * of projections, and their gradients.  (The Sherry page stops at the linear
+ * layer; these entry points are this library's, for the layers around it.)
+ * With q, s the sherry_quant_act rule on x (x itself of any sherry_dtype,
+ * widened to fp32 exactly), acc = q . T^T exactly in int32, and
+ *     z[m][n] = (float)((float)acc[m][n] * alpha[n]) * s[m]  (+ bias[n], fp32)
+ *   linear   y[m][n] = act(z[m][n]) (+ residual[m][n])
+ *   gated    h[m][n] = act(z[m][2n]) * z[m][2n + 1]: row 2n of the weight is
+ *            row n of the gate projection, row 2n + 1 row n of the up
+ *            projection, and alpha, bias and acc are interleaved the same way
+ * in fp32, rounded once to the output's type.  acc, x_i8 and x_scale are
+ * bit-identical to sherry_linear_ex's for the same fp32 activations.
+ * Gradients pass through the quantiser as through the identity (its rounding
+ * has slope 0 almost everywhere): with dz the gradient of z,
+ *     dx[m][k]  = sum_n dz[m][n] alpha[n] T[n][k]
+ *     dalpha[n] = sum_m dz[m][n] acc[m][n] s[m],  dbias[n] = sum_m dz[m][n]
+ *   linear   dz = dy * act'(z)           (the gradient of residual is dy)
+ *   gated    dz[2n] = dh * z[2n + 1] * act'(z[2n]),  dz[2n + 1] = dh * act(z[2n])
+ * The sums over n of dx run in integers: dz * alpha of a token becomes fixed
+ * point below the token's largest |dz * alpha| (16 bits for SHERRY_BF16, 31
+ * for SHERRY_F32 and SHERRY_F16), cut into signed base-256 digits that the
+ * tensor cores multiply with T exactly.  A token whose dz * alpha holds an
+ * Inf or NaN gives a dx row of NaN.  Results do not depend on the launch
+ * shape or on the order of any sum across blocks: the same call gives the
+ * same bits.
+ * Tensors are dense row-major.  Workspace, concurrency and errors are those
+ * of sherry_linear; an output may not overlap an input, except y == residual.
+ * =========================================================================== */
+
+/* sherry_quant_act for x of any element type (x [M][K], 16-byte aligned). */
+int sherry_quant_act_dt(const void* x, int x_dtype, int64_t M, int64_t K, int8_t* x_i8,
+                        float* x_scale, void* stream);
+
+/*
+ * sherry_repack_gated -- device, asynchronous.  As sherry_repack, of two
+ * canonical code streams of one shape: the native layout of the 2N-row weight
+ * whose rows 2n and 2n + 1 are row n of `gate` and of `up`.
+ *   native_dev [out] sherry_native_bytes(2N, K) bytes, 16-byte aligned
+ */
+int sherry_repack_gated(const uint8_t* gate_dev, const uint8_t* up_dev, int64_t N, int64_t K,
+                        void* native_dev, void* stream);
+
+/*
+ * sherry_linear_epilogue -- device, asynchronous.  The linear layer above.
+ *   x        [in]  x_dtype [M][K], 16-byte aligned
+ *   bias     [in]  fp32 [N] or NULL;  act: sherry_act
+ *   residual [in]  x_dtype [M][N] or NULL; may be y itself
+ *   y        [out] x_dtype [M][N]
+ *   acc      [out] int32 [M][N] or NULL (kept for sherry_linear_grad)
+ *   x_i8, x_scale  [out] int8 [M][K] (16-byte aligned) and fp32 [M], as in
+ *            sherry_linear_ex: given, they hold the quantised activations;
+ *            x_i8 == NULL uses the reserved buffer.  x_scale alone may be
+ *            given (kept for the gradient).
+ * Wnative, alpha, and what may run before the call: as sherry_linear_ex; bias
+ * and residual may be written by the kernel launched just before.
+ */
+int sherry_linear_epilogue(const void* x, int x_dtype, const void* Wnative, const float* alpha,
+                           const float* bias, int act, const void* residual, void* y, int32_t* acc,
+                           int8_t* x_i8, float* x_scale, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * sherry_gated -- device, asynchronous.  Both projections, the activation and
+ * the product in one contraction kernel (for one token also the quantiser).
+ *   Wnative  [in]  from sherry_repack_gated;  alpha, bias fp32 [2N] interleaved
+ *   h        [out] x_dtype [M][N];  acc [out] int32 [M][2N] interleaved, or NULL
+ * Other arguments as sherry_linear_epilogue; 2N must be below 2^31.
+ */
+int sherry_gated(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias,
+                 int act, void* h, int32_t* acc, int8_t* x_i8, float* x_scale, int64_t M, int64_t N,
+                 int64_t K, void* stream);
+
+/* Bytes of the transposed layout that the gradients read, for an R x K weight
+ * (R = 2N for a gated pair): ceil(K/128) * ceil(R/128) * 4096, 2 bits a
+ * weight.  Returns 0 for invalid shapes. */
+size_t sherry_transposed_bytes(int64_t R, int64_t K);
+
+/*
+ * sherry_repack_t, sherry_repack_gated_t -- device, asynchronous.  Canonical
+ * codes -> the transposed layout (0, 1 for +1, 2 for -1), once per weight.
+ * Block (k tile, row tile) of 128 k x 128 rows: [piece 2][k 128][word 4];
+ * word i of piece q of a k covers rows 64 q + 16 i .. + 15 of the block, the
+ * weight of row 4 c + e among them at bit 2 (c & 1) + 16 (c >> 1) + 4 e, so
+ * that one shift and mask give four byte selectors.  Padding is zero.
+ *   out_dev [out] sherry_transposed_bytes bytes, 16-byte aligned
+ */
+int sherry_repack_t(const uint8_t* codes_dev, int64_t N, int64_t K, void* out_dev, void* stream);
+int sherry_repack_gated_t(const uint8_t* gate_dev, const uint8_t* up_dev, int64_t N, int64_t K,
+                          void* out_dev, void* stream);
+
+/* Bytes of the caller's work buffer of a gradient call with M tokens, R rows
+ * and tensors of `dtype`: the digits of dz * alpha and one scale per token.
+ * Returns 0 for invalid arguments. */
+size_t sherry_grad_work_bytes(int dtype, int64_t M, int64_t R);
+
+/* Tokens of int8 digits per token of a gradient call: sherry_reserve(this
+ * times M, ..) sets aside the split-K workspace of sherry_linear_grad and
+ * sherry_gated_grad.  0 for an invalid dtype. */
+int sherry_grad_digits(int dtype);
+
+/*
+ * sherry_linear_grad -- device, asynchronous.  Gradients of
+ * sherry_linear_epilogue.
+ *   dy       [in]  dtype [M][N]
+ *   acc      [in]  int32 [M][N], x_scale fp32 [M], from the forward call; acc
+ *            may be NULL when act is SHERRY_ACT_NONE and dalpha is NULL, and
+ *            x_scale when acc is
+ *   Wt       [in]  from sherry_repack_t, 16-byte aligned; may be NULL when dx is
+ *   alpha, bias, act  as in the forward call
+ *   dx       [out] dtype [M][K] or NULL
+ *   dalpha, dbias [out] fp32 [N] or NULL, overwritten
+ *   work     sherry_grad_work_bytes(dtype, M, N) bytes, 16-byte aligned; may
+ *            be NULL when dx is
+ * N below 2^24.  At least one output must be given.
+ */
+int sherry_linear_grad(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                       const float* alpha, const float* bias, int act, void* dx, float* dalpha,
+                       float* dbias, void* work, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * sherry_gated_grad -- device, asynchronous.  Gradients of sherry_gated: dh
+ * dtype [M][N]; acc int32 [M][2N] and x_scale required; Wt from
+ * sherry_repack_gated_t; alpha, bias, dalpha, dbias fp32 [2N] interleaved;
+ * work sherry_grad_work_bytes(dtype, M, 2N) bytes.  2N below 2^24.
+ */
+int sherry_gated_grad(const void* dh, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                      const float* alpha, const float* bias, int act, void* dx, float* dalpha,
+                      float* dbias, void* work, int64_t M, int64_t N, int64_t K, void* stream);
+
 /*
  * sherry_selftest_wait -- device, asynchronous.  A check of failure
  * detection (no counterpart on the page): one warp waits, with the bounded
@@ -427,8 +570,9 @@ size_t sherry_workspace_bytes(int64_t max_M, int64_t max_K);
  * the workspace of every later call with M <= max_M and K <= max_K (any N):
  * sherry_gemm, sherry_gemm_acc, sherry_gemm_tc, sherry_linear(_ex) and the
  * W4A8 tensor-core entry points.  Grows what an earlier call reserved (never
- * shrinks it); when it grows it first waits for the device to be idle, then
- * frees the old buffer, allocates and zero-fills the new one.  Call it before
+ * shrinks it).  When the activation buffer grows, it first waits for the
+ * device to be idle and frees the old one; the split-K workspace's older
+ * buffers stay (captured graphs may hold their address).  Call it before
  * capturing a stream into a CUDA graph and before timing.  The asynchronous
  * entry points never allocate: without enough workspace they return
  * SHERRY_ERR_WORKSPACE.  Calls whose tensor-core launch splits no tile over

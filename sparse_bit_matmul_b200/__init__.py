@@ -10,6 +10,7 @@ raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -29,6 +30,9 @@ ABI_SYMBOLS = (
     "sherry_w4a8_packed_bytes", "sherry_w4a8_native_bytes", "sherry_w4a8_pack", "sherry_w4a8_unpack",
     "sherry_w4a8_repack", "sherry_w4a8_gemm", "sherry_w4a8_gemm_acc", "sherry_w4a8_gemm_tc",
     "sherry_w4a8_gemm_gemv",
+    "sherry_quant_act_dt", "sherry_repack_gated", "sherry_linear_epilogue", "sherry_gated",
+    "sherry_transposed_bytes", "sherry_repack_t", "sherry_repack_gated_t", "sherry_grad_work_bytes",
+    "sherry_grad_digits", "sherry_linear_grad", "sherry_gated_grad",
 )
 
 _lib = None
@@ -85,6 +89,20 @@ def load() -> ctypes.CDLL:
     L.sherry_w4a8_gemm_acc.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp]
     L.sherry_w4a8_gemm_tc.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp]
     L.sherry_w4a8_gemm_gemv.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp]
+    L.sherry_quant_act_dt.argtypes = [vp, c_int, i64, i64, vp, vp, vp]
+    L.sherry_repack_gated.argtypes = [vp, vp, i64, i64, vp, vp]
+    L.sherry_linear_epilogue.argtypes = [vp, c_int, vp, vp, vp, c_int, vp, vp, vp, vp, vp, i64, i64, i64, vp]
+    L.sherry_gated.argtypes = [vp, c_int, vp, vp, vp, c_int, vp, vp, vp, vp, i64, i64, i64, vp]
+    L.sherry_transposed_bytes.argtypes = [i64, i64]
+    L.sherry_transposed_bytes.restype = ctypes.c_size_t
+    L.sherry_repack_t.argtypes = [vp, i64, i64, vp, vp]
+    L.sherry_repack_gated_t.argtypes = [vp, vp, i64, i64, vp, vp]
+    L.sherry_grad_work_bytes.argtypes = [c_int, i64, i64]
+    L.sherry_grad_work_bytes.restype = ctypes.c_size_t
+    L.sherry_grad_digits.argtypes = [c_int]
+    grad = [vp, c_int, vp, vp, vp, vp, vp, c_int, vp, vp, vp, vp, i64, i64, i64, vp]
+    L.sherry_linear_grad.argtypes = grad
+    L.sherry_gated_grad.argtypes = grad
     for name in ABI_SYMBOLS:
         getattr(L, name).restype = getattr(L, name).restype or c_int
     _lib = L
@@ -273,34 +291,336 @@ def selftest_wait(limit_ns: int, stream=None):
     _check(load().sherry_selftest_wait(int(limit_ns), st), "sherry_selftest_wait")
 
 
+# --------------------------------------------------- feed-forward operators
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}   # sherry_act
+_DTYPES = {}            # torch dtype -> sherry_dtype, filled on first use
+_split_reserved = set()  # devices whose split-K workspace covers every call
+SPLIT_MAX_M = 1536      # from this many tokens on the split-K workspace no longer grows
+
+
+def _ffn_types():
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    return torch, _DTYPES
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _check_tensor(t, name: str, dtype, shape, device):
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous {dtype} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}, strides {tuple(t.stride())}")
+    return t.data_ptr()
+
+
+def _activation(act: str) -> int:
+    a = ACTIVATIONS.get("none" if act is None else act)
+    if a is None:
+        raise ValueError(f"act: want one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return a
+
+
+def _matrix(t, name: str, types):
+    """Shape and sherry_dtype of a [M][.] tensor of a feed-forward call."""
+    _need(t.dim() == 2 and t.is_cuda and t.is_contiguous() and t.dtype in types,
+          f"{name}: want a contiguous 2-D CUDA tensor of float32, bfloat16 or float16, got {t.dtype} "
+          f"{tuple(t.shape)} on {t.device}, strides {tuple(t.stride())}")
+    return t.shape[0], t.shape[1], types[t.dtype]
+
+
+def _on_device(fn):
+    """Runs a call with its first argument's device current."""
+    @functools.wraps(fn)
+    def call(x, *args, **kwargs):
+        import torch
+        if not x.is_cuda or x.device.index == torch.cuda.current_device():
+            return fn(x, *args, **kwargs)
+        with torch.cuda.device(x.device):
+            return fn(x, *args, **kwargs)
+    return call
+
+
+def _ensure_split(t):
+    """Sets aside the whole split-K workspace (about 15 MB, once per device), so that it never moves
+    under a captured graph."""
+    import torch
+    idx = t.device.index
+    if idx in _split_reserved:
+        return
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("the workspace is not set aside yet: call reserve_split() before capturing a graph")
+    reserve_split(idx)
+
+
+def reserve_split(device=None):
+    """Sets aside, host-synchronously, the split-K workspace of every linear_epilogue, gated and gradient
+    call on `device` (default: the current one).  The first such call does it too; do it before
+    capturing a graph."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device("cuda", device) \
+        if isinstance(device, int) else torch.device(device)
+    idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    with torch.cuda.device(idx):
+        _check(load().sherry_reserve(SPLIT_MAX_M, 1), "sherry_reserve")
+    _split_reserved.add(idx)
+
+
+@_on_device
+def repack_gated(gate_dev, up_dev, N: int, K: int, out=None):
+    """Canonical codes of a gate and an up projection [N][5K/32] on the device -> the native layout of the
+    2N-row weight whose rows 2n, 2n + 1 are row n of each."""
+    import torch
+    if out is None:
+        out = torch.empty(native_bytes(2 * N, K), dtype=torch.uint8, device=gate_dev.device)
+    _check(load().sherry_repack_gated(_dptr(gate_dev), _dptr(up_dev), N, K, _dptr(out), _stream(gate_dev)),
+           "sherry_repack_gated")
+    return out
+
+
+def transposed_bytes(R: int, K: int) -> int:
+    return int(load().sherry_transposed_bytes(R, K))
+
+
+@_on_device
+def repack_t(codes_dev, N: int, K: int, out=None):
+    """Canonical codes on the device -> the transposed layout the gradients read."""
+    import torch
+    if out is None:
+        out = torch.empty(transposed_bytes(N, K), dtype=torch.uint8, device=codes_dev.device)
+    _check(load().sherry_repack_t(_dptr(codes_dev), N, K, _dptr(out), _stream(codes_dev)), "sherry_repack_t")
+    return out
+
+
+@_on_device
+def repack_gated_t(gate_dev, up_dev, N: int, K: int, out=None):
+    """repack_t of the interleaved 2N-row weight of repack_gated."""
+    import torch
+    if out is None:
+        out = torch.empty(transposed_bytes(2 * N, K), dtype=torch.uint8, device=gate_dev.device)
+    _check(load().sherry_repack_gated_t(_dptr(gate_dev), _dptr(up_dev), N, K, _dptr(out), _stream(gate_dev)),
+           "sherry_repack_gated_t")
+    return out
+
+
+def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s):
+    torch, types = _ffn_types()
+    M, K, dt = _matrix(x, "x", types)
+    a = _activation(act)
+    R = 2 * N if gated else N
+    dev = x.device
+    _need(N > 0 and K > 0 and K % 32 == 0, f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
+    wp = _check_tensor(w_native, "w_native", torch.uint8, (-(-R // 128) * -(-K // 128) * 2560,), dev)
+    ap = _check_tensor(alpha, "alpha", torch.float32, (R,), dev)
+    bp = None if bias is None else _check_tensor(bias, "bias", torch.float32, (R,), dev)
+    rp = None if residual is None else _check_tensor(residual, "residual", x.dtype, (M, N), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _check_tensor(out, "out", x.dtype, (M, N), dev)
+    cp = None if acc is None else _check_tensor(acc, "acc", torch.int32, (M, R), dev)
+    qp = None if out_q is None else _check_tensor(out_q, "out_q", torch.int8, (M, K), dev)
+    sp = None if out_s is None else _check_tensor(out_s, "out_s", torch.float32, (M,), dev)
+    if M == 0:
+        return out
+    if M > 1 or qp is not None:
+        # the call's own activation buffers: nothing is shared with other streams or graphs
+        if qp is None:
+            q = torch.empty((M, K), dtype=torch.int8, device=dev)
+            qp = q.data_ptr()
+        if sp is None:
+            s = torch.empty(M, dtype=torch.float32, device=dev)
+            sp = s.data_ptr()
+    if dev.index not in _split_reserved:
+        _ensure_split(x)
+    L = _lib or load()
+    st = torch.cuda.current_stream(dev).cuda_stream
+    if gated:
+        rc = L.sherry_gated(x.data_ptr(), dt, wp, ap, bp, a, op, cp, qp, sp, M, N, K, st)
+    else:
+        rc = L.sherry_linear_epilogue(x.data_ptr(), dt, wp, ap, bp, a, rp, op, cp, qp, sp, M, N, K, st)
+    if rc != OK:
+        _check(rc, "sherry_gated" if gated else "sherry_linear_epilogue")
+    return out
+
+
+@_on_device
+def linear_epilogue(x, w_native, alpha, N: int, bias=None, act: str = "none", residual=None, out=None, acc=None,
+                    out_q=None, out_s=None):
+    """y [M][N] = act(linear(x) + bias) + residual in one contraction (sherry_linear_epilogue).
+
+    x, residual and y are float32, bfloat16 or float16 (one type per call); bias fp32 [N]; act a key of
+    ACTIVATIONS.  out may be residual itself.  acc int32 [M][N], out_q int8 [M][K] and out_s fp32 [M]
+    receive the exact sums, the quantised activations and their scales (linear_backward needs acc and
+    out_s)."""
+    return _forward(False, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s)
+
+
+@_on_device
+def gated(x, w_native, alpha, N: int, bias=None, act: str = "silu", out=None, acc=None, out_q=None, out_s=None):
+    """h [M][N] = act(gate(x)) * up(x) in one contraction (sherry_gated).
+
+    w_native from repack_gated; alpha, bias fp32 [2N] and acc int32 [M][2N] interleave gate and up
+    (entries 2n, 2n + 1).  Other arguments as linear_epilogue."""
+    return _forward(True, x, w_native, alpha, N, bias, act, None, out, acc, out_q, out_s)
+
+
+def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales):
+    torch, types = _ffn_types()
+    M, N, dt = _matrix(dy, "dy", types)
+    a = _activation(act)
+    R = 2 * N if gated else N
+    dev = dy.device
+    _need(N > 0 and K > 0 and K % 32 == 0, f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
+    _need(want_dx or want_scales, "nothing to compute")
+    need_acc = gated or a != 0 or want_scales
+    _need(acc is not None or not need_acc, "acc: needed for this gradient")
+    _need(acc is None or x_scale is not None, "x_scale: needed with acc")
+    ap = _check_tensor(alpha, "alpha", torch.float32, (R,), dev)
+    bp = None if bias is None else _check_tensor(bias, "bias", torch.float32, (R,), dev)
+    cp = None if acc is None else _check_tensor(acc, "acc", torch.int32, (M, R), dev)
+    sp = None if x_scale is None else _check_tensor(x_scale, "x_scale", torch.float32, (M,), dev)
+    dx = wp = xp = kp = dalpha = dbias = None
+    if want_dx:
+        wp = _check_tensor(w_t, "w_t", torch.uint8, (-(-R // 128) * -(-K // 128) * 4096,), dev)
+        dx = out if out is not None else torch.empty((M, K), dtype=dy.dtype, device=dev)
+        xp = dx.data_ptr() if out is None else _check_tensor(out, "out", dy.dtype, (M, K), dev)
+    if want_scales:
+        make = torch.empty if M else torch.zeros
+        dalpha = make(R, dtype=torch.float32, device=dev)
+        dbias = make(R, dtype=torch.float32, device=dev)
+    if M == 0:
+        return dx, dalpha, dbias
+    L = _lib or load()
+    if want_dx:
+        work = torch.empty(L.sherry_grad_work_bytes(dt, M, R), dtype=torch.uint8, device=dev)
+        kp = work.data_ptr()
+        if dev.index not in _split_reserved:
+            _ensure_split(dy)
+    fn = L.sherry_gated_grad if gated else L.sherry_linear_grad
+    rc = fn(dy.data_ptr(), dt, cp, sp, wp, ap, bp, a, xp, None if dalpha is None else dalpha.data_ptr(),
+            None if dbias is None else dbias.data_ptr(), kp, M, N, K, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != OK:
+        _check(rc, "sherry_gated_grad" if gated else "sherry_linear_grad")
+    return dx, dalpha, dbias
+
+
+@_on_device
+def linear_backward(dy, w_t, alpha, K: int, acc=None, x_scale=None, bias=None, act: str = "none", out=None,
+                    want_dx: bool = True, want_scales: bool = True):
+    """Gradients of linear_epilogue: (dx [M][K] of dy's type, dalpha fp32 [N], dbias fp32 [N]).
+
+    dy [M][N]; w_t from repack_t; acc and x_scale as the forward call gave them (acc and out_s), bias and
+    act as it took them.  want_dx / want_scales False leave out dx / dalpha and dbias (None in their
+    place); with act "none" and want_scales False acc and x_scale are not needed.  The gradient of the
+    residual is dy itself."""
+    return _backward(False, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales)
+
+
+@_on_device
+def gated_backward(dh, w_t, alpha, K: int, acc, x_scale, bias=None, act: str = "silu", out=None,
+                   want_dx: bool = True, want_scales: bool = True):
+    """Gradients of gated: (dx [M][K], dalpha fp32 [2N], dbias fp32 [2N], interleaved).  w_t from
+    repack_gated_t; other arguments as linear_backward."""
+    return _backward(True, dh, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales)
+
+
 class PackedLinear:
     """Weights of one Sherry linear layer resident on the device.
 
     ``PackedLinear.from_weights(W)`` packs on the host (sherry_pack), copies
     the canonical codes and alpha to the device and repacks them into the
     kernel-native layout.  ``forward(x)`` quantises the activations and runs
-    the GEMM (sherry_linear), asynchronously on the current stream.
+    the GEMM (sherry_linear), asynchronously on the current stream; with a
+    bias, an activation or a residual, or 16-bit activations, it is
+    sherry_linear_epilogue.  ``trainable=True`` also lays out the transposed
+    weight that ``backward`` reads.
     """
 
-    def __init__(self, w_native, alpha, N: int, K: int):
-        self.w_native, self.alpha, self.N, self.K = w_native, alpha, N, K
+    def __init__(self, w_native, alpha, N: int, K: int, w_t=None):
+        self.w_native, self.alpha, self.N, self.K, self.w_t = w_native, alpha, N, K, w_t
 
     @classmethod
-    def from_weights(cls, W: np.ndarray, device="cuda"):
+    def from_weights(cls, W: np.ndarray, device="cuda", trainable: bool = False):
         import torch
         codes, alpha = pack(W)
-        return cls.from_codes(codes, alpha, W.shape[1], device)
+        return cls.from_codes(codes, alpha, W.shape[1], device, trainable)
 
     @classmethod
-    def from_codes(cls, codes: np.ndarray, alpha: np.ndarray, K: int, device="cuda"):
+    def from_codes(cls, codes: np.ndarray, alpha: np.ndarray, K: int, device="cuda", trainable: bool = False):
         import torch
         N = codes.shape[0]
         codes_d = torch.from_numpy(codes).to(device)
         w_native = repack(codes_d, N, K)
-        return cls(w_native, torch.from_numpy(alpha).to(device), N, K)
+        return cls(w_native, torch.from_numpy(alpha).to(device), N, K, repack_t(codes_d, N, K) if trainable else None)
 
-    def forward(self, x, out=None):
-        return linear(x, self.w_native, self.alpha, self.N, out=out)
+    def forward(self, x, out=None, bias=None, act: str = "none", residual=None, acc=None, out_s=None):
+        import torch
+        if x.dtype is torch.float32 and bias is None and act in (None, "none") and residual is None and out_s is None:
+            return linear(x, self.w_native, self.alpha, self.N, out=out, acc=acc)
+        return linear_epilogue(x, self.w_native, self.alpha, self.N, bias=bias, act=act, residual=residual, out=out,
+                               acc=acc, out_s=out_s)
+
+    def backward(self, dy, acc=None, x_scale=None, bias=None, act: str = "none", want_dx: bool = True,
+                 want_scales: bool = True):
+        """linear_backward of this layer: (dx, dalpha, dbias)."""
+        _need(self.w_t is not None or not want_dx, "backward: the layer was made without trainable=True")
+        return linear_backward(dy, self.w_t, self.alpha, self.K, acc, x_scale, bias=bias, act=act, want_dx=want_dx,
+                               want_scales=want_scales)
+
+
+class GatedFFN:
+    """A gated feed-forward block over packed weights: y = down(act(gate(x)) * up(x)) + residual.
+
+    ``GatedFFN.from_weights(W_gate, W_up, W_down)`` (fp32 [F][K], [F][K], [K2][F]) packs on the host;
+    ``forward(x, residual)`` is two contractions, each with its epilogue.  With ``trainable=True``,
+    ``forward(x, residual, keep=True)`` also returns what ``backward(dy, kept)`` needs for the gradients
+    of x and of the scales (the packed weights themselves stay as they are).
+    """
+
+    def __init__(self, w_native, alpha, down: PackedLinear, F: int, K: int, act: str = "silu", w_t=None):
+        self.w_native, self.alpha, self.down, self.F, self.K, self.act, self.w_t = w_native, alpha, down, F, K, act, w_t
+
+    @classmethod
+    def from_weights(cls, W_gate: np.ndarray, W_up: np.ndarray, W_down: np.ndarray, act: str = "silu", device="cuda",
+                     trainable: bool = False):
+        import torch
+        _need(W_gate.shape == W_up.shape and W_down.shape[1] == W_gate.shape[0],
+              f"GatedFFN: shapes {W_gate.shape}, {W_up.shape}, {W_down.shape} do not chain")
+        _activation(act)
+        F, K = W_gate.shape
+        (cg, ag), (cu, au) = pack(W_gate), pack(W_up)
+        cg, cu = torch.from_numpy(cg).to(device), torch.from_numpy(cu).to(device)
+        alpha = torch.from_numpy(np.ascontiguousarray(np.stack([ag, au], 1).reshape(-1))).to(device)
+        return cls(repack_gated(cg, cu, F, K), alpha, PackedLinear.from_weights(W_down, device, trainable), F, K, act,
+                   repack_gated_t(cg, cu, F, K) if trainable else None)
+
+    def forward(self, x, residual=None, keep: bool = False):
+        import torch
+        if not keep:
+            h = gated(x, self.w_native, self.alpha, self.F, act=self.act)
+            return linear_epilogue(h, self.down.w_native, self.down.alpha, self.down.N, residual=residual)
+        M = x.shape[0]
+        acc = torch.empty((M, 2 * self.F), dtype=torch.int32, device=x.device)
+        acc_d = torch.empty((M, self.down.N), dtype=torch.int32, device=x.device)
+        s, s_d = (torch.empty(M, dtype=torch.float32, device=x.device) for _ in range(2))
+        h = gated(x, self.w_native, self.alpha, self.F, act=self.act, acc=acc, out_s=s)
+        y = linear_epilogue(h, self.down.w_native, self.down.alpha, self.down.N, residual=residual, acc=acc_d, out_s=s_d)
+        return y, (acc, s, acc_d, s_d)
+
+    def backward(self, dy, kept, want_dx: bool = True, want_scales: bool = True):
+        """(dx, dalpha fp32 [2F] interleaved, dalpha of the down projection fp32 [K2]); the gradient of the
+        residual is dy itself."""
+        _need(self.w_t is not None, "backward: the block was made without trainable=True")
+        acc, s, acc_d, s_d = kept
+        dh, dalpha_d, _ = self.down.backward(dy, acc_d, s_d, want_scales=want_scales)
+        dx, dalpha, _ = gated_backward(dh, self.w_t, self.alpha, self.K, acc, s, act=self.act, want_dx=want_dx,
+                                       want_scales=want_scales)
+        return dx, dalpha, dalpha_d
 
 
 # ------------------------------------------------ W4A8 FastGEMM (SINT4 x int8)

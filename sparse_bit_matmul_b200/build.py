@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libsherry_b200.so")
-SOURCES = ["sherry_cuda.cu", "sherry_host.cpp"]
+SOURCES = ["sherry_cuda.cu", "ffn_cuda.cu", "sherry_host.cpp"]
 HEADERS = sorted(f for f in os.listdir(os.path.join(os.path.dirname(os.path.abspath(__file__)), "csrc"))
                  if f.endswith((".h", ".cuh")))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -47,15 +47,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     objs = []
     build_dir = os.path.join(HERE, "_build")
     os.makedirs(build_dir, exist_ok=True)
-    for src in SOURCES:
+    jobs = []
+    for src in SOURCES:                    # one compiler per source, side by side
         obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
         cmd = [NVCC, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if verbose or res.returncode != 0:
-            sys.stderr.write(res.stdout + res.stderr)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}")
+        jobs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         objs.append(obj)
+    outs = [(src, job.communicate()[0], job.returncode) for src, job in jobs]
+    for src, out, rc in outs:
+        if verbose or rc != 0:
+            sys.stderr.write(out)
+    for src, out, rc in outs:
+        if rc != 0:
+            raise RuntimeError(f"nvcc failed for {src}")
     tmp = SO + ".tmp"
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xcompiler", "-fopenmp",
            "-o", tmp, *objs, "-lgomp"]

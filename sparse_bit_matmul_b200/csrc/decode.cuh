@@ -38,10 +38,19 @@
 //     banks.
 //   * The K-parts of a row are summed in shared memory and the epilogue writes
 //     y (and acc) with coalesced stores.
+//
+// With EP (the feed-forward entry points of ffn_cuda.cu) the activations may
+// be 16-bit (XT), and the epilogue adds bias, activation and residual, or
+// multiplies act(row 2n) with row 2n + 1 (CTAs own whole pairs: row ranges
+// begin at multiples of 4).  The bias and residual of a thread's first output
+// are fetched before the decode loop, so that their latency hides behind it.
 #pragma once
 
 #include <cstdint>
 
+#include <type_traits>
+
+#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "sherry_internal.h"
@@ -74,6 +83,32 @@ struct Params {
     int NS;                      // ring slots of code steps held in shared memory (NS >= CPT: all of them)
     int S;                       // bytes between consecutive K chunks of the int8 activation buffer
 };
+
+struct EpParams : Params {
+    const float* bias;           // [N] or null
+    const void* res;             // [M][No] or null
+    void* out;                   // [M][No]: No = N, or N / 2 when gated
+    int dtype;                   // sherry_dtype of x (FUSED), res and out
+    int act;                     // sherry_act
+    int gated;
+};
+
+// Four consecutive activations as fp32 (16-bit types widen exactly).
+template <class XT>
+__device__ __forceinline__ float4 load_x4(const XT* row, int i)
+{
+    if constexpr (std::is_same_v<XT, float>) {
+        return reinterpret_cast<const float4*>(row)[i];
+    } else {
+        const uint2 w = reinterpret_cast<const uint2*>(row)[i];
+        if constexpr (std::is_same_v<XT, __nv_bfloat16>)
+            return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+}
 
 // Shared memory: table | scales | warp maxima (two token slots) | partial sums [P][M][R] |
 // alpha [R] | code ring [NS][P][5][R] words | activations [M][Kc][S] int8.
@@ -454,7 +489,7 @@ __device__ __forceinline__ void cp_async_wait_pending(int n)
 // the row in registers (all loads in flight at once); XV = 0 streams it from
 // global memory twice.  Whether the row is in registers is a compile-time
 // property of each instantiation.
-template <int XV>
+template <int XV, class XT = float>
 __device__ __forceinline__ void fused_activations(const Params& p, int8_t* qbuf, int QK, int S, float* scale_s,
                                                   float* warp_max, int M, int K4)
 {
@@ -463,7 +498,7 @@ __device__ __forceinline__ void fused_activations(const Params& p, int8_t* qbuf,
     constexpr bool in_regs = XV > 0;
     constexpr int NV = XV > 0 ? XV : 1;
     for (int m = 0; m < M; ++m) {
-        const float4* xr = reinterpret_cast<const float4*>(p.x + (int64_t)m * p.K);
+        const XT* xr = reinterpret_cast<const XT*>(p.x) + (int64_t)m * p.K;
         int8_t* qr = qbuf + m * QK;
         float4 v[NV];
         float mx = 0.0f;
@@ -475,13 +510,13 @@ __device__ __forceinline__ void fused_activations(const Params& p, int8_t* qbuf,
             // all loads in flight at once
 #pragma unroll
             for (int u = 0; u < XV; ++u)
-                if (u < nsl) v[u] = xr[tid + u * nthr];
+                if (u < nsl) v[u] = load_x4<XT>(xr, tid + u * nthr);
 #pragma unroll
             for (int u = 0; u < XV; ++u)
                 if (u < nsl) mx = fmaxf(mx, quant::absmax4(v[u]));
         } else {
 #pragma unroll 4
-            for (int i = tid; i < K4; i += nthr) mx = fmaxf(mx, quant::absmax4(xr[i]));
+            for (int i = tid; i < K4; i += nthr) mx = fmaxf(mx, quant::absmax4(load_x4<XT>(xr, i)));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -512,7 +547,7 @@ __device__ __forceinline__ void fused_activations(const Params& p, int8_t* qbuf,
             }
         } else {
             for (int i = tid; i < K4; i += nthr) {
-                const uint32_t w = quant::quantise4(xr[i], sc);
+                const uint32_t w = quant::quantise4(load_x4<XT>(xr, i), sc);
                 *reinterpret_cast<uint32_t*>(qr + (i >> 5) * S + 4 * (i & 31)) = w;
                 if (qo) qo[i] = w;
             }
@@ -520,9 +555,9 @@ __device__ __forceinline__ void fused_activations(const Params& p, int8_t* qbuf,
     }
 }
 
-template <int MT, bool FUSED, int RT>
+template <int MT, bool FUSED, int RT, class XT = float, bool EP = false>
 __global__ void __launch_bounds__(kMaxThreads, 2)
-    sherry_decode_kernel(const Params p)
+    sherry_decode_kernel(const std::conditional_t<EP, EpParams, Params> p)
 {
     static_assert(RT == 1 || RT == 2 || RT == 4, "rows per thread");
     static_assert(kMaxRing <= 4, "cp_async_wait_pending covers up to 3 pending groups");
@@ -587,8 +622,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
         // rows of up to kXV float4s per thread are held in registers; longer
         // rows stream from global memory (XV = 0)
         float* warp_max = reinterpret_cast<float*>(smem + kOffWarpMax);
-        if (K4 <= kXV * nthr) fused_activations<kXV>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
-        else fused_activations<0>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
+        if (K4 <= kXV * nthr) fused_activations<kXV, XT>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
+        else fused_activations<0, XT>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
     } else {
         // plain 16-byte loads, so that the copy groups in flight are the code steps only
         const int K16 = (int)(p.K >> 4);
@@ -614,6 +649,27 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     // the next kernel may start now: its weight prefetch overlaps this decode
     // instead of queueing in front of this CTA's activation reads
     ptx::pdl_launch_dependents();
+
+    // outputs of this CTA: one per (token, row) or (token, row pair)
+    int O = M * Rc;
+    [[maybe_unused]] int Rw = Rc;                            // outputs per token
+    [[maybe_unused]] float pre_b0 = 0.0f, pre_b1 = 0.0f, pre_r = 0.0f;
+    if constexpr (EP) {
+        if (p.gated) Rw = Rc >> 1;
+        O = M * Rw;
+        if (tid < O) {
+            const int m = tid / Rw, ii = tid - m * Rw;
+            if (p.gated) {
+                if (p.bias) {
+                    pre_b0 = p.bias[r0 + 2 * ii];
+                    pre_b1 = p.bias[r0 + 2 * ii + 1];
+                }
+            } else {
+                if (p.bias) pre_b0 = p.bias[r0 + ii];
+                if (p.res) pre_r = ep::load_elem(p.res, m * p.N + r0 + ii, p.dtype);
+            }
+        }
+    }
 
     // ---- decode + dp4a: RT rows per thread, one ring step at a time -----------------
     // Step k holds chunk part * CPT + k of every part.  When the codes stream,
@@ -740,15 +796,45 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
                 for (int r = 0; r < RT; ++r) red[(part * M + m) * R + qi * RT + r] = acc[r][m];
     }
     __syncthreads();
-    const int O = M * Rc;
-    // output o = (token m, row i): one thread sums its P partials
-    for (int idx = tid; idx < O; idx += nthr) {
-        const int m = idx / Rc, ii = idx - m * Rc;
-        int32_t a32 = 0;
-        for (int pp = 0; pp < P; ++pp) a32 += red[(pp * M + m) * R + ii];
-        const int64_t n = r0 + ii;
-        if (p.acc) p.acc[m * p.N + n] = a32;
-        if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)a32, alpha_sm[ii]), scale_s[m]);
+    if constexpr (EP) {
+        for (int idx = tid; idx < O; idx += nthr) {
+            const int m = idx / Rw, ii = idx - m * Rw;
+            const int i0 = p.gated ? 2 * ii : ii;
+            const int64_t n = r0 + i0;
+            const bool first_out = idx == tid;
+            int32_t a0 = 0, a1 = 0;
+            for (int pp = 0; pp < P; ++pp) {
+                const int32_t* rp = red + (pp * M + m) * R + i0;
+                a0 += rp[0];
+                if (p.gated) a1 += rp[1];
+            }
+            const float s = scale_s[m];
+            float z0 = __fmul_rn(__fmul_rn((float)a0, alpha_sm[i0]), s);
+            if (p.bias) z0 = __fadd_rn(z0, first_out ? pre_b0 : p.bias[n]);
+            float y = ep::act_one(z0, p.act);
+            if (p.gated) {
+                float z1 = __fmul_rn(__fmul_rn((float)a1, alpha_sm[i0 + 1]), s);
+                if (p.bias) z1 = __fadd_rn(z1, first_out ? pre_b1 : p.bias[n + 1]);
+                y = __fmul_rn(y, z1);
+            } else if (p.res) {
+                y = __fadd_rn(y, first_out ? pre_r : ep::load_elem(p.res, m * p.N + n, p.dtype));
+            }
+            if (p.acc) {
+                p.acc[m * p.N + n] = a0;
+                if (p.gated) p.acc[m * p.N + n + 1] = a1;
+            }
+            ep::store_elem(p.out, m * (p.gated ? p.N >> 1 : p.N) + (p.gated ? n >> 1 : n), y, p.dtype);
+        }
+    } else {
+        // output o = (token m, row i): one thread sums its P partials
+        for (int idx = tid; idx < O; idx += nthr) {
+            const int m = idx / Rc, ii = idx - m * Rc;
+            int32_t a32 = 0;
+            for (int pp = 0; pp < P; ++pp) a32 += red[(pp * M + m) * R + ii];
+            const int64_t n = r0 + ii;
+            if (p.acc) p.acc[m * p.N + n] = a32;
+            if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)a32, alpha_sm[ii]), scale_s[m]);
+        }
     }
 }
 

@@ -1,0 +1,125 @@
+// Element types, activations and their slopes, shared by the epilogues of the
+// forward kernels (tc_gemm.cuh, decode.cuh) and the gradient kernels
+// (grad.cuh).
+//
+// act(z):
+//   none z | relu max(z, 0) | relu2 max(z, 0)^2 | gelu z Phi(z), Phi the
+//   normal distribution function | silu z S(z) | gelu_tanh z S(t(z)) with
+//   t(z) = 2 sqrt(2/pi) (z + 0.044715 z^3), S the logistic function
+//   (z/2 (1 + tanh(t/2)) = z S(t)).
+// silu and gelu_tanh share one body.
+// S(t) = 1 / (1 + e^-t) with the hardware exponential: e^-t overflows to
+// infinity for t < -88, where S is 0 to fp32 either way, and its relative
+// error (a few 2^-24 for |t| up to 10) reaches the result scaled by
+// 1 - S(t), so the larger half of the values hardly sees it.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sherry.h"
+
+namespace sherry {
+namespace ep {
+
+__host__ __device__ inline int elem_size(int dtype) { return dtype == SHERRY_F32 ? 4 : 2; }
+
+__device__ __forceinline__ float from16(uint16_t u, int dtype)
+{
+    return dtype == SHERRY_BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+}
+
+__device__ __forceinline__ uint16_t to16(float v, int dtype)
+{
+    return dtype == SHERRY_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+// element `i` of a tensor of `dtype`
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype)
+{
+    if (dtype == SHERRY_F32) return static_cast<const float*>(p)[i];
+    return from16(static_cast<const uint16_t*>(p)[i], dtype);
+}
+
+__device__ __forceinline__ void store_elem(void* p, int64_t i, float v, int dtype)
+{
+    if (dtype == SHERRY_F32) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = to16(v, dtype);
+}
+
+constexpr float kGeluC1 = 1.5957691216057308f;       // 2 sqrt(2 / pi)
+constexpr float kGeluC3 = 0.0713548162726009f;       // 2 sqrt(2 / pi) 0.044715
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+__device__ __forceinline__ float logistic(float t) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-t))); }
+
+// t(z) of silu and gelu_tanh (silu apart: z^2 may overflow)
+__device__ __forceinline__ float sigmoid_arg(float z, bool silu)
+{
+    return silu ? z : __fmul_rn(z, __fmaf_rn(__fmul_rn(z, z), kGeluC3, kGeluC1));
+}
+
+// max(z, 0); NaN stays NaN
+__device__ __forceinline__ float relu(float z) { return z < 0.0f ? 0.0f : z; }
+
+// act over an array held in registers: one switch for the whole array
+template <int N>
+__device__ __forceinline__ void apply_act(float (&v)[N], int act)
+{
+    if (act == SHERRY_ACT_NONE) return;
+    if (act == SHERRY_ACT_SILU || act == SHERRY_ACT_GELU_TANH) {
+        const bool silu = act == SHERRY_ACT_SILU;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __fmul_rn(v[i], logistic(sigmoid_arg(v[i], silu)));
+    } else if (act == SHERRY_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = __fmul_rn(__fmul_rn(0.5f, v[i]), __fadd_rn(1.0f, erff(__fmul_rn(v[i], kSqrtHalf))));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float r = relu(v[i]);
+            v[i] = act == SHERRY_ACT_RELU2 ? __fmul_rn(r, r) : r;
+        }
+    }
+}
+
+__device__ __forceinline__ float act_one(float z, int act)
+{
+    float v[1] = {z};
+    apply_act<1>(v, act);
+    return v[0];
+}
+
+// act(z) and its derivative (0 at the corner of relu)
+__device__ __forceinline__ void act_slope(float z, int act, float& f, float& d)
+{
+    if (act == SHERRY_ACT_NONE) {
+        f = z;
+        d = 1.0f;
+    } else if (act == SHERRY_ACT_SILU || act == SHERRY_ACT_GELU_TANH) {
+        // d/dz [z S(t)] = S + z S (1 - S) t',  t' = 1 or c1 + 3 c3 z^2
+        const bool silu = act == SHERRY_ACT_SILU;
+        const float s = logistic(sigmoid_arg(z, silu));
+        const float t1 = silu ? 1.0f : __fmaf_rn(__fmul_rn(z, z), 3.0f * kGeluC3, kGeluC1);
+        f = __fmul_rn(z, s);
+        // a far z: z^2 may overflow where S (1 - S) is 0
+        const float w = __fmul_rn(s, __fsub_rn(1.0f, s));
+        d = w == 0.0f ? s : __fmaf_rn(__fmul_rn(z, w), t1, s);
+    } else if (act == SHERRY_ACT_GELU) {
+        // d/dz [z Phi(z)] = Phi + z phi
+        const float phi_cdf = __fmul_rn(0.5f, __fadd_rn(1.0f, erff(__fmul_rn(z, kSqrtHalf))));
+        const float pdf = __fmul_rn(kInvSqrt2Pi, expf(__fmul_rn(-0.5f, __fmul_rn(z, z))));
+        f = __fmul_rn(z, phi_cdf);
+        d = pdf == 0.0f ? phi_cdf : __fmaf_rn(z, pdf, phi_cdf);
+    } else {
+        const float r = relu(z);
+        f = act == SHERRY_ACT_RELU2 ? __fmul_rn(r, r) : r;
+        d = z > 0.0f ? (act == SHERRY_ACT_RELU2 ? __fmul_rn(2.0f, z) : 1.0f) : 0.0f;
+    }
+}
+
+}  // namespace ep
+}  // namespace sherry

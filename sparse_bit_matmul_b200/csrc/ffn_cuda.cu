@@ -1,0 +1,582 @@
+// Feed-forward operators of the C ABI (include/sherry.h): the linear layer
+// with bias, activation and residual, the gated pair of projections, their
+// gradients, and the weight layouts they read.  The contractions are the
+// decode and tensor-core kernels of decode.cuh and tc_gemm.cuh with other
+// epilogues; grad.cuh holds the elementwise half of the gradients.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "sherry.h"
+#include "sherry_internal.h"
+#include "host_common.h"
+#include "decode.cuh"
+#include "grad.cuh"
+#include "quant.cuh"
+#include "tc_gemm.cuh"
+
+namespace sherry {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Activation quantiser for 16-bit activations: the rule and the shape of
+// quant_act_kernel (one block per token, the row held in registers between
+// the absmax and the quantisation when it fits), eight values per load.
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 512;
+constexpr int kQuantXV = 4;                 // rows up to 16384 in registers
+
+template <class XT>
+__device__ __forceinline__ void widen8(const uint4& w, float4& a, float4& b)
+{
+    const uint2 lo = make_uint2(w.x, w.y), hi = make_uint2(w.z, w.w);
+    a = decode::load_x4<XT>(reinterpret_cast<const XT*>(&lo), 0);
+    b = decode::load_x4<XT>(reinterpret_cast<const XT*>(&hi), 0);
+}
+
+template <class XT>
+__global__ void __launch_bounds__(kQuantThreads)
+    quant_act16_kernel(const XT* __restrict__ x, int64_t K, int8_t* __restrict__ q, float* __restrict__ scale)
+{
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    const int64_t m = blockIdx.x;
+    const uint4* xr = reinterpret_cast<const uint4*>(x + m * K);
+    uint2* qw = reinterpret_cast<uint2*>(q + m * K);
+    const int K8 = (int)(K / 8);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool in_regs = K8 <= kQuantXV * kQuantThreads;
+
+    uint4 v[kQuantXV];
+    float a = 0.0f;
+    auto absmax8 = [](const uint4& w) {
+        float4 f, g;
+        widen8<XT>(w, f, g);
+        return fmaxf(quant::absmax4(f), quant::absmax4(g));
+    };
+    if (in_regs) {
+#pragma unroll
+        for (int u = 0; u < kQuantXV; ++u) {
+            const int idx = tid + u * kQuantThreads;
+            v[u] = idx < K8 ? xr[idx] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < kQuantXV; ++u) a = fmaxf(a, absmax8(v[u]));
+    } else {
+#pragma unroll 4
+        for (int i = tid; i < K8; i += kQuantThreads) a = fmaxf(a, absmax8(xr[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    __shared__ float warp_max[kQuantThreads / 32];
+    if (lane == 0) warp_max[warp] = a;
+    __syncthreads();
+    a = lane < kQuantThreads / 32 ? warp_max[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+
+    const quant::Scale sc = quant::make_scale(a);
+    if (tid == 0) scale[m] = sc.s;
+    auto quantise8 = [&sc](const uint4& w) {
+        float4 f, g;
+        widen8<XT>(w, f, g);
+        return make_uint2(quant::quantise4(f, sc), quant::quantise4(g, sc));
+    };
+    if (in_regs) {
+#pragma unroll
+        for (int u = 0; u < kQuantXV; ++u) {
+            const int idx = tid + u * kQuantThreads;
+            if (idx < K8) qw[idx] = quantise8(v[u]);
+        }
+    } else {
+#pragma unroll 4
+        for (int i = tid; i < K8; i += kQuantThreads) qw[i] = quantise8(xr[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Weight layouts (one thread per output word, once per weight).
+// ---------------------------------------------------------------------------
+// Canonical row `r` of a weight, or of the gated pair (rows 2n, 2n + 1).
+struct Codes {
+    const uint8_t* a;
+    const uint8_t* b;           // up projection, or null
+    int64_t row_bytes;
+    __device__ __forceinline__ const uint8_t* row(int64_t r) const
+    {
+        return b ? ((r & 1) ? b : a) + (r >> 1) * row_bytes : a + r * row_bytes;
+    }
+};
+
+__global__ void repack_gated_kernel(Codes codes, int64_t R, int64_t K, uint32_t* __restrict__ out, int64_t words)
+{
+    const int64_t Kc = sherry_k_chunks(K);
+    for (int64_t idx = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; idx < words;
+         idx += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t j = (idx / SHERRY_TILE_ROWS) % SHERRY_CHUNK_WORDS;
+        const int64_t r = (idx - 8 * j) & (SHERRY_TILE_ROWS - 1);
+        const int64_t c = (idx / (SHERRY_TILE_ROWS * SHERRY_CHUNK_WORDS)) % Kc;
+        const int64_t n = idx / (SHERRY_TILE_ROWS * SHERRY_CHUNK_WORDS * Kc) * SHERRY_TILE_ROWS + r;
+        const int64_t b0 = c * (SHERRY_CHUNK_WORDS * 4) + 4 * j;
+        uint32_t w = 0;
+        if (n < R) {
+            const uint8_t* src = codes.row(n);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (b0 + b < codes.row_bytes) w |= (uint32_t)src[b0 + b] << (8 * b);
+        }
+        out[idx] = w;
+    }
+}
+
+__global__ void repack_t_kernel(Codes codes, int64_t R, int64_t K, uint32_t* __restrict__ out, int64_t words)
+{
+    const int64_t RT = sherry_row_tiles(R);
+    for (int64_t idx = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; idx < words;
+         idx += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t i = idx & 3, kk = (idx >> 2) & 127, q = (idx >> 9) & 1, blk = idx >> 10;
+        const int64_t rt = blk % RT, k = blk / RT * SHERRY_KCHUNK + kk;
+        const int64_t n0 = rt * SHERRY_TILE_ROWS + 64 * q + 16 * i;
+        const int64_t bit = 5 * (k >> 2);
+        const int64_t byte = bit >> 3;
+        const uint32_t pos = (uint32_t)(k & 3);
+        uint32_t w = 0;
+        for (int e = 0; e < 16; ++e) {
+            const int64_t n = n0 + e;
+            if (n >= R || k >= K) break;
+            const uint8_t* src = codes.row(n);
+            uint32_t two = src[byte];
+            if (byte + 1 < codes.row_bytes) two |= (uint32_t)src[byte + 1] << 8;
+            const uint32_t code = (two >> (bit & 7)) & 31u, z = code & 3u;
+            if (pos == z) continue;
+            const uint32_t t = ((code >> (2 + pos - (pos > z ? 1u : 0u))) & 1u) ? 2u : 1u;
+            const int c = e >> 2;
+            w |= t << (2 * (c & 1) + 16 * (c >> 1) + 4 * (e & 3));
+        }
+        out[idx] = w;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host helpers
+// ---------------------------------------------------------------------------
+// Runs `set` once per device (function attributes belong to a context); a
+// device beyond the 64 tracked runs it every time.
+template <class F>
+int once_per_device(std::atomic<uint64_t>& done, F set)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SHERRY_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return SHERRY_OK;
+    if (set() != cudaSuccess) return SHERRY_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_release);
+    return SHERRY_OK;
+}
+
+bool dtype_ok(int dtype) { return dtype == SHERRY_F32 || dtype == SHERRY_BF16 || dtype == SHERRY_F16; }
+bool act_ok(int act) { return act >= SHERRY_ACT_NONE && act <= SHERRY_ACT_GELU_TANH; }
+bool aligned_elem(const void* p, int dtype)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(ep::elem_size(dtype) - 1)) == 0;
+}
+
+// out [Mo][No]: boxes of box_n columns x box_m rows, for complete tiles
+int make_out_map(CUtensorMap* map, void* out, int dtype, int64_t Mo, int64_t No, int box_n, int box_m)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return SHERRY_ERR_CUDA;
+    const CUtensorMapDataType t = dtype == SHERRY_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : dtype == SHERRY_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    cuuint64_t dims[2] = {(cuuint64_t)No, (cuuint64_t)Mo};
+    cuuint64_t strides[1] = {(cuuint64_t)No * ep::elem_size(dtype)};
+    cuuint32_t box[2] = {(cuuint32_t)box_n, (cuuint32_t)box_m};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, t, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SHERRY_OK
+               : SHERRY_ERR_CUDA;
+}
+
+// One tensor-core launch.  b: int8 rows [p.M][p.K], ld bytes apart.  p holds
+// the problem; tiles, workspace and status are filled in here.
+template <int BN, int SC, int WF, int EK, int D>
+int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, cudaStream_t stream)
+{
+    using C = tc::Cfg<BN, SC, WF>;
+    DeviceInfo di;
+    int st = device_info(&di);
+    if (st != SHERRY_OK) return st;
+    p.y = nullptr;
+    p.TM = (p.M + BN - 1) / BN;
+    p.TN = sherry_row_tiles(p.N);
+    p.Kc = sherry_k_chunks(p.K);
+    p.U = p.TM * p.TN * p.Kc;
+    const int64_t grid = tc_grid(p.TM * p.TN, p.U, di.sms, p.Kc, BN);
+    p.ws = nullptr;
+    p.counters = nullptr;
+    if ((p.TM * p.TN) % grid != 0) {
+        void* ws = nullptr;
+        const size_t ws_acc = (size_t)grid * BN * SHERRY_TILE_ROWS * sizeof(int32_t);
+        st = get_workspace(ws_acc + (size_t)grid * sizeof(uint32_t), &ws);
+        if (st != SHERRY_OK) return st;
+        p.ws = static_cast<int32_t*>(ws);
+        p.counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + ws_acc);
+    }
+    p.status = device_status_ptr();
+    if (!p.status) return SHERRY_ERR_CUDA;
+
+    CUtensorMap map, omap;
+    st = make_x_map(&map, b, p.M, p.K, ld, BN);
+    if (st != SHERRY_OK) return st;
+    std::memset(&omap, 0, sizeof(omap));
+    p.y_tma = (p.No * ep::elem_size(p.dtype)) % 16 == 0 && aligned16(p.out);
+    if (p.y_tma && make_out_map(&omap, p.out, p.dtype, p.Mo, p.No, EK == tc::kEpGated ? 16 : 32, C::kSlice / D) != SHERRY_OK)
+        p.y_tma = 0;
+
+    const int smem = std::max(C::kSmemBytes, 120 * 1024);    // one CTA per SM
+    if (smem > di.max_smem_optin) return SHERRY_ERR_DEVICE;
+    auto kernel = tc::sherry_gemm_tc_kernel<BN, SC, WF, EK, D>;
+    static std::atomic<uint64_t> done{0};
+    st = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (st != SHERRY_OK) return st;
+    return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream, map, omap, p));
+}
+
+// The token tiles of sherry_gemm_tc (its measurements hold: the loads, decode
+// and MMAs are the same).
+template <int EK>
+int launch_forward_tc(const int8_t* b, const tc::EpParams& p, cudaStream_t s)
+{
+    constexpr int W = tc::kWeightSherry;
+    if (p.M <= 16) return launch_tc<16, 4, W, EK, 1>(b, p.K, p, s);
+    if (p.M <= 32) return launch_tc<32, 4, W, EK, 1>(b, p.K, p, s);
+    if (p.M <= 64) return launch_tc<64, 4, W, EK, 1>(b, p.K, p, s);
+    if (p.M < 1536) return launch_tc<128, 2, W, EK, 1>(b, p.K, p, s);
+    return launch_tc<192, 1, W, EK, 1>(b, p.K, p, s);
+}
+
+template <int D>
+int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, cudaStream_t s)
+{
+    constexpr int W = tc::kWeightT2, EK = tc::kEpGrad;
+    if (p.M <= 16) return launch_tc<16, 4, W, EK, D>(b, ld, p, s);
+    if (p.M <= 32) return launch_tc<32, 4, W, EK, D>(b, ld, p, s);
+    if (p.M <= 64) return launch_tc<64, 2, W, EK, D>(b, ld, p, s);
+    if (p.M < 1536) return launch_tc<128, 2, W, EK, D>(b, ld, p, s);
+    return launch_tc<192, 1, W, EK, D>(b, ld, p, s);
+}
+
+template <int MT, bool FUSED, int RT, class XT>
+int launch_decode_rt(const decode::EpParams& p, const decode::Plan& pl, cudaStream_t stream)
+{
+    auto kernel = decode::sherry_decode_kernel<MT, FUSED, RT, XT, true>;
+    static std::atomic<uint64_t> done{0};
+    const int st = once_per_device(done, [&] {
+        // one carveout for every shape, so that the next call's CTAs share the SM
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, decode::kSmemBudgetMax);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        return e;
+    });
+    if (st != SHERRY_OK) return st;
+    return cuda_status(launch_pdl(kernel, dim3((unsigned)pl.G), dim3((unsigned)pl.threads), (size_t)pl.smem, stream, p));
+}
+
+template <int MT, bool FUSED, class XT>
+int launch_decode(decode::EpParams p, const decode::Plan& pl, const DeviceInfo& di, cudaStream_t stream)
+{
+    p.Kc = sherry_k_chunks(p.K);
+    p.G = pl.G;
+    p.R = pl.R;
+    p.Q = pl.Q;
+    p.P = pl.P;
+    p.CPT = pl.CPT;
+    p.NS = pl.NS;
+    p.S = pl.S;
+    if (pl.smem > di.max_smem_optin) return SHERRY_ERR_DEVICE;
+    if (pl.RT == 4) return launch_decode_rt<MT, FUSED, 4, XT>(p, pl, stream);
+    if (pl.RT == 2) return launch_decode_rt<MT, FUSED, 2, XT>(p, pl, stream);
+    return launch_decode_rt<MT, FUSED, 1, XT>(p, pl, stream);
+}
+
+// Both forward operators: R weight rows, No output columns.
+int forward(const void* x, int dtype, const void* wn, const float* alpha, const float* bias, int act,
+            const void* res, void* out, int32_t* acc, int8_t* x_i8, float* x_scale, int64_t M, int64_t R, int64_t No,
+            int64_t K, bool gated, cudaStream_t s)
+{
+    if (!dtype_ok(dtype) || !act_ok(act)) return SHERRY_ERR_INVALID_ARG;
+    if (!x || !wn || !alpha || !out || (x_i8 && !x_scale)) return SHERRY_ERR_INVALID_ARG;
+    if (M <= 0 || No <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
+    if (!sherry_shape_ok(M, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x) || !aligned16(wn) || (x_i8 && !aligned16(x_i8))) return SHERRY_ERR_INVALID_ARG;
+    if (!aligned_elem(out, dtype) || (res && !aligned_elem(res, dtype))) return SHERRY_ERR_INVALID_ARG;
+    DeviceInfo di;
+    int st = device_info(&di);
+    if (st != SHERRY_OK) return st;
+
+    decode::Plan pl;
+    const bool few = M <= SHERRY_GEMM_DECODE_AUTO_MAX_M && decode::plan(R, sherry_k_chunks(K), M, di.sms, &pl);
+    decode::EpParams d = {};
+    if (few) {
+        d.wnative = static_cast<const uint8_t*>(wn);
+        d.alpha = alpha;
+        d.acc = acc;
+        d.M = M;
+        d.N = R;
+        d.K = K;
+        d.bias = bias;
+        d.res = res;
+        d.out = out;
+        d.dtype = dtype;
+        d.act = act;
+        d.gated = gated ? 1 : 0;
+    }
+    if (few && M <= SHERRY_LINEAR_FUSED_MAX_M) {
+        static_assert(SHERRY_LINEAR_FUSED_MAX_M == 1, "fused launches instantiated for one token");
+        d.x = static_cast<const float*>(x);
+        d.xq_out = x_i8;
+        d.xs_out = x_scale;
+        if (dtype == SHERRY_F32) return launch_decode<1, true, float>(d, pl, di, s);
+        if (dtype == SHERRY_BF16) return launch_decode<1, true, __nv_bfloat16>(d, pl, di, s);
+        return launch_decode<1, true, __half>(d, pl, di, s);
+    }
+    if (!x_i8) {
+        void* buf = nullptr;
+        st = get_act_buffer(act_buffer_bytes(M, K), &buf);
+        if (st != SHERRY_OK) return st;
+        x_i8 = static_cast<int8_t*>(buf);
+        if (!x_scale)
+            x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + (((size_t)M * (size_t)K + 255) & ~size_t(255)));
+    }
+    st = sherry_quant_act_dt(x, dtype, M, K, x_i8, x_scale, s);
+    if (st != SHERRY_OK) return st;
+    if (few) {
+        d.xq = x_i8;
+        d.x_scale = x_scale;
+        return launch_decode<2, false, float>(d, pl, di, s);
+    }
+    tc::EpParams p = {};
+    p.wnative = static_cast<const uint8_t*>(wn);
+    p.alpha = alpha;
+    p.x_scale = x_scale;
+    p.acc = acc;
+    p.M = M;
+    p.N = R;
+    p.K = K;
+    p.bias = bias;
+    p.res = res;
+    p.out = out;
+    p.Mo = M;
+    p.No = No;
+    p.dtype = dtype;
+    p.act = act;
+    return gated ? launch_forward_tc<tc::kEpGated>(x_i8, p, s) : launch_forward_tc<tc::kEpLinear>(x_i8, p, s);
+}
+
+// Row stride of the digit rows: whole 16-byte units (TMA).
+int64_t digit_ld(int64_t R) { return (R + 15) & ~int64_t(15); }
+
+int64_t digit_bytes(int dtype, int64_t M, int64_t R)
+{
+    return ((int64_t)sherry_grad_digits(dtype) * M * digit_ld(R) + 255) & ~int64_t(255);
+}
+
+constexpr int64_t kGradMaxRows = (int64_t(1) << 24) - 1;
+
+constexpr int kDigitsSmemMax = 200 * 1024;
+
+template <bool GATED, int D>
+int launch_digits(grad::Params g, cudaStream_t s)
+{
+    auto kernel = grad::grad_digits_kernel<GATED, D>;
+    static std::atomic<uint64_t> done{0};
+    const int st = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDigitsSmemMax);
+    });
+    if (st != SHERRY_OK) return st;
+    const int64_t need = ((g.R + 3) & ~int64_t(3)) * 4;
+    const int smem = need <= kDigitsSmemMax ? (int)need : 0;
+    g.cache = smem / 4;
+    const int threads = g.R >= 8192 ? 1024 : g.R >= 1024 ? 256 : 128;
+    return cuda_status(launch_pdl(kernel, dim3((unsigned)g.M), dim3((unsigned)threads), (size_t)smem, s, g));
+}
+
+int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* wt, const float* alpha,
+             const float* bias, int act, void* dx, float* dalpha, float* dbias, void* work, int64_t M, int64_t R,
+             int64_t No, int64_t K, bool gated, cudaStream_t s)
+{
+    if (!dtype_ok(dtype) || !act_ok(act)) return SHERRY_ERR_INVALID_ARG;
+    if (!dy || !alpha || (!dx && !dalpha && !dbias)) return SHERRY_ERR_INVALID_ARG;
+    if (dx && (!wt || !work)) return SHERRY_ERR_INVALID_ARG;
+    if (!acc && (gated || act != SHERRY_ACT_NONE || dalpha)) return SHERRY_ERR_INVALID_ARG;
+    if (acc && !x_scale) return SHERRY_ERR_INVALID_ARG;
+    if (M <= 0 || No <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
+    if (!sherry_shape_ok(M, R, K) || R > kGradMaxRows || M > SHERRY_MAX_DIM / 4) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned_elem(dy, dtype) || (reinterpret_cast<uintptr_t>(acc) & 7u)) return SHERRY_ERR_INVALID_ARG;
+    if (dx && (!aligned16(wt) || !aligned16(work) || !aligned_elem(dx, dtype))) return SHERRY_ERR_INVALID_ARG;
+    DeviceInfo di;
+    int st = device_info(&di);
+    if (st != SHERRY_OK) return st;
+
+    const int D = sherry_grad_digits(dtype);
+    grad::Params g = {};
+    g.dy = dy;
+    g.acc = acc;
+    g.x_scale = x_scale;
+    g.alpha = alpha;
+    g.bias = bias;
+    g.dtype = dtype;
+    g.act = act;
+    g.M = M;
+    g.R = R;
+    g.No = No;
+    g.ld = digit_ld(R);
+    g.dig = static_cast<int8_t*>(work);
+    g.dscale = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + digit_bytes(dtype, M, R));
+    g.vec = R % 4 == 0 && aligned16(dy) && aligned16(acc) && aligned16(alpha) && aligned16(bias);
+    g.dalpha = dalpha;
+    g.dbias = dbias;
+    if (dx) {
+        if (gated) st = D == 2 ? launch_digits<true, 2>(g, s) : launch_digits<true, 4>(g, s);
+        else st = D == 2 ? launch_digits<false, 2>(g, s) : launch_digits<false, 4>(g, s);
+        if (st != SHERRY_OK) return st;
+    }
+    if (dalpha || dbias) {
+        const dim3 grid((unsigned)((No + 31) / 32)), block(32 * grad::kColWarps);
+        const cudaError_t e = gated ? launch_pdl(grad::grad_columns_kernel<true>, grid, block, 0, s, g)
+                                    : launch_pdl(grad::grad_columns_kernel<false>, grid, block, 0, s, g);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    if (!dx) return SHERRY_OK;
+    tc::EpParams p = {};
+    p.wnative = static_cast<const uint8_t*>(wt);
+    p.x_scale = g.dscale;
+    p.M = M * D;
+    p.N = K;
+    p.K = R;
+    p.out = dx;
+    p.Mo = M;
+    p.No = K;
+    p.dtype = dtype;
+    return D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, s) : launch_grad_tc<4>(g.dig, g.ld, p, s);
+}
+
+int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)
+{
+    if (!a || !out) return SHERRY_ERR_INVALID_ARG;
+    if (N <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
+    if (!sherry_shape_ok(1, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(out)) return SHERRY_ERR_INVALID_ARG;
+    const int64_t words = (int64_t)((transposed ? sherry_transposed_bytes(R, K) : sherry_native_bytes(R, K)) / 4);
+    const int threads = 256;
+    const unsigned blocks = (unsigned)std::min<int64_t>((words + threads - 1) / threads, 148 * 32);
+    const Codes codes = {a, b, K / 32 * 5};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (transposed) repack_t_kernel<<<blocks, threads, 0, s>>>(codes, R, K, static_cast<uint32_t*>(out), words);
+    else repack_gated_kernel<<<blocks, threads, 0, s>>>(codes, R, K, static_cast<uint32_t*>(out), words);
+    return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+}  // namespace sherry
+
+using namespace sherry;
+
+extern "C" {
+
+int sherry_quant_act_dt(const void* x, int x_dtype, int64_t M, int64_t K, int8_t* x_i8, float* x_scale, void* stream)
+{
+    if (!dtype_ok(x_dtype)) return SHERRY_ERR_INVALID_ARG;
+    if (x_dtype == SHERRY_F32)
+        return sherry_quant_act(static_cast<const float*>(x), M, K, x_i8, x_scale, stream);
+    if (!x || !x_i8 || !x_scale) return SHERRY_ERR_INVALID_ARG;
+    if (M <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
+    if (!sherry_shape_ok(M, 1, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x) || !aligned16(x_i8)) return SHERRY_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const dim3 grid((unsigned)M), block(kQuantThreads);
+    if (x_dtype == SHERRY_BF16)
+        return cuda_status(launch_pdl(quant_act16_kernel<__nv_bfloat16>, grid, block, 0, s,
+                                      static_cast<const __nv_bfloat16*>(x), K, x_i8, x_scale));
+    return cuda_status(launch_pdl(quant_act16_kernel<__half>, grid, block, 0, s, static_cast<const __half*>(x), K, x_i8,
+                                  x_scale));
+}
+
+int sherry_repack_gated(const uint8_t* gate_dev, const uint8_t* up_dev, int64_t N, int64_t K, void* native_dev,
+                        void* stream)
+{
+    if (!up_dev) return SHERRY_ERR_INVALID_ARG;
+    if (N > SHERRY_MAX_DIM / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    return repack(false, gate_dev, up_dev, N, 2 * N, K, native_dev, stream);
+}
+
+int sherry_repack_t(const uint8_t* codes_dev, int64_t N, int64_t K, void* out_dev, void* stream)
+{
+    return repack(true, codes_dev, nullptr, N, N, K, out_dev, stream);
+}
+
+int sherry_repack_gated_t(const uint8_t* gate_dev, const uint8_t* up_dev, int64_t N, int64_t K, void* out_dev,
+                          void* stream)
+{
+    if (!up_dev) return SHERRY_ERR_INVALID_ARG;
+    if (N > SHERRY_MAX_DIM / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    return repack(true, gate_dev, up_dev, N, 2 * N, K, out_dev, stream);
+}
+
+int sherry_linear_epilogue(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias,
+                           int act, const void* residual, void* y, int32_t* acc, int8_t* x_i8, float* x_scale,
+                           int64_t M, int64_t N, int64_t K, void* stream)
+{
+    return forward(x, x_dtype, Wnative, alpha, bias, act, residual, y, acc, x_i8, x_scale, M, N, N, K, false,
+                   static_cast<cudaStream_t>(stream));
+}
+
+int sherry_gated(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias, int act,
+                 void* h, int32_t* acc, int8_t* x_i8, float* x_scale, int64_t M, int64_t N, int64_t K, void* stream)
+{
+    if (N > SHERRY_MAX_DIM / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    return forward(x, x_dtype, Wnative, alpha, bias, act, nullptr, h, acc, x_i8, x_scale, M, 2 * N, N, K, true,
+                   static_cast<cudaStream_t>(stream));
+}
+
+size_t sherry_transposed_bytes(int64_t R, int64_t K)
+{
+    if (!sherry_shape_ok(1, R, K)) return 0;
+    return (size_t)sherry_row_tiles(R) * (size_t)sherry_k_chunks(K) * SHERRY_T2_CHUNK_BYTES;
+}
+
+int sherry_grad_digits(int dtype) { return dtype == SHERRY_BF16 ? 2 : dtype == SHERRY_F32 || dtype == SHERRY_F16 ? 4 : 0; }
+
+size_t sherry_grad_work_bytes(int dtype, int64_t M, int64_t R)
+{
+    if (!dtype_ok(dtype) || M < 1 || M > SHERRY_MAX_DIM / 4 || R < 1 || R > kGradMaxRows) return 0;
+    return (size_t)digit_bytes(dtype, M, R) + 4 * (size_t)M;
+}
+
+int sherry_linear_grad(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                       const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
+                       void* work, int64_t M, int64_t N, int64_t K, void* stream)
+{
+    return backward(dy, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, M, N, N, K, false,
+                    static_cast<cudaStream_t>(stream));
+}
+
+int sherry_gated_grad(const void* dh, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                      const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
+                      void* work, int64_t M, int64_t N, int64_t K, void* stream)
+{
+    if (N > kGradMaxRows / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    return backward(dh, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, M, 2 * N, N, K, true,
+                    static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

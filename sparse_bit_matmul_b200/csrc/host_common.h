@@ -1,0 +1,69 @@
+// Host-side helpers shared by the library's CUDA translation units
+// (definitions in sherry_cuda.cu unless inline).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "sherry.h"
+
+namespace sherry {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? SHERRY_OK : SHERRY_ERR_CUDA; }
+
+struct DeviceInfo {
+    bool checked = false;
+    bool ok = false;
+    int sms = 0;
+    int max_smem_optin = 0;
+};
+
+// The current device (SHERRY_ERR_DEVICE unless it is sm_100).
+int device_info(DeviceInfo* out);
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
+// int8 rows x [M][K], ld bytes apart: boxes of 128 bytes x bn rows, 128-byte swizzle.
+int make_x_map(CUtensorMap* map, const int8_t* x, int64_t M, int64_t K, int64_t ld, int bn);
+
+// The device status word of the current device.
+unsigned* device_status_ptr();
+
+// CTAs of a tensor-core launch (see the definition).
+int64_t tc_grid(int64_t T, int64_t U, int64_t sms, int64_t Kc, int bn);
+
+// Buffers set aside by sherry_reserve on the current device
+// (SHERRY_ERR_WORKSPACE when smaller than asked for): the split-K workspace,
+// and the int8 activations with their scales.
+int get_workspace(size_t bytes, void** out);
+int get_act_buffer(size_t bytes, void** out);
+size_t act_buffer_bytes(int64_t M, int64_t K);
+
+// Launch with programmatic dependent launch: the kernel may start while the
+// previous kernel on the stream finishes; it orders itself with
+// griddepcontrol.wait before touching anything that kernel may write.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                       Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace sherry

@@ -65,7 +65,7 @@ __device__ __forceinline__ int quantise_exact(float x, float s)
 
 // The exact path for a whole group of four, out of line: rare, and it keeps
 // the division's code and registers away from the common path.
-__device__ __noinline__ uint32_t quantise4_exact(float4 v, float s)
+static __device__ __noinline__ uint32_t quantise4_exact(float4 v, float s)
 {
     const uint32_t a = (uint32_t)quantise_exact(v.x, s) & 0xFFu;
     const uint32_t b = (uint32_t)quantise_exact(v.y, s) & 0xFFu;

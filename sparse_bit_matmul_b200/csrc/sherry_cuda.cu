@@ -13,6 +13,7 @@
 
 #include "sherry.h"
 #include "sherry_internal.h"
+#include "host_common.h"
 #include "gemv.cuh"
 #include "decode.cuh"
 #include "quant.cuh"
@@ -210,16 +211,6 @@ __global__ void __launch_bounds__(SHERRY_TILE_ROWS)
 // ---------------------------------------------------------------------------
 // host helpers
 // ---------------------------------------------------------------------------
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? SHERRY_OK : SHERRY_ERR_CUDA; }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn()
 {
     static EncodeTiledFn fn = nullptr;
@@ -234,12 +225,7 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-struct DeviceInfo {
-    bool checked = false;
-    bool ok = false;
-    int sms = 0;
-    int max_smem_optin = 0;
-};
+namespace {
 
 std::mutex g_mutex;
 std::vector<DeviceInfo> g_dev;
@@ -249,6 +235,8 @@ struct Workspace {
     size_t bytes = 0;
 };
 std::vector<Workspace> g_ws;
+
+}  // namespace
 
 int device_info(DeviceInfo* out)
 {
@@ -305,8 +293,10 @@ int get_workspace(size_t bytes, void** out)
     return SHERRY_OK;
 }
 
+namespace {
+
 // Token tile of the tensor-core kernel for M tokens (the dispatch of
-// sherry_gemm_tc and sherry_w4a8_gemm_tc).
+// sherry_gemm_tc, sherry_w4a8_gemm_tc and the feed-forward entry points).
 int tc_token_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M < 1536 ? 128 : 192; }
 
 // Split-K workspace for every launch of up to M tokens on `sms` SMs: the
@@ -334,12 +324,14 @@ int make_y_map(CUtensorMap* map, const float* y, int64_t M, int64_t N, int box_m
     return r == CUDA_SUCCESS ? SHERRY_OK : SHERRY_ERR_CUDA;
 }
 
-int make_x_map(CUtensorMap* map, const int8_t* x, int64_t M, int64_t K, int bn)
+}  // namespace
+
+int make_x_map(CUtensorMap* map, const int8_t* x, int64_t M, int64_t K, int64_t ld, int bn)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return SHERRY_ERR_CUDA;
     cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M};
-    cuuint64_t strides[1] = {(cuuint64_t)K};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
     cuuint32_t box[2] = {SHERRY_KCHUNK, (cuuint32_t)bn};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(x), dims, strides, box, estr,
@@ -355,25 +347,7 @@ unsigned* device_status_ptr()
     return static_cast<unsigned*>(p);
 }
 
-// Launch with programmatic dependent launch: the kernel may start while the
-// previous kernel on the stream finishes; it orders itself with
-// griddepcontrol.wait before touching anything that kernel may write.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
+namespace {
 
 template <int BN, int SC, int WF = tc::kWeightSherry>
 int launch_tc(const int8_t* x, const float* xs, const void* wn, const float* alpha, float* y, int32_t* acc,
@@ -413,7 +387,7 @@ int launch_tc(const int8_t* x, const float* xs, const void* wn, const float* alp
     if (!p.status) return SHERRY_ERR_CUDA;
 
     CUtensorMap map, ymap;
-    st = make_x_map(&map, x, M, K, BN);
+    st = make_x_map(&map, x, M, K, K, BN);
     if (st != SHERRY_OK) return st;
     std::memset(&ymap, 0, sizeof(ymap));
     p.y_tma = (y && N % 4 == 0 && aligned16(y)) ? 1 : 0;
@@ -567,6 +541,8 @@ int launch_decode(const decode::Params& p0, cudaStream_t stream)
 // by sherry_reserve, never allocated here.
 std::vector<Workspace> g_act;
 
+}  // namespace
+
 size_t act_buffer_bytes(int64_t M, int64_t K) { return (((size_t)M * (size_t)K + 255) & ~size_t(255)) + 4 * (size_t)M; }
 
 int get_act_buffer(size_t bytes, void** out)
@@ -579,12 +555,17 @@ int get_act_buffer(size_t bytes, void** out)
     return SHERRY_OK;
 }
 
+namespace {
+
 // Grow one per-device buffer to at least `bytes` (host-synchronous; the
 // device is idle before an older, smaller buffer is freed), zero-filled.
-int grow_buffer(Workspace& w, size_t bytes)
+// keep_old: the older buffer stays allocated, since captured graphs may hold
+// its address (the split-K workspace: it grows at most four times, with the
+// token tile, and all its sizes together are 33 MB).
+int grow_buffer(Workspace& w, size_t bytes, bool keep_old)
 {
     if (w.bytes >= bytes) return SHERRY_OK;
-    if (w.ptr) {
+    if (w.ptr && !keep_old) {
         if (cudaDeviceSynchronize() != cudaSuccess) return SHERRY_ERR_CUDA;
         cudaFree(w.ptr);
         w.ptr = nullptr;
@@ -683,7 +664,7 @@ int launch_tc_noalloc(const int8_t* x, const float* xs, const void* wn, const fl
         cudaMemsetAsync(p.counters, 0, (size_t)grid * sizeof(uint32_t), stream) != cudaSuccess)
         return SHERRY_ERR_CUDA;
     CUtensorMap map, ymap;
-    st = make_x_map(&map, x, M, K, BN);
+    st = make_x_map(&map, x, M, K, K, BN);
     if (st != SHERRY_OK) return st;
     std::memset(&ymap, 0, sizeof(ymap));
     p.y_tma = (y && N % 4 == 0 && aligned16(y)) ? 1 : 0;
@@ -986,9 +967,9 @@ int sherry_reserve(int64_t max_M, int64_t max_K)
     std::lock_guard<std::mutex> lk(g_mutex);
     if ((int)g_ws.size() <= dev) g_ws.resize(dev + 1);
     if ((int)g_act.size() <= dev) g_act.resize(dev + 1);
-    st = grow_buffer(g_ws[dev], tc_workspace_bytes(max_M, di.sms));
+    st = grow_buffer(g_ws[dev], tc_workspace_bytes(max_M, di.sms), true);
     if (st != SHERRY_OK) return st;
-    return grow_buffer(g_act[dev], act_buffer_bytes(max_M, max_K));
+    return grow_buffer(g_act[dev], act_buffer_bytes(max_M, max_K), false);
 }
 
 int sherry_last_device_status(int reset)

@@ -27,6 +27,12 @@
 // the int8 values 16 w of k0..k0+3 and k0+4..k0+7, and a warp loading the
 // 16-byte pieces of 32 consecutive rows reads 512 contiguous bytes.
 #define SHERRY_W4_CHUNK_BYTES (SHERRY_TILE_ROWS * SHERRY_KCHUNK / 2)
+// Transposed ternary layout of the gradients (sherry_repack_t): one (k tile,
+// row tile) block of 128 k x 128 rows at 2 bits a weight, [piece q 0..1][k
+// 0..127][word i 0..3].  A warp loading the 16-byte pieces of 32 consecutive k
+// reads 512 contiguous bytes.
+#define SHERRY_T2_CHUNK_BYTES (SHERRY_TILE_ROWS * SHERRY_KCHUNK / 4)
+
 // Largest K of the W4A8 path: |sum of q * 16 w| <= 127 * 128 * K below 2^31.
 #define SHERRY_W4_MAX_K int64_t(132104)
 

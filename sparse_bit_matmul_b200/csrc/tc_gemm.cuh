@@ -58,11 +58,23 @@
 // byte (shift and mask, no table), the MMAs sum q * 16 w exactly in int32,
 // and the epilogue divides those sums by 16 (an exact arithmetic shift)
 // before the two fp32 products with the channel scale and the token scale.
+//
+// The feed-forward entry points (ffn_cuda.cu) run it with other epilogues
+// (EK): kEpLinear adds bias, activation and residual; kEpGated has gate and
+// up rows in adjacent TMEM lanes, exchanges them by one shuffle per two sums
+// (the even lane finishes the even token of a pair, the odd lane the odd one,
+// so no lane idles) and writes act(gate) * up; kEpGrad is the input gradient:
+// the weights are T^T at two bits each (kWeightT2, four byte selectors per
+// shift and mask, one byte permute per TMEM cell, no table), the "tokens" are
+// the int8 base-256 digits of a fixed-point gradient, D per token, and the
+// epilogue joins a token's D sums.  Its sums are as exact as the forward's,
+// so the split-K reductions stay free of order.
 #pragma once
 
 #include <cstdint>
 #include <cuda.h>
 
+#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "sherry_internal.h"
 
@@ -78,6 +90,13 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;              // 2 s per wait
 // weight formats
 constexpr int kWeightSherry = 0;     // 5-bit 3:4 ternary group codes
 constexpr int kWeightInt4 = 1;       // SINT4, two per byte
+constexpr int kWeightT2 = 2;         // transposed ternary, 2 bits each (sherry_repack_t)
+
+// epilogues
+constexpr int kEpPlain = 0;          // y = acc * alpha * x_scale, fp32
+constexpr int kEpLinear = 1;         // + bias, activation, residual; any element type
+constexpr int kEpGated = 2;          // rows 2n, 2n + 1: act(z[2n]) * z[2n + 1]
+constexpr int kEpGrad = 3;           // joins the digits of fixed-point gradients
 
 template <int BN, int SC, int WF = kWeightSherry>
 struct Cfg {
@@ -90,9 +109,11 @@ struct Cfg {
     static constexpr int kEpiWarp0 = kDecWarp0 + 4 * kDecGroups;
     static constexpr int kThreads = 32 * (kEpiWarp0 + 4);
     static_assert(SC >= 1 && SC <= 4, "SC");
-    static_assert(WF == kWeightSherry || WF == kWeightInt4, "WF");
+    static_assert(WF == kWeightSherry || WF == kWeightInt4 || WF == kWeightT2, "WF");
     // weight bytes of one (row tile, K chunk) block
-    static constexpr int kChunkWBytes = WF == kWeightSherry ? SHERRY_CHUNK_BYTES_PER_TILE : SHERRY_W4_CHUNK_BYTES;
+    static constexpr int kChunkWBytes = WF == kWeightSherry ? SHERRY_CHUNK_BYTES_PER_TILE
+                                        : WF == kWeightInt4 ? SHERRY_W4_CHUNK_BYTES
+                                                            : SHERRY_T2_CHUNK_BYTES;
     // int32 sums of q * 16 w are divided by 16 before the epilogue uses them
     static constexpr int kAccShift = WF == kWeightInt4 ? 4 : 0;
     static constexpr int kBChunkBytes = BN * 128;
@@ -162,6 +183,98 @@ struct Params {
     int64_t U;                  // total units TM*TN*Kc
     int y_tma;                  // y rows 16-byte multiples: complete tiles leave through TMA stores
 };
+
+// Parameters of the epilogues other than kEpPlain.  kEpGrad: M counts digit
+// rows (D per token), N is the output's row length, x_scale one per token.
+struct EpParams : Params {
+    const float* bias;          // [N] or null
+    const void* res;            // [Mo][No] or null (kEpLinear)
+    void* out;                  // [Mo][No]
+    int64_t Mo, No;             // output rows (tokens) and row length
+    int dtype;                  // sherry_dtype of out and res
+    int act;                    // sherry_act
+};
+
+template <int EK>
+struct ParamsOf {
+    using type = EpParams;
+};
+template <>
+struct ParamsOf<kEpPlain> {
+    using type = Params;
+};
+
+// S sums of one weight row (32 lanes: 32 rows), of S consecutive tokens or
+// digit rows with the scales sc, into output values: kEpLinear o[i] of token
+// i, kEpGated o[i] of token 2 i + (lane & 1) and the lane's row pair, kEpGrad
+// o[i] of token i (digit rows D i .. D i + D - 1, lowest digit first).
+// All 32 lanes call it.
+template <int EK, int D, int S, int O>
+__device__ __forceinline__ void ep_values(const EpParams& p, const uint32_t (&v)[S], const float* sc, float al,
+                                          float bi, int lane, float (&o)[O])
+{
+    if constexpr (EK == kEpGrad) {
+        static_assert(O * D == S, "digits");
+#pragma unroll
+        for (int i = 0; i < O; ++i) {
+            // every step rounds relative to the joined value
+            float f = (float)(int32_t)v[i * D + D - 1];
+#pragma unroll
+            for (int d = D - 2; d >= 0; --d) f = __fmaf_rn(f, 256.0f, (float)(int32_t)v[i * D + d]);
+            o[i] = __fmul_rn(f, sc[i]);
+        }
+    } else if constexpr (EK == kEpLinear) {
+        static_assert(O == S, "one value per sum");
+#pragma unroll
+        for (int i = 0; i < O; ++i) o[i] = __fmul_rn(__fmul_rn((float)(int32_t)v[i], al), sc[i]);
+        if (p.bias) {
+#pragma unroll
+            for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], bi);
+        }
+        ep::apply_act<O>(o, p.act);
+    } else {
+        static_assert(2 * O == S, "one value per pair of sums");
+        const bool odd = lane & 1;
+        float up[O];
+#pragma unroll
+        for (int i = 0; i < O; ++i) {
+            float z0 = __fmul_rn(__fmul_rn((float)(int32_t)v[2 * i], al), sc[2 * i]);
+            float z1 = __fmul_rn(__fmul_rn((float)(int32_t)v[2 * i + 1], al), sc[2 * i + 1]);
+            if (p.bias) {
+                z0 = __fadd_rn(z0, bi);
+                z1 = __fadd_rn(z1, bi);
+            }
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
+            o[i] = odd ? got : z0;
+            up[i] = odd ? z1 : got;
+        }
+        ep::apply_act<O>(o, p.act);
+#pragma unroll
+        for (int i = 0; i < O; ++i) o[i] = __fmul_rn(o[i], up[i]);
+    }
+}
+
+// ep_values of 16 sums, stored element by element: output rows from m0 on,
+// column col (out of range: not stored).
+template <int EK, int D>
+__device__ __forceinline__ void ep_store16(const EpParams& p, const uint32_t (&v)[16], const float* sc, float al,
+                                           float bi, int lane, int64_t m0, int64_t col)
+{
+    constexpr int O = EK == kEpGated ? 8 : 16 / D;
+    float o[O];
+    ep_values<EK, D, 16, O>(p, v, sc, al, bi, lane, o);
+    if (col >= p.No) return;
+#pragma unroll
+    for (int i = 0; i < O; ++i) {
+        const int64_t m = m0 + (EK == kEpGated ? 2 * i + (lane & 1) : i);
+        if (m >= p.Mo) continue;
+        float y = o[i];
+        if constexpr (EK == kEpLinear) {
+            if (p.res) y = __fadd_rn(y, ep::load_elem(p.res, m * p.No + col, p.dtype));
+        }
+        ep::store_elem(p.out, m * p.No + col, y, p.dtype);
+    }
+}
 
 // The work of one CTA as a sequence of tile segments (a segment = chunks
 // [cb, ce) of one tile; units are numbered tile-major, unit = tile * Kc +
@@ -266,12 +379,13 @@ __device__ __forceinline__ void report(unsigned* status, volatile int* abort_fla
     *abort_flag = 1;
 }
 
-template <int BN, int SC, int WF = kWeightSherry>
+template <int BN, int SC, int WF = kWeightSherry, int EK = kEpPlain, int D = 1>
 __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
     sherry_gemm_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
-                          const Params p)
+                          const typename ParamsOf<EK>::type p)
 {
     using C = Cfg<BN, SC, WF>;
+    static_assert(EK == kEpGrad ? 16 % D == 0 : D == 1, "digits per token");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(128) uint32_t table[32];
     // 1024-byte aligned start, computed by pointer arithmetic so that the
@@ -583,6 +697,39 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(afull_bar(a));
+                } else if constexpr (WF == kWeightT2) {
+                    // four 2-bit weights -> four int8 by one byte permute
+                    ok = ptx::mbar_wait_bounded(aempty_bar(a), aph ^ 1u, kWaitLimitNs);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) report(p.status, abort_flag, SHERRY_DEV_TIMEOUT_DECODER);
+                        quit = true;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t wrow = codes_s + (uint32_t)(16 * row);
+#pragma unroll
+                    for (int j = 0; j < SC; ++j) {
+                        if (j >= nch) break;
+                        uint32_t a_vals[32];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t v[4];
+                            ptx::lds_v4_u32(wrow + (uint32_t)(j * C::kChunkWBytes + q * SHERRY_TILE_ROWS * 16), v);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    a_vals[16 * q + 4 * i + c] = __byte_perm(
+                                        0x00FF0100u, 0u, (v[i] >> (2 * (c & 1) + 16 * (c >> 1))) & 0x3333u);
+                        }
+                        ptx::tmem_st_32x32b_x32(lane_base + (uint32_t)(C::kACol0 + a * C::kACols + 32 * j), a_vals);
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(empty_bar(s));
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(afull_bar(a));
                 } else {
                 uint32_t w[SC][SHERRY_CHUNK_WORDS];
 #pragma unroll
@@ -646,11 +793,17 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             // the MMAs: fetch them into shared memory (double-buffered by
             // segment) before waiting for the accumulators
             float* sc_s = reinterpret_cast<float*>(smem + C::kOffMisc + 64) + (seg & 1) * BN;
-            for (int i = etid; i < BN; i += 128) {
-                const int64_t m = tm * BN + i;
-                sc_s[i] = (m < p.M) ? __ldg(p.x_scale + m) : 0.0f;
+            int64_t Mo = p.M;                          // scales: one per token
+            if constexpr (EK != kEpPlain) Mo = p.Mo;
+            for (int i = etid; i < BN / D; i += 128) {
+                const int64_t m = tm * (BN / D) + i;
+                sc_s[i] = (m < Mo) ? __ldg(p.x_scale + m) : 0.0f;
             }
-            const float al = (n < p.N) ? __ldg(p.alpha + n) : 0.0f;
+            float al = 0.0f, bi = 0.0f;
+            if constexpr (EK != kEpGrad) al = (n < p.N) ? __ldg(p.alpha + n) : 0.0f;
+            if constexpr (EK == kEpLinear || EK == kEpGated) bi = (p.bias && n < p.N) ? __ldg(p.bias + n) : 0.0f;
+            // output column of this lane's row
+            const int64_t col = EK == kEpGated ? n >> 1 : n;
             // every epilogue thread waits; the AND over the 128 of them makes
             // the leave-or-stay decision uniform
             bool ok = !*abort_flag && ptx::mbar_wait_bounded(dfull_bar(d), dph, kWaitLimitNs);
@@ -668,8 +821,76 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                 nparts = bl - bf + 1;
             }
             int32_t* wsl = p.ws + slot * (int64_t)BN * SHERRY_TILE_ROWS;
-            const bool via_tma = complete && p.y_tma && p.y && !p.acc;
-            if (via_tma) {
+            bool via_tma = complete && p.y_tma;
+            if constexpr (EK == kEpPlain) via_tma = via_tma && p.y && !p.acc;
+            if constexpr (EK != kEpPlain) {
+                if (via_tma) {
+                    // as below, for SL sums of the lane's row at a time: OT
+                    // output tokens x OW columns per slice
+                    constexpr int SL = C::kSlice;
+                    constexpr int OW = EK == kEpGated ? 16 : 32;
+                    constexpr int OT = SL / D;
+                    constexpr int O = EK == kEpGated ? SL / 2 : OT;
+                    float* stg_w = reinterpret_cast<float*>(smem + C::kOffStaging) + quad * (2 * SL * 32);
+                    const int scol = EK == kEpGated ? lane >> 1 : lane;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < BN; j0 += SL) {
+                        const int64_t m0 = (tm * BN + j0) / D;
+                        if (m0 >= p.Mo) break;
+                        uint32_t v[SL];
+                        if constexpr (SL == 32) ptx::tmem_ld_32x32b_x32(lane_base + (uint32_t)(d * BN + j0), v);
+                        else ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
+                        float rs[EK == kEpLinear ? O : 1];
+                        if constexpr (EK == kEpLinear) {
+                            if (p.res) {
+#pragma unroll
+                                for (int i = 0; i < O; ++i)
+                                    rs[i] = (m0 + i < p.Mo && col < p.No)
+                                                ? ep::load_elem(p.res, (m0 + i) * p.No + col, p.dtype)
+                                                : 0.0f;
+                            }
+                        }
+                        if (lane == 0) ptx::bulk_wait_group_read<1>();
+                        __syncwarp();
+                        ptx::tmem_wait_ld();
+                        if constexpr (EK != kEpGrad) {
+                            if (p.acc && n < p.N) {
+#pragma unroll
+                                for (int i = 0; i < SL; ++i)
+                                    if (m0 + i < p.M) p.acc[(m0 + i) * p.N + n] = (int32_t)v[i];
+                            }
+                        }
+                        float o[O];
+                        ep_values<EK, D, SL, O>(p, v, sc_s + j0 / D, al, bi, lane, o);
+                        if constexpr (EK == kEpLinear) {
+                            if (p.res) {
+#pragma unroll
+                                for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], rs[i]);
+                            }
+                        }
+                        float* stg = stg_w + (stage_slice & 1) * (SL * 32);
+                        if (p.dtype == SHERRY_F32) {
+#pragma unroll
+                            for (int i = 0; i < O; ++i)
+                                stg[(EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol] = o[i];
+                        } else {
+                            uint16_t* st16 = reinterpret_cast<uint16_t*>(stg);
+#pragma unroll
+                            for (int i = 0; i < O; ++i)
+                                st16[(EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol] = ep::to16(o[i], p.dtype);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_2d(&ymap,
+                                              (int32_t)((tn * SHERRY_TILE_ROWS + quad * 32) / (EK == kEpGated ? 2 : 1)),
+                                              (int32_t)m0, ptx::smem_u32(stg));
+                            ptx::bulk_commit_group();
+                        }
+                        ++stage_slice;
+                    }
+                }
+            } else if (via_tma) {
                 // Each warp stores its own 32 rows x kSlice tokens through TMA
                 // from its own double-buffered staging, with its own bulk
                 // groups: no barrier across the epilogue warps per slice.
@@ -706,6 +927,9 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                 uint32_t v[16];
                 ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
                 ptx::tmem_wait_ld();
+                if constexpr (EK != kEpPlain) {
+                    if (complete) ep_store16<EK, D>(p, v, sc_s + j0 / D, al, bi, lane, (tm * BN + j0) / D, col);
+                }
 #pragma unroll
                 for (int jj = 0; jj < 16; ++jj) {
                     const int64_t m = tm * BN + j0 + jj;
@@ -713,9 +937,11 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                     const int32_t a32 = (int32_t)v[jj];      // a partial sum goes to the slot as is
                     if (complete) {
                         const int32_t af = a32 >> C::kAccShift;
-                        if (n < p.N) {
+                        if (EK != kEpGrad && n < p.N) {
                             if (p.acc) p.acc[m * p.N + n] = af;
-                            if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j0 + jj]);
+                            if constexpr (EK == kEpPlain) {
+                                if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j0 + jj]);
+                            }
                         }
                     } else {
                         ptx::red_add_s32(wsl + (j0 + jj) * SHERRY_TILE_ROWS + r, a32);
@@ -748,6 +974,12 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
 #pragma unroll
                         for (int jj = 0; jj < 16; ++jj)
                             v[jj] = (j0 + jj < jn) ? __ldcg(wsl + (j0 + jj) * SHERRY_TILE_ROWS + r) : 0;
+                        if constexpr (EK != kEpPlain) {
+                            uint32_t u[16];
+#pragma unroll
+                            for (int jj = 0; jj < 16; ++jj) u[jj] = (uint32_t)v[jj];
+                            ep_store16<EK, D>(p, u, sc_s + j0 / D, al, bi, lane, (cur_tm * BN + j0) / D, col);
+                        }
 #pragma unroll
                         for (int jj = 0; jj < 16; ++jj) {
                             const int j = j0 + jj;
@@ -755,9 +987,11 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                             const int64_t m = cur_tm * BN + j;
                             wsl[j * SHERRY_TILE_ROWS + r] = 0;
                             const int32_t af = v[jj] >> C::kAccShift;
-                            if (n < p.N) {
+                            if (EK != kEpGrad && n < p.N) {
                                 if (p.acc) p.acc[m * p.N + n] = af;
-                                if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j]);
+                                if constexpr (EK == kEpPlain) {
+                                    if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j]);
+                                }
                             }
                         }
                     }
