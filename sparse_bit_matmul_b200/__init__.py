@@ -292,7 +292,7 @@ def selftest_wait(limit_ns: int, stream=None):
 
 
 # --------------------------------------------------- feed-forward operators
-ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}   # sherry_act
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}   # sherry_act
 _DTYPES = {}            # torch dtype -> sherry_dtype, filled on first use
 _split_reserved = set()  # devices whose split-K workspace covers every call
 SPLIT_MAX_M = 1536      # from this many tokens on the split-K workspace no longer grows
@@ -311,25 +311,27 @@ def _need(ok: bool, what: str):
 
 
 def _check_tensor(t, name: str, dtype, shape, device):
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: want contiguous {dtype} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}, strides {tuple(t.stride())}")
     return t.data_ptr()
 
 
-def _activation(act: str) -> int:
-    a = ACTIVATIONS.get("none" if act is None else act)
+def _activation(act) -> int:
+    a = ACTIVATIONS.get(act)
     if a is None:
-        raise ValueError(f"act: want one of {sorted(ACTIVATIONS)}, got {act!r}")
+        raise ValueError(f"act: want one of {list(ACTIVATIONS)[1:]}, got {act!r}")
     return a
 
 
 def _matrix(t, name: str, types):
     """Shape and sherry_dtype of a [M][.] tensor of a feed-forward call."""
-    _need(t.dim() == 2 and t.is_cuda and t.is_contiguous() and t.dtype in types,
-          f"{name}: want a contiguous 2-D CUDA tensor of float32, bfloat16 or float16, got {t.dtype} "
-          f"{tuple(t.shape)} on {t.device}, strides {tuple(t.stride())}")
-    return t.shape[0], t.shape[1], types[t.dtype]
+    code = types.get(t.dtype)
+    shape = t.shape
+    if code is None or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous 2-D CUDA tensor of float32, bfloat16 or float16, got {t.dtype} "
+                         f"{tuple(shape)} on {t.device}, strides {tuple(t.stride())}")
+    return shape[0], shape[1], code
 
 
 def _on_device(fn):
@@ -412,7 +414,8 @@ def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q,
     a = _activation(act)
     R = 2 * N if gated else N
     dev = x.device
-    _need(N > 0 and K > 0 and K % 32 == 0, f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
+    if N <= 0 or K <= 0 or K % 32:
+        raise ValueError(f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
     wp = _check_tensor(w_native, "w_native", torch.uint8, (-(-R // 128) * -(-K // 128) * 2560,), dev)
     ap = _check_tensor(alpha, "alpha", torch.float32, (R,), dev)
     bp = None if bias is None else _check_tensor(bias, "bias", torch.float32, (R,), dev)
@@ -475,7 +478,8 @@ def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, w
     a = _activation(act)
     R = 2 * N if gated else N
     dev = dy.device
-    _need(N > 0 and K > 0 and K % 32 == 0, f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
+    if N <= 0 or K <= 0 or K % 32:
+        raise ValueError(f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
     _need(want_dx or want_scales, "nothing to compute")
     need_acc = gated or a != 0 or want_scales
     _need(acc is not None or not need_acc, "acc: needed for this gradient")

@@ -8,10 +8,12 @@
 //   t(z) = 2 sqrt(2/pi) (z + 0.044715 z^3), S the logistic function
 //   (z/2 (1 + tanh(t/2)) = z S(t)).
 // silu and gelu_tanh share one body.
-// S(t) = 1 / (1 + e^-t) with the hardware exponential: e^-t overflows to
-// infinity for t < -88, where S is 0 to fp32 either way, and its relative
-// error (a few 2^-24 for |t| up to 10) reaches the result scaled by
-// 1 - S(t), so the larger half of the values hardly sees it.
+// S(t) = 1 / (1 + e^-t) with the hardware's approximate power of two and
+// reciprocal (two special-function instructions a value: the epilogue has one
+// warp per scheduler).  e^-t overflows to infinity for t < -88, where S is 0
+// to fp32 either way; its relative error (2 ulp and the rounding of t log2 e)
+// reaches the result scaled by 1 - S(t), so the larger half of the values
+// hardly sees it.
 #pragma once
 
 #include <cstdint>
@@ -53,7 +55,13 @@ constexpr float kGeluC3 = 0.0713548162726009f;       // 2 sqrt(2 / pi) 0.044715
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
-__device__ __forceinline__ float logistic(float t) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-t))); }
+__device__ __forceinline__ float logistic(float t)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(t, -1.4426950408889634f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+    return r;
+}
 
 // t(z) of silu and gelu_tanh (silu apart: z^2 may overflow)
 __device__ __forceinline__ float sigmoid_arg(float z, bool silu)

@@ -236,8 +236,13 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, cudaStream_t stream)
     if (st != SHERRY_OK) return st;
     std::memset(&omap, 0, sizeof(omap));
     p.y_tma = (p.No * ep::elem_size(p.dtype)) % 16 == 0 && aligned16(p.out);
-    if (p.y_tma && make_out_map(&omap, p.out, p.dtype, p.Mo, p.No, EK == tc::kEpGated ? 16 : 32, C::kSlice / D) != SHERRY_OK)
-        p.y_tma = 0;
+    if (p.res) p.y_tma = p.y_tma && aligned16(p.res);
+    if (p.y_tma) {
+        st = make_out_map(&omap, p.out, p.dtype, p.Mo, p.No, EK == tc::kEpGated ? 16 : 32, 16 / D);
+        if (st == SHERRY_OK && p.res)
+            st = make_out_map(&p.rmap, const_cast<void*>(p.res), p.dtype, p.Mo, p.No, 32, 16);
+        if (st != SHERRY_OK) return st;
+    }
 
     const int smem = std::max(C::kSmemBytes, 120 * 1024);    // one CTA per SM
     if (smem > di.max_smem_optin) return SHERRY_ERR_DEVICE;

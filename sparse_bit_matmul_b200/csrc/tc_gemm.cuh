@@ -159,6 +159,9 @@ struct Cfg {
     static constexpr int kSlice = BN < 32 ? BN : 32;
     static constexpr int kOffStaging = (kOffMisc + kMiscBytes + 127) & ~127;
     static constexpr int kStagingBytes = 4 * 2 * kSlice * 32 * 4;
+    // the other epilogues cut a warp's staging into slots of 16 sums x 32
+    // rows: two at BN = 16 (one slice a tile), else four
+    static constexpr int kEpSlots = kStagingBytes / (4 * 16 * 32 * 4);
     static constexpr int kSmemBytes = kOffStaging + kStagingBytes + 1024;   // + alignment slack
     // dynamic plus static (the table of the code path, 1 KB as compiled)
     // within the 227 KB per-block limit
@@ -187,6 +190,7 @@ struct Params {
 // Parameters of the epilogues other than kEpPlain.  kEpGrad: M counts digit
 // rows (D per token), N is the output's row length, x_scale one per token.
 struct EpParams : Params {
+    CUtensorMap rmap;           // residual boxes of 32 columns x 16 tokens (kEpLinear, with y_tma and res)
     const float* bias;          // [N] or null
     const void* res;            // [Mo][No] or null (kEpLinear)
     void* out;                  // [Mo][No]
@@ -254,25 +258,68 @@ __device__ __forceinline__ void ep_values(const EpParams& p, const uint32_t (&v)
     }
 }
 
+// v[i] to base + i * stride bytes for i < cnt: one running address, no
+// per-element products.
+template <int O, class T>
+__device__ __forceinline__ void store_strided(char* base, int64_t stride, int cnt, const T (&v)[O])
+{
+#pragma unroll
+    for (int i = 0; i < O; ++i) {
+        if (i < cnt) *reinterpret_cast<T*>(base) = v[i];
+        base += stride;
+    }
+}
+
+// The kept sums of 16 tokens from m0 on, row n.
+__device__ __forceinline__ void ep_keep16(const EpParams& p, const uint32_t (&v)[16], int64_t m0, int64_t n)
+{
+    if (!p.acc) return;
+    const int64_t left = n < p.N ? p.M - m0 : 0;
+    store_strided<16, uint32_t>(reinterpret_cast<char*>(p.acc + m0 * p.N + n), 4 * p.N, (int)(left < 16 ? left : 16), v);
+}
+
 // ep_values of 16 sums, stored element by element: output rows from m0 on,
-// column col (out of range: not stored).
+// column col (out of range: not stored).  The residual is loaded whole before
+// the first store (it may be the output itself, so a load could not pass a
+// store on its own).
 template <int EK, int D>
 __device__ __forceinline__ void ep_store16(const EpParams& p, const uint32_t (&v)[16], const float* sc, float al,
                                            float bi, int lane, int64_t m0, int64_t col)
 {
     constexpr int O = EK == kEpGated ? 8 : 16 / D;
+    constexpr int kStep = EK == kEpGated ? 2 : 1;            // output rows between values
+    const int first = EK == kEpGated ? lane & 1 : 0;
+    const int64_t left = (p.Mo - m0 - first + kStep - 1) / kStep;
+    const int cnt = col >= p.No ? 0 : left < O ? (int)left : O;
+    const int es = ep::elem_size(p.dtype);
+    const int64_t at = ((m0 + first) * p.No + col) * es, stride = (int64_t)kStep * p.No * es;
+    float rs[EK == kEpLinear ? O : 1];
+    if constexpr (EK == kEpLinear) {
+        if (p.res) {
+            const char* r = static_cast<const char*>(p.res) + at;
+#pragma unroll
+            for (int i = 0; i < O; ++i) {
+                rs[i] = i < cnt ? ep::load_elem(r, 0, p.dtype) : 0.0f;
+                r += stride;
+            }
+        }
+    }
     float o[O];
     ep_values<EK, D, 16, O>(p, v, sc, al, bi, lane, o);
-    if (col >= p.No) return;
+    if constexpr (EK == kEpLinear) {
+        if (p.res) {
 #pragma unroll
-    for (int i = 0; i < O; ++i) {
-        const int64_t m = m0 + (EK == kEpGated ? 2 * i + (lane & 1) : i);
-        if (m >= p.Mo) continue;
-        float y = o[i];
-        if constexpr (EK == kEpLinear) {
-            if (p.res) y = __fadd_rn(y, ep::load_elem(p.res, m * p.No + col, p.dtype));
+            for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], rs[i]);
         }
-        ep::store_elem(p.out, m * p.No + col, y, p.dtype);
+    }
+    char* base = static_cast<char*>(p.out) + at;
+    if (p.dtype == SHERRY_F32) {
+        store_strided<O, float>(base, stride, cnt, o);
+    } else {
+        uint16_t h[O];
+#pragma unroll
+        for (int i = 0; i < O; ++i) h[i] = ep::to16(o[i], p.dtype);
+        store_strided<O, uint16_t>(base, stride, cnt, h);
     }
 }
 
@@ -382,10 +429,13 @@ __device__ __forceinline__ void report(unsigned* status, volatile int* abort_fla
 template <int BN, int SC, int WF = kWeightSherry, int EK = kEpPlain, int D = 1>
 __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
     sherry_gemm_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
-                          const typename ParamsOf<EK>::type p)
+                          const __grid_constant__ typename ParamsOf<EK>::type p)
 {
     using C = Cfg<BN, SC, WF>;
     static_assert(EK == kEpGrad ? 16 % D == 0 : D == 1, "digits per token");
+    // kEpLinear: a barrier per staging slot of each epilogue warp, for the
+    // residual boxes loaded into it
+    __shared__ __align__(8) uint64_t res_bars[EK == kEpLinear ? 4 * C::kEpSlots : 1];
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(128) uint32_t table[32];
     // 1024-byte aligned start, computed by pointer arithmetic so that the
@@ -442,6 +492,8 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             ptx::mbar_init(dempty_bar(d), 4);
         }
         ptx::mbar_init(drain_bar, 1);
+        if constexpr (EK == kEpLinear)
+            for (int i = 0; i < 4 * C::kEpSlots; ++i) ptx::mbar_init(ptx::smem_u32(&res_bars[i]), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -783,6 +835,12 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
         int d = 0;
         uint32_t dph = 0;
         uint32_t stage_slice = 0;                  // output slices staged so far
+        [[maybe_unused]] uint32_t res_phase = 0;   // parity of each slot's residual barrier
+        [[maybe_unused]] bool res_ok = true;
+        [[maybe_unused]] const uint32_t res_bar0 =
+            ptx::smem_u32(&res_bars[EK == kEpLinear ? quad * C::kEpSlots : 0]);
+        [[maybe_unused]] float* const stg_w =
+            reinterpret_cast<float*>(smem + C::kOffStaging) + quad * (C::kEpSlots * 16 * 32);
         SegWalk w(p, blockIdx.x, G);
         for (; !w.done(); w.next()) {
             const int64_t tile = w.tile;
@@ -804,12 +862,50 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             if constexpr (EK == kEpLinear || EK == kEpGated) bi = (p.bias && n < p.N) ? __ldg(p.bias + n) : 0.0f;
             // output column of this lane's row
             const int64_t col = EK == kEpGated ? n >> 1 : n;
+            bool via_tma = complete && p.y_tma;
+            if constexpr (EK == kEpPlain) via_tma = via_tma && p.y && !p.acc;
+            // slices of 16 sums that hold tokens, and the residual's first boxes
+            const int64_t rows_left = p.M - tm * BN;
+            [[maybe_unused]] const int nslices = (int)((rows_left < BN ? rows_left : BN) + 15) >> 4;
+            [[maybe_unused]] const int32_t out_x =
+                (int32_t)((tn * SHERRY_TILE_ROWS + quad * 32) / (EK == kEpGated ? 2 : 1));
+            [[maybe_unused]] auto load_res = [&](int q, uint32_t slot) {
+                if constexpr (EK == kEpLinear) {
+                    const uint32_t bar = res_bar0 + 8u * slot;
+                    ptx::mbar_arrive_expect_tx(bar, (uint32_t)(16 * 32 * ep::elem_size(p.dtype)));
+                    ptx::tma_load_2d(ptx::smem_u32(stg_w + slot * (16 * 32)), &p.rmap, out_x, (int32_t)(tm * BN + 16 * q),
+                                     bar);
+                }
+            };
+            [[maybe_unused]] bool has_res = false;
+            [[maybe_unused]] int res_upto = 0;         // slices whose residual box was issued
+            if constexpr (EK == kEpLinear) {
+                has_res = via_tma && p.res;
+                has_res = has_res && res_ok;
+                if (has_res) {
+                    res_upto = nslices < C::kEpSlots - 1 ? nslices : C::kEpSlots - 1;
+                    if (lane == 0) {
+                        ptx::bulk_wait_group_read<0>();
+                        for (int q = 0; q < res_upto; ++q) load_res(q, (stage_slice + q) % C::kEpSlots);
+                    }
+                    __syncwarp();
+                }
+            }
             // every epilogue thread waits; the AND over the 128 of them makes
             // the leave-or-stay decision uniform
             bool ok = !*abort_flag && ptx::mbar_wait_bounded(dfull_bar(d), dph, kWaitLimitNs);
             ok = ptx::named_bar_and(1, 128, ok);
             if (!ok) {
                 if (etid == 0) report(p.status, abort_flag, SHERRY_DEV_TIMEOUT_EPILOGUE);
+                if constexpr (EK == kEpLinear) {
+                    // the residual boxes in flight land before the CTA may exit
+                    if (has_res)
+                        for (int q = 0; q < res_upto; ++q) {
+                            const uint32_t slot = (stage_slice + q) % C::kEpSlots;
+                            if (!ptx::mbar_wait_bounded(res_bar0 + 8u * slot, (res_phase >> slot) & 1u, kWaitLimitNs))
+                                atomicCAS(p.status, 0u, (unsigned)SHERRY_DEV_TIMEOUT_DRAIN);
+                        }
+                }
                 break;
             }
             ptx::tc_fence_after();
@@ -821,71 +917,77 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                 nparts = bl - bf + 1;
             }
             int32_t* wsl = p.ws + slot * (int64_t)BN * SHERRY_TILE_ROWS;
-            bool via_tma = complete && p.y_tma;
-            if constexpr (EK == kEpPlain) via_tma = via_tma && p.y && !p.acc;
             if constexpr (EK != kEpPlain) {
                 if (via_tma) {
-                    // as below, for SL sums of the lane's row at a time: OT
-                    // output tokens x OW columns per slice
-                    constexpr int SL = C::kSlice;
+                    // As below, for 16 sums of the lane's row at a time: OT
+                    // output tokens x OW columns per slice, kEpSlots staging
+                    // slots per warp.  A residual box is loaded by TMA into
+                    // the slot its outputs will take, up to kEpSlots - 1
+                    // slices ahead (the first ones before the accumulators are
+                    // complete), and replaced in place.
                     constexpr int OW = EK == kEpGated ? 16 : 32;
-                    constexpr int OT = SL / D;
-                    constexpr int O = EK == kEpGated ? SL / 2 : OT;
-                    float* stg_w = reinterpret_cast<float*>(smem + C::kOffStaging) + quad * (2 * SL * 32);
+                    constexpr int OT = 16 / D;
+                    constexpr int O = EK == kEpGated ? 8 : OT;
                     const int scol = EK == kEpGated ? lane >> 1 : lane;
 #pragma unroll 1
-                    for (int j0 = 0; j0 < BN; j0 += SL) {
+                    for (int q = 0; q < nslices; ++q) {
+                        const int j0 = 16 * q;
                         const int64_t m0 = (tm * BN + j0) / D;
-                        if (m0 >= p.Mo) break;
-                        uint32_t v[SL];
-                        if constexpr (SL == 32) ptx::tmem_ld_32x32b_x32(lane_base + (uint32_t)(d * BN + j0), v);
-                        else ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
-                        float rs[EK == kEpLinear ? O : 1];
-                        if constexpr (EK == kEpLinear) {
-                            if (p.res) {
-#pragma unroll
-                                for (int i = 0; i < O; ++i)
-                                    rs[i] = (m0 + i < p.Mo && col < p.No)
-                                                ? ep::load_elem(p.res, (m0 + i) * p.No + col, p.dtype)
-                                                : 0.0f;
+                        uint32_t v[16];
+                        ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
+                        const uint32_t slot = stage_slice % C::kEpSlots;
+                        float* stg = stg_w + slot * (16 * 32);
+                        uint16_t* st16 = reinterpret_cast<uint16_t*>(stg);
+                        if (has_res) {
+                            if constexpr (EK == kEpLinear) {
+                                // every box issued is waited for; after a wait
+                                // ran out no further one is issued
+                                if (q < res_upto) {
+                                    const bool in = ptx::mbar_wait_bounded(res_bar0 + 8u * slot,
+                                                                           (res_phase >> slot) & 1u, kWaitLimitNs);
+                                    if (!__all_sync(0xffffffffu, in)) {
+                                        res_ok = false;
+                                        if (lane == 0) report(p.status, abort_flag, SHERRY_DEV_TIMEOUT_EPILOGUE);
+                                    }
+                                    res_phase ^= 1u << slot;
+                                }
                             }
+                        } else {
+                            // the slot's earlier store has read it
+                            if (lane == 0) ptx::bulk_wait_group_read<C::kEpSlots - 1>();
+                            __syncwarp();
                         }
-                        if (lane == 0) ptx::bulk_wait_group_read<1>();
-                        __syncwarp();
                         ptx::tmem_wait_ld();
-                        if constexpr (EK != kEpGrad) {
-                            if (p.acc && n < p.N) {
-#pragma unroll
-                                for (int i = 0; i < SL; ++i)
-                                    if (m0 + i < p.M) p.acc[(m0 + i) * p.N + n] = (int32_t)v[i];
-                            }
-                        }
+                        if constexpr (EK != kEpGrad) ep_keep16(p, v, m0, n);
                         float o[O];
-                        ep_values<EK, D, SL, O>(p, v, sc_s + j0 / D, al, bi, lane, o);
-                        if constexpr (EK == kEpLinear) {
-                            if (p.res) {
-#pragma unroll
-                                for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], rs[i]);
-                            }
-                        }
-                        float* stg = stg_w + (stage_slice & 1) * (SL * 32);
+                        ep_values<EK, D, 16, O>(p, v, sc_s + j0 / D, al, bi, lane, o);
                         if (p.dtype == SHERRY_F32) {
 #pragma unroll
-                            for (int i = 0; i < O; ++i)
-                                stg[(EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol] = o[i];
+                            for (int i = 0; i < O; ++i) {
+                                float* at = stg + (EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol;
+                                *at = has_res ? __fadd_rn(o[i], *at) : o[i];
+                            }
                         } else {
-                            uint16_t* st16 = reinterpret_cast<uint16_t*>(stg);
 #pragma unroll
-                            for (int i = 0; i < O; ++i)
-                                st16[(EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol] = ep::to16(o[i], p.dtype);
+                            for (int i = 0; i < O; ++i) {
+                                uint16_t* at = st16 + (EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol;
+                                *at = ep::to16(has_res ? __fadd_rn(o[i], ep::from16(*at, p.dtype)) : o[i], p.dtype);
+                            }
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            ptx::tma_store_2d(&ymap,
-                                              (int32_t)((tn * SHERRY_TILE_ROWS + quad * 32) / (EK == kEpGated ? 2 : 1)),
-                                              (int32_t)m0, ptx::smem_u32(stg));
+                            ptx::tma_store_2d(&ymap, out_x, (int32_t)m0, ptx::smem_u32(stg));
                             ptx::bulk_commit_group();
+                        }
+                        if constexpr (EK == kEpLinear) {
+                            if (has_res && res_ok && res_upto < nslices) {
+                                if (lane == 0) {
+                                    ptx::bulk_wait_group_read<1>();      // the store of slice q - 1, the slot's last
+                                    load_res(res_upto, (stage_slice + C::kEpSlots - 1) % C::kEpSlots);
+                                }
+                                ++res_upto;
+                            }
                         }
                         ++stage_slice;
                     }
@@ -928,7 +1030,12 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                 ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
                 ptx::tmem_wait_ld();
                 if constexpr (EK != kEpPlain) {
-                    if (complete) ep_store16<EK, D>(p, v, sc_s + j0 / D, al, bi, lane, (tm * BN + j0) / D, col);
+                    if (complete) {
+                        if ((tm * BN + j0) / D >= p.Mo) break;
+                        if constexpr (EK != kEpGrad) ep_keep16(p, v, tm * BN + j0, n);
+                        ep_store16<EK, D>(p, v, sc_s + j0 / D, al, bi, lane, (tm * BN + j0) / D, col);
+                        continue;
+                    }
                 }
 #pragma unroll
                 for (int jj = 0; jj < 16; ++jj) {
@@ -937,11 +1044,9 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                     const int32_t a32 = (int32_t)v[jj];      // a partial sum goes to the slot as is
                     if (complete) {
                         const int32_t af = a32 >> C::kAccShift;
-                        if (EK != kEpGrad && n < p.N) {
+                        if (n < p.N) {
                             if (p.acc) p.acc[m * p.N + n] = af;
-                            if constexpr (EK == kEpPlain) {
-                                if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j0 + jj]);
-                            }
+                            if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j0 + jj]);
                         }
                     } else {
                         ptx::red_add_s32(wsl + (j0 + jj) * SHERRY_TILE_ROWS + r, a32);
@@ -978,6 +1083,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                             uint32_t u[16];
 #pragma unroll
                             for (int jj = 0; jj < 16; ++jj) u[jj] = (uint32_t)v[jj];
+                            if constexpr (EK != kEpGrad) ep_keep16(p, u, cur_tm * BN + j0, n);
                             ep_store16<EK, D>(p, u, sc_s + j0 / D, al, bi, lane, (cur_tm * BN + j0) / D, col);
                         }
 #pragma unroll
@@ -987,9 +1093,9 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                             const int64_t m = cur_tm * BN + j;
                             wsl[j * SHERRY_TILE_ROWS + r] = 0;
                             const int32_t af = v[jj] >> C::kAccShift;
-                            if (EK != kEpGrad && n < p.N) {
-                                if (p.acc) p.acc[m * p.N + n] = af;
-                                if constexpr (EK == kEpPlain) {
+                            if constexpr (EK == kEpPlain) {
+                                if (n < p.N) {
+                                    if (p.acc) p.acc[m * p.N + n] = af;
                                     if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j]);
                                 }
                             }
