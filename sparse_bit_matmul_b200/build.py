@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libsherry_b200.so")
-SOURCES = ["sherry_cuda.cu", "ffn_cuda.cu", "sherry_host.cpp"]
+SOURCES = ["sherry_cuda.cu", "ffn_cuda.cu", "grad_cuda.cu", "sherry_host.cpp"]
 HEADERS = sorted(f for f in os.listdir(os.path.join(os.path.dirname(os.path.abspath(__file__)), "csrc"))
                  if f.endswith((".h", ".cuh")))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

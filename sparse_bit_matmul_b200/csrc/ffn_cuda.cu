@@ -164,20 +164,6 @@ __global__ void repack_t_kernel(Codes codes, int64_t R, int64_t K, uint32_t* __r
 // ---------------------------------------------------------------------------
 // host helpers
 // ---------------------------------------------------------------------------
-// Runs `set` once per device (function attributes belong to a context); a
-// device beyond the 64 tracked runs it every time.
-template <class F>
-int once_per_device(std::atomic<uint64_t>& done, F set)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return SHERRY_ERR_CUDA;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (done.load(std::memory_order_acquire) & bit) return SHERRY_OK;
-    if (set() != cudaSuccess) return SHERRY_ERR_CUDA;
-    done.fetch_or(bit, std::memory_order_release);
-    return SHERRY_OK;
-}
-
 bool dtype_ok(int dtype) { return dtype == SHERRY_F32 || dtype == SHERRY_BF16 || dtype == SHERRY_F16; }
 bool act_ok(int act) { return act >= SHERRY_ACT_NONE && act <= SHERRY_ACT_GELU_TANH; }
 bool aligned_elem(const void* p, int dtype)
@@ -397,24 +383,6 @@ int64_t digit_bytes(int dtype, int64_t M, int64_t R)
 
 constexpr int64_t kGradMaxRows = (int64_t(1) << 24) - 1;
 
-constexpr int kDigitsSmemMax = 200 * 1024;
-
-template <bool GATED, int D>
-int launch_digits(grad::Params g, cudaStream_t s)
-{
-    auto kernel = grad::grad_digits_kernel<GATED, D>;
-    static std::atomic<uint64_t> done{0};
-    const int st = once_per_device(done, [&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDigitsSmemMax);
-    });
-    if (st != SHERRY_OK) return st;
-    const int64_t need = ((g.R + 3) & ~int64_t(3)) * 4;
-    const int smem = need <= kDigitsSmemMax ? (int)need : 0;
-    g.cache = smem / 4;
-    const int threads = g.R >= 8192 ? 1024 : g.R >= 1024 ? 256 : 128;
-    return cuda_status(launch_pdl(kernel, dim3((unsigned)g.M), dim3((unsigned)threads), (size_t)smem, s, g));
-}
-
 int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* wt, const float* alpha,
              const float* bias, int act, void* dx, float* dalpha, float* dbias, void* work, int64_t M, int64_t R,
              int64_t No, int64_t K, bool gated, cudaStream_t s)
@@ -439,8 +407,6 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.x_scale = x_scale;
     g.alpha = alpha;
     g.bias = bias;
-    g.dtype = dtype;
-    g.act = act;
     g.M = M;
     g.R = R;
     g.No = No;
@@ -451,15 +417,12 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.dalpha = dalpha;
     g.dbias = dbias;
     if (dx) {
-        if (gated) st = D == 2 ? launch_digits<true, 2>(g, s) : launch_digits<true, 4>(g, s);
-        else st = D == 2 ? launch_digits<false, 2>(g, s) : launch_digits<false, 4>(g, s);
+        st = grad::launch_digits(g, gated, act, dtype, di.sms, s);
         if (st != SHERRY_OK) return st;
     }
     if (dalpha || dbias) {
-        const dim3 grid((unsigned)((No + 31) / 32)), block(32 * grad::kColWarps);
-        const cudaError_t e = gated ? launch_pdl(grad::grad_columns_kernel<true>, grid, block, 0, s, g)
-                                    : launch_pdl(grad::grad_columns_kernel<false>, grid, block, 0, s, g);
-        if (e != cudaSuccess) return cuda_status(e);
+        st = grad::launch_columns(g, gated, act, dtype, di.sms, s);
+        if (st != SHERRY_OK) return st;
     }
     if (!dx) return SHERRY_OK;
     tc::EpParams p = {};

@@ -18,6 +18,8 @@
 #pragma once
 
 #include <cstdint>
+#include <cstring>
+#include <cuda_runtime.h>
 
 #include "epilogue.cuh"
 #include "ptx.cuh"
@@ -32,24 +34,34 @@ struct Params {
     const float* x_scale;       // [M] (with acc)
     const float* alpha;         // [R]
     const float* bias;          // [R] or null
-    int dtype, act;
     int64_t M, R, No;           // R = No, or 2 No when gated
     int8_t* dig;                // [M * D][ld] digit rows
     float* dscale;              // [M]
     int64_t ld;                 // a multiple of 16, >= R
-    int cache;                  // floats of e that fit in the block's shared memory
+    int seg;                    // rows of the weight per block of a cluster, a multiple of 4
+    int cached;                 // a block's e fits in its shared memory
     int vec;                    // rows and bases allow 16-byte loads of four rows' values
     float* dalpha;              // [R] or null
     float* dbias;               // [R] or null
 };
 
-// dz of one pre-activation (linear)
-__device__ __forceinline__ float dz_linear(float dy, float z, int act)
+template <int DT>
+struct Elem {
+    using type = uint16_t;
+};
+template <>
+struct Elem<SHERRY_F32> {
+    using type = float;
+};
+template <int DT>
+__device__ __forceinline__ float widen(typename Elem<DT>::type v)
 {
-    float f, d;
-    ep::act_slope(z, act, f, d);
-    return __fmul_rn(dy, d);
+    if constexpr (DT == SHERRY_F32) return v;
+    else return ep::from16(v, DT);
 }
+
+template <int DT>
+constexpr int kDigits = DT == SHERRY_BF16 ? 2 : 4;
 
 __device__ __forceinline__ float pre_act(int32_t acc, float al, float s, bool has_bias, float b)
 {
@@ -57,123 +69,165 @@ __device__ __forceinline__ float pre_act(int32_t acc, float al, float s, bool ha
     return has_bias ? __fadd_rn(z, b) : z;
 }
 
-// four consecutive 16-byte aligned values, or element by element with a bound
-__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t end, bool vec, float (&v)[4])
+// Four values from p, which has `left` of them (16-byte aligned when vec and
+// left >= 4).
+template <class T>
+__device__ __forceinline__ void load4(const T* p, int64_t left, bool vec, T (&v)[4])
 {
     if (vec) {
-        const float4 t = *reinterpret_cast<const float4*>(p + i);
-        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+        const uint4 t = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) memcpy(&v[k], &w[k], 4);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = i + k < end ? p[i + k] : 0.0f;
-    }
-}
-__device__ __forceinline__ void load4(const int32_t* p, int64_t i, int64_t end, bool vec, int32_t (&v)[4])
-{
-    if (vec) {
-        const int4 t = *reinterpret_cast<const int4*>(p + i);
-        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = i + k < end ? p[i + k] : 0;
+        for (int k = 0; k < 4; ++k) v[k] = k < left ? p[k] : T(0);
     }
 }
 
-// dy of output columns c .. c + C - 1 of token m
-template <int C>
-__device__ __forceinline__ void load_dy(const Params& p, int64_t m, int64_t c, float (&g)[C])
+// C values of dy (2 or 4) from p, which has `left` of them.
+template <int DT, int C>
+__device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int64_t left, bool vec, float (&g)[C])
 {
-    const int64_t at = m * p.No + c;
-    if (p.vec) {
-        if (p.dtype == SHERRY_F32) {
+    using E = typename Elem<DT>::type;
+    if (vec) {
+        if constexpr (DT == SHERRY_F32) {
 #pragma unroll
             for (int k = 0; k < C; k += 2) {
-                const float2 t = *reinterpret_cast<const float2*>(static_cast<const float*>(p.dy) + at + k);
+                const float2 t = *reinterpret_cast<const float2*>(p + k);
                 g[k] = t.x;
                 g[k + 1] = t.y;
             }
         } else {
+            uint32_t t[C / 2];
+            if constexpr (C == 4) {
+                const uint2 w = *reinterpret_cast<const uint2*>(p);
+                t[0] = w.x;
+                t[1] = w.y;
+            } else {
+                t[0] = *reinterpret_cast<const uint32_t*>(p);
+            }
 #pragma unroll
-            for (int k = 0; k < C; k += 2) {
-                const uint32_t t = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.dy) + at + k);
-                g[k] = ep::from16((uint16_t)(t & 0xFFFFu), p.dtype);
-                g[k + 1] = ep::from16((uint16_t)(t >> 16), p.dtype);
+            for (int k = 0; k < C / 2; ++k) {
+                g[2 * k] = widen<DT>((E)(t[k] & 0xFFFFu));
+                g[2 * k + 1] = widen<DT>((E)(t[k] >> 16));
             }
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < C; ++k) g[k] = c + k < p.No ? ep::load_elem(p.dy, at + k, p.dtype) : 0.0f;
+        for (int k = 0; k < C; ++k) g[k] = k < left ? widen<DT>(p[k]) : 0.0f;
     }
 }
 
-// e of rows 4u .. 4u + 3 of token m (0 past R)
-template <bool GATED>
-__device__ __forceinline__ void e4(const Params& p, int64_t m, int64_t u, float s, float (&e)[4])
+// What four consecutive weight rows need of alpha and bias.
+struct Rows4 {
+    float al[4], b[4];
+};
+__device__ __forceinline__ Rows4 load_rows(const Params& p, int64_t r)
 {
-    const int64_t r = 4 * u;
-    if (r >= p.R) {
-        e[0] = e[1] = e[2] = e[3] = 0.0f;
-        return;
-    }
-    float al[4], b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int32_t a[4] = {0, 0, 0, 0};
-    load4(p.alpha, r, p.R, p.vec, al);
-    if (p.bias) load4(p.bias, r, p.R, p.vec, b);
-    if (p.acc) load4(p.acc + m * p.R, r, p.R, p.vec, a);
-    const bool hb = p.bias != nullptr;
+    Rows4 w;
+    load4(p.alpha + r, p.R - r, p.vec, w.al);
+    w.b[0] = w.b[1] = w.b[2] = w.b[3] = 0.0f;
+    if (p.bias) load4(p.bias + r, p.R - r, p.vec, w.b);
+    return w;
+}
+
+// dz of four consecutive weight rows of one token, from their sums a and the
+// token's dy (two columns when gated)
+template <bool GATED, int ACT, int C>
+__device__ __forceinline__ void dz4(const int32_t (&a)[4], const float (&g)[C], const Rows4& w, bool hb, float s,
+                                    float (&dz)[4])
+{
     if constexpr (GATED) {
-        float g[2];
-        load_dy<2>(p, m, r >> 1, g);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             float f, d;
-            ep::act_slope(pre_act(a[2 * k], al[2 * k], s, hb, b[2 * k]), p.act, f, d);
-            const float up = pre_act(a[2 * k + 1], al[2 * k + 1], s, hb, b[2 * k + 1]);
-            e[2 * k] = __fmul_rn(__fmul_rn(__fmul_rn(g[k], up), d), al[2 * k]);
-            e[2 * k + 1] = __fmul_rn(__fmul_rn(g[k], f), al[2 * k + 1]);
+            ep::act_slope(pre_act(a[2 * k], w.al[2 * k], s, hb, w.b[2 * k]), ACT, f, d);
+            const float up = pre_act(a[2 * k + 1], w.al[2 * k + 1], s, hb, w.b[2 * k + 1]);
+            dz[2 * k] = __fmul_rn(__fmul_rn(g[k], up), d);
+            dz[2 * k + 1] = __fmul_rn(g[k], f);
         }
     } else {
-        float g[4];
-        load_dy<4>(p, m, r, g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = __fmul_rn(dz_linear(g[k], pre_act(a[k], al[k], s, hb, b[k]), p.act), al[k]);
+        for (int k = 0; k < 4; ++k) {
+            float f, d;
+            ep::act_slope(pre_act(a[k], w.al[k], s, hb, w.b[k]), ACT, f, d);
+            dz[k] = __fmul_rn(g[k], d);
+        }
     }
 }
 
-// One block per token: e into shared memory (recomputed when it does not
-// fit), its largest magnitude, then the digit rows.
-template <bool GATED, int D>
-__global__ void __launch_bounds__(1024) grad_digits_kernel(const Params p)
+// e of rows r .. r + 3 of token m (r < R; 0 past R)
+template <bool GATED, int ACT, int DT>
+__device__ __forceinline__ void e4(const Params& p, int64_t m, int64_t r, float s, float (&e)[4])
 {
+    constexpr int C = GATED ? 2 : 4;
+    const int64_t c = GATED ? r >> 1 : r;
+    float g[C], dz[4];
+    int32_t a[4] = {0, 0, 0, 0};
+    load_dy<DT, C>(static_cast<const typename Elem<DT>::type*>(p.dy) + m * p.No + c, p.No - c, p.vec, g);
+    if (p.acc) load4(p.acc + m * p.R + r, p.R - r, p.vec, a);
+    const Rows4 w = load_rows(p, r);
+    dz4<GATED, ACT, C>(a, g, w, p.bias != nullptr, s, dz);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = __fmul_rn(dz[k], w.al[k]);
+}
+
+// One cluster of blocks per token, `seg` weight rows per block: e into shared
+// memory (recomputed when it does not fit), the token's largest |e| over the
+// cluster, then the digit rows.
+constexpr int kDigitThreads = 256;
+
+template <bool GATED, int ACT, int DT>
+__global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params p)
+{
+    constexpr int D = kDigits<DT>;
+    constexpr int kWarps = kDigitThreads / 32;
     extern __shared__ __align__(16) float cache[];
-    __shared__ float warp_max[32];
+    __shared__ float warp_max[kWarps];
+    __shared__ float block_max;                              // NaN: the block met an Inf or NaN
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const int64_t m = blockIdx.x;
-    const int tid = threadIdx.x, nthr = blockDim.x;
-    const int64_t U = (p.R + 3) >> 2;
-    const bool cached = 4 * U <= p.cache;
+    const uint32_t CX = gridDim.x, rank = blockIdx.x;
+    const int64_t m = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t r0 = (int64_t)rank * p.seg;
+    const int U = (int)((min(r0 + p.seg, (p.R + 3) & ~int64_t(3)) - r0) >> 2);     // units of four rows, may be <= 0
     const float s = p.acc ? p.x_scale[m] : 0.0f;
     float mx = 0.0f;
     bool bad = false;
-    for (int64_t u = tid; u < U; u += nthr) {
+#pragma unroll 2
+    for (int u = tid; u < U; u += kDigitThreads) {
         float e[4];
-        e4<GATED>(p, m, u, s, e);
+        e4<GATED, ACT, DT>(p, m, r0 + 4 * u, s, e);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float a = fabsf(e[k]);
             mx = fmaxf(mx, a);
             bad |= !(a <= 3.4028234e38f);
         }
-        if (cached) *reinterpret_cast<float4*>(cache + 4 * u) = make_float4(e[0], e[1], e[2], e[3]);
+        if (p.cached) *reinterpret_cast<float4*>(cache + 4 * u) = make_float4(e[0], e[1], e[2], e[3]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
+    if (lane == 0) warp_max[tid >> 5] = mx;
     bad = __syncthreads_or(bad);
-    mx = (tid & 31) < (nthr >> 5) ? warp_max[tid & 31] : 0.0f;
+    mx = lane < kWarps ? warp_max[lane] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = kWarps / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = __shfl_sync(0xffffffffu, mx, 0);
+    if (CX > 1) {
+        if (tid == 0) block_max = bad ? __uint_as_float(0x7FC00000u) : mx;
+        ptx::cluster_arrive_release();
+        ptx::cluster_wait_acquire();
+        float other = 0.0f;
+        if (lane < (int)CX) other = ptx::ld_cluster_f32(ptx::smem_u32(&block_max), (uint32_t)lane);
+        ptx::cluster_arrive_release();                       // waited for at the end: the maxima stay readable
+        bad = __any_sync(0xffffffffu, other != other);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) other = fmaxf(other, __shfl_xor_sync(0xffffffffu, other, o));
+        mx = other;
+    }
 
     // v = e * inv, dx = sum * sc
     float inv = 0.0f, sc = 0.0f;
@@ -194,15 +248,19 @@ __global__ void __launch_bounds__(1024) grad_digits_kernel(const Params p)
         }
     }
     if (bad) sc = __uint_as_float(0x7FC00000u);              // the whole dx row becomes NaN
-    if (tid == 0) p.dscale[m] = sc;
-    for (int64_t u = tid; u < (p.ld >> 2); u += nthr) {
+    if (tid == 0 && rank == 0) p.dscale[m] = sc;
+    // the block of the last rows also writes the padding up to ld
+    const int W = (int)((min(r0 + p.seg, p.ld) - r0) >> 2);
+    int8_t* dig = p.dig + m * D * p.ld + r0;
+#pragma unroll 2
+    for (int u = tid; u < W; u += kDigitThreads) {
         float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (u < U && inv != 0.0f) {
-            if (cached) {
+            if (p.cached) {
                 const float4 t = *reinterpret_cast<const float4*>(cache + 4 * u);
                 e[0] = t.x; e[1] = t.y; e[2] = t.z; e[3] = t.w;
             } else {
-                e4<GATED>(p, m, u, s, e);
+                e4<GATED, ACT, DT>(p, m, r0 + 4 * u, s, e);
             }
         }
         int32_t v[4];
@@ -210,75 +268,90 @@ __global__ void __launch_bounds__(1024) grad_digits_kernel(const Params p)
         for (int k = 0; k < 4; ++k) v[k] = __float2int_rn(__fmul_rn(e[k], inv));
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            uint32_t w = 0;
+            // the low bytes of the four values; then v = (v - digit) / 256,
+            // which is (v + 128) >> 8 for a digit in [-128, 127]
+            const uint32_t lo = __byte_perm((uint32_t)v[0], (uint32_t)v[1], 0x0040u);
+            const uint32_t hi = __byte_perm((uint32_t)v[2], (uint32_t)v[3], 0x0040u);
+            *reinterpret_cast<uint32_t*>(dig + d * p.ld + 4 * u) = __byte_perm(lo, hi, 0x5410u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                w |= ((uint32_t)v[k] & 0xFFu) << (8 * k);
-                v[k] = (v[k] - (int32_t)(int8_t)(v[k] & 0xFF)) >> 8;
-            }
-            *reinterpret_cast<uint32_t*>(p.dig + (m * D + d) * p.ld + 4 * u) = w;
+            for (int k = 0; k < 4; ++k) v[k] = (v[k] + 128) >> 8;
         }
     }
+    if (CX > 1) ptx::cluster_wait_acquire();
 }
 
-// Column sums: a block owns 32 output columns, its warps take the tokens in
-// turn, and the warps' sums meet in shared memory in a fixed order.
-constexpr int kColWarps = 16;
+// Column sums: a block owns the rows of 32 lanes x 4 weight rows, its warps
+// (and the blocks of its cluster, which share the columns) take the tokens in
+// turn, and the partial sums meet in a fixed order.
+constexpr int kColWarps = 8;
+constexpr int kColRows = 128;                                // weight rows per block
 
-template <bool GATED>
+template <bool GATED, int ACT, int DT>
 __global__ void __launch_bounds__(32 * kColWarps) grad_columns_kernel(const Params p)
 {
-    constexpr int S = GATED ? 4 : 2;                         // dalpha, dbias of each row of the column
-    __shared__ float part[kColWarps][S][32];
+    constexpr int C = GATED ? 2 : 4;
+    using E = typename Elem<DT>::type;
+    __shared__ float part[kColWarps][2][kColRows];
+    __shared__ float total[2][kColRows];
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    const bool in = c < p.No;
-    float sum[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) sum[i] = 0.0f;
-    if (in) {
+    const uint32_t CY = gridDim.y, rank = blockIdx.y;
+    const int64_t r = (int64_t)blockIdx.x * kColRows + 4 * lane;
+    float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r < p.R) {
         const bool hb = p.bias != nullptr;
-        float al[2] = {0.0f, 0.0f}, b[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < (GATED ? 2 : 1); ++k) {
-            const int64_t r = GATED ? 2 * c + k : c;
-            al[k] = p.alpha[r];
-            if (hb) b[k] = p.bias[r];
-        }
+        const Rows4 w = load_rows(p, r);
+        const int64_t c = GATED ? r >> 1 : r;
+        const int64_t m0 = (int64_t)rank * kColWarps + warp, step = (int64_t)CY * kColWarps;
+        const E* dy = static_cast<const E*>(p.dy) + m0 * p.No + c;
+        const int32_t* ac = p.acc ? p.acc + m0 * p.R + r : nullptr;
+        const int64_t dstep = step * p.No, astep = step * p.R, left = p.R - r, cleft = p.No - c;
 #pragma unroll 4
-        for (int64_t m = warp; m < p.M; m += kColWarps) {
-            const float g = ep::load_elem(p.dy, m * p.No + c, p.dtype);
-            const float s = p.acc ? p.x_scale[m] : 0.0f;
-            if constexpr (GATED) {
-                const int2 a = *reinterpret_cast<const int2*>(p.acc + m * p.R + 2 * c);
-                float f, d;
-                ep::act_slope(pre_act(a.x, al[0], s, hb, b[0]), p.act, f, d);
-                const float up = pre_act(a.y, al[1], s, hb, b[1]);
-                const float z0 = __fmul_rn(__fmul_rn(g, up), d), z1 = __fmul_rn(g, f);
-                sum[0] = __fmaf_rn(z0, __fmul_rn((float)a.x, s), sum[0]);
-                sum[1] = __fmaf_rn(z1, __fmul_rn((float)a.y, s), sum[1]);
-                sum[2] = __fadd_rn(sum[2], z0);
-                sum[3] = __fadd_rn(sum[3], z1);
-            } else {
-                const int32_t a = p.acc ? p.acc[m * p.R + c] : 0;
-                const float z = dz_linear(g, pre_act(a, al[0], s, hb, b[0]), p.act);
-                sum[0] = __fmaf_rn(z, __fmul_rn((float)a, s), sum[0]);
-                sum[1] = __fadd_rn(sum[1], z);
+        for (int64_t m = m0; m < p.M; m += step) {
+            float g[C], dz[4], s = 0.0f;
+            int32_t a[4] = {0, 0, 0, 0};
+            load_dy<DT, C>(dy, cleft, p.vec, g);
+            if (ac) {
+                load4(ac, left, p.vec, a);
+                s = p.x_scale[m];
+                ac += astep;
+            }
+            dy += dstep;
+            dz4<GATED, ACT, C>(a, g, w, hb, s, dz);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sa[k] = __fmaf_rn(dz[k], __fmul_rn((float)a[k], s), sa[k]);
+                sb[k] = __fadd_rn(sb[k], dz[k]);
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < S; ++i) part[warp][i][lane] = sum[i];
+    *reinterpret_cast<float4*>(&part[warp][0][4 * lane]) = make_float4(sa[0], sa[1], sa[2], sa[3]);
+    *reinterpret_cast<float4*>(&part[warp][1][4 * lane]) = make_float4(sb[0], sb[1], sb[2], sb[3]);
     __syncthreads();
-    if (warp < S && in) {
-        float t = 0.0f;
-        for (int w = 0; w < kColWarps; ++w) t = __fadd_rn(t, part[w][warp][lane]);
-        float* out = (GATED ? warp < 2 : warp < 1) ? p.dalpha : p.dbias;
-        if (out) out[GATED ? 2 * c + (warp & 1) : c] = t;
+    static_assert(32 * kColWarps == 2 * kColRows, "one thread per sum");
+    const int which = threadIdx.x / kColRows, i = threadIdx.x % kColRows;
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kColWarps; ++w) t = __fadd_rn(t, part[w][which][i]);
+    if (CY > 1) {
+        total[which][i] = t;
+        ptx::cluster_arrive_release();
+        ptx::cluster_wait_acquire();
+        if (rank == 0)
+            for (uint32_t y = 1; y < CY; ++y) t = __fadd_rn(t, ptx::ld_cluster_f32(ptx::smem_u32(&total[which][i]), y));
+        ptx::cluster_arrive_release();                       // the sums stay readable until read
+        ptx::cluster_wait_acquire();
+        if (rank != 0) return;
     }
+    const int64_t n = (int64_t)blockIdx.x * kColRows + i;
+    float* out = which ? p.dbias : p.dalpha;
+    if (out && n < p.R) out[n] = t;
 }
+
+// Host: the two launches of a gradient call (grad_cuda.cu).
+int launch_digits(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream);
+int launch_columns(const Params& p, bool gated, int act, int dtype, int sms, cudaStream_t stream);
 
 }  // namespace grad
 }  // namespace sherry

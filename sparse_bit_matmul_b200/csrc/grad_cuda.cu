@@ -1,0 +1,120 @@
+// Launches of the elementwise half of the feed-forward gradients (grad.cuh),
+// one kernel per activation and element type.
+#include <algorithm>
+#include <atomic>
+
+#include "sherry.h"
+#include "sherry_internal.h"
+#include "host_common.h"
+#include "grad.cuh"
+
+namespace sherry {
+namespace grad {
+namespace {
+
+constexpr int kCacheMax = 200 * 1024;       // bytes of e a block may hold
+constexpr int kSegMin = 1024;               // weight rows worth a block of their own
+constexpr int kSegMax = 8192;               // above, a block's 32 KB keep its neighbours off the SM
+constexpr int kClusterMax = 8;
+
+template <class K>
+cudaError_t launch_cluster(K kernel, dim3 grid, dim3 cluster, int threads, size_t smem, cudaStream_t stream,
+                           const Params& p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster.x;
+    attr[1].val.clusterDim.y = cluster.y;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool GATED, int ACT, int DT>
+int digits(Params p, int sms, cudaStream_t stream)
+{
+    auto kernel = grad_digits_kernel<GATED, ACT, DT>;
+    static std::atomic<uint64_t> done{0};
+    const int st = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheMax);
+    });
+    if (st != SHERRY_OK) return st;
+    // Blocks per token: so many that a block holds at most kSegMax rows, and
+    // more while the grid leaves SMs without four blocks.
+    int cx = 1;
+    while (cx < kClusterMax && (p.ld > (int64_t)cx * kSegMax || (p.M * cx < 4 * (int64_t)sms && p.ld >= (int64_t)cx * 2 * kSegMin)))
+        cx *= 2;
+    p.seg = (int)(((p.ld + cx - 1) / cx + 15) & ~int64_t(15));
+    const int64_t need = 4 * std::min<int64_t>(p.seg, (p.R + 3) & ~int64_t(3));
+    p.cached = need <= kCacheMax;
+    // tokens in grid.y: at most 65535 a launch
+    Params q = p;
+    for (int64_t m0 = 0; m0 < p.M; m0 += 65535) {
+        const int64_t left = p.M - m0, n = left < 65535 ? left : 65535;
+        q.dy = static_cast<const uint8_t*>(p.dy) + m0 * p.No * (DT == SHERRY_F32 ? 4 : 2);
+        q.acc = p.acc ? p.acc + m0 * p.R : nullptr;
+        q.x_scale = p.x_scale ? p.x_scale + m0 : nullptr;
+        q.dig = p.dig + m0 * kDigits<DT> * p.ld;
+        q.dscale = p.dscale + m0;
+        const cudaError_t e = launch_cluster(kernel, dim3((unsigned)cx, (unsigned)n), dim3((unsigned)cx, 1), kDigitThreads,
+                                             p.cached ? (size_t)need : 0, stream, q);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    return SHERRY_OK;
+}
+
+template <bool GATED, int ACT, int DT>
+int columns(const Params& p, int sms, cudaStream_t stream)
+{
+    const int64_t bx = (p.R + kColRows - 1) / kColRows;
+    // Blocks that share the columns: while SMs are left without four blocks
+    // and every warp keeps four tokens.
+    int cy = 1;
+    while (cy < kClusterMax && bx * cy < 4 * (int64_t)sms && p.M >= (int64_t)cy * 2 * kColWarps * 4) cy *= 2;
+    return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT>, dim3((unsigned)bx, (unsigned)cy),
+                                      dim3(1, (unsigned)cy), 32 * kColWarps, 0, stream, p));
+}
+
+template <bool GATED, int ACT>
+int of_type(bool dig, const Params& p, int dtype, int sms, cudaStream_t s)
+{
+    if (dtype == SHERRY_F32) return dig ? digits<GATED, ACT, SHERRY_F32>(p, sms, s) : columns<GATED, ACT, SHERRY_F32>(p, sms, s);
+    if (dtype == SHERRY_BF16) return dig ? digits<GATED, ACT, SHERRY_BF16>(p, sms, s) : columns<GATED, ACT, SHERRY_BF16>(p, sms, s);
+    return dig ? digits<GATED, ACT, SHERRY_F16>(p, sms, s) : columns<GATED, ACT, SHERRY_F16>(p, sms, s);
+}
+
+template <bool GATED>
+int of_act(bool dig, const Params& p, int act, int dtype, int sms, cudaStream_t s)
+{
+    switch (act) {
+    case SHERRY_ACT_NONE: return of_type<GATED, SHERRY_ACT_NONE>(dig, p, dtype, sms, s);
+    case SHERRY_ACT_RELU: return of_type<GATED, SHERRY_ACT_RELU>(dig, p, dtype, sms, s);
+    case SHERRY_ACT_RELU2: return of_type<GATED, SHERRY_ACT_RELU2>(dig, p, dtype, sms, s);
+    case SHERRY_ACT_SILU: return of_type<GATED, SHERRY_ACT_SILU>(dig, p, dtype, sms, s);
+    case SHERRY_ACT_GELU: return of_type<GATED, SHERRY_ACT_GELU>(dig, p, dtype, sms, s);
+    default: return of_type<GATED, SHERRY_ACT_GELU_TANH>(dig, p, dtype, sms, s);
+    }
+}
+
+}  // namespace
+
+int launch_digits(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream)
+{
+    return gated ? of_act<true>(true, p, act, dtype, sms, stream) : of_act<false>(true, p, act, dtype, sms, stream);
+}
+
+int launch_columns(const Params& p, bool gated, int act, int dtype, int sms, cudaStream_t stream)
+{
+    return gated ? of_act<true>(false, p, act, dtype, sms, stream) : of_act<false>(false, p, act, dtype, sms, stream);
+}
+
+}  // namespace grad
+}  // namespace sherry

@@ -2,6 +2,7 @@
 // (definitions in sherry_cuda.cu unless inline).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -64,6 +65,20 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Runs `set` once per device (function attributes belong to a context); a
+// device beyond the 64 tracked runs it every time.
+template <class F>
+int once_per_device(std::atomic<uint64_t>& done, F set)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SHERRY_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return SHERRY_OK;
+    if (set() != cudaSuccess) return SHERRY_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_release);
+    return SHERRY_OK;
 }
 
 }  // namespace sherry

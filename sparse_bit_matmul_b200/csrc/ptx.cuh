@@ -333,6 +333,13 @@ __device__ __forceinline__ void red_cluster_add_s32(uint32_t local_addr, uint32_
 {
     asm volatile("red.shared::cluster.add.s32 [%0], %1;" ::"r"(mapa(local_addr, cta)), "r"(v) : "memory");
 }
+// The float at `local_addr`'s offset in the shared memory of CTA `cta`.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t local_addr, uint32_t cta)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa(local_addr, cta)) : "memory");
+    return v;
+}
 // Shared load the compiler may schedule freely (no side effects declared).
 __device__ __forceinline__ uint32_t lds_u32_nv(uint32_t addr)
 {

@@ -266,6 +266,12 @@ def test_every_slope(act):
 def test_gradient_of_more_rows_than_shared_memory_holds():
     run_backward(False, 3, 32, 52001, "bf16", "relu", False)
     run_backward(True, 2, 64, 26004, "f32", "silu", True)
+    run_backward(False, 1, 32, 420003, "bf16", "silu", True)
+
+
+def test_more_tokens_than_one_grid_dimension():
+    run_forward(True, 70001, 32, 3, "bf16", "silu", False, False)
+    run_backward(True, 70001, 32, 3, "bf16", "silu", False)
 
 
 def test_linear_gradient_without_sums():
