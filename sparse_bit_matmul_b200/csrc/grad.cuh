@@ -23,6 +23,7 @@
 
 #include "epilogue.cuh"
 #include "ptx.cuh"
+#include "quant.cuh"
 #include "sherry_internal.h"
 
 namespace sherry {
@@ -119,16 +120,17 @@ __device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int64_
     }
 }
 
-// What four consecutive weight rows need of alpha and bias.
+// What four consecutive weight rows (of `left` from there on) need of alpha and bias.
 struct Rows4 {
     float al[4], b[4];
 };
-__device__ __forceinline__ Rows4 load_rows(const Params& p, int64_t r)
+template <bool VEC>
+__device__ __forceinline__ Rows4 load_rows(const float* alpha, const float* bias, int64_t left)
 {
     Rows4 w;
-    load4(p.alpha + r, p.R - r, p.vec, w.al);
+    load4(alpha, left, VEC, w.al);
     w.b[0] = w.b[1] = w.b[2] = w.b[3] = 0.0f;
-    if (p.bias) load4(p.bias + r, p.R - r, p.vec, w.b);
+    if (bias) load4(bias, left, VEC, w.b);
     return w;
 }
 
@@ -157,91 +159,100 @@ __device__ __forceinline__ void dz4(const int32_t (&a)[4], const float (&g)[C], 
     }
 }
 
-// e of rows r .. r + 3 of token m (r < R; 0 past R)
-template <bool GATED, int ACT, int DT>
-__device__ __forceinline__ void e4(const Params& p, int64_t m, int64_t r, float s, float (&e)[4])
-{
-    constexpr int C = GATED ? 2 : 4;
-    const int64_t c = GATED ? r >> 1 : r;
-    float g[C], dz[4];
-    int32_t a[4] = {0, 0, 0, 0};
-    load_dy<DT, C>(static_cast<const typename Elem<DT>::type*>(p.dy) + m * p.No + c, p.No - c, p.vec, g);
-    if (p.acc) load4(p.acc + m * p.R + r, p.R - r, p.vec, a);
-    const Rows4 w = load_rows(p, r);
-    dz4<GATED, ACT, C>(a, g, w, p.bias != nullptr, s, dz);
+// e of units of four rows of one token's segment: unit u from row 4 u on.
+template <bool GATED, int ACT, int DT, bool VEC>
+struct Segment {
+    static constexpr int C = GATED ? 2 : 4;
+    using E = typename Elem<DT>::type;
+    const E* dy;
+    const int32_t* acc;
+    const float *alpha, *bias;
+    float s;
+    int rows, cols;             // left in the segment's arrays
+
+    __device__ __forceinline__ Segment(const Params& p, int64_t m, int64_t r0)
+    {
+        const int64_t c0 = GATED ? r0 >> 1 : r0;
+        dy = static_cast<const E*>(p.dy) + m * p.No + c0;
+        acc = p.acc ? p.acc + m * p.R + r0 : nullptr;
+        alpha = p.alpha + r0;
+        bias = p.bias ? p.bias + r0 : nullptr;
+        s = p.acc ? p.x_scale[m] : 0.0f;
+        rows = (int)(p.R - r0);
+        cols = (int)(p.No - c0);
+    }
+    __device__ __forceinline__ void e4(int u, float (&e)[4]) const
+    {
+        float g[C], dz[4];
+        int32_t a[4] = {0, 0, 0, 0};
+        load_dy<DT, C>(dy + C * u, cols - C * u, VEC, g);
+        if (acc) load4(acc + 4 * u, rows - 4 * u, VEC, a);
+        const Rows4 w = load_rows<VEC>(alpha + 4 * u, bias ? bias + 4 * u : nullptr, rows - 4 * u);
+        dz4<GATED, ACT, C>(a, g, w, bias != nullptr, s, dz);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = __fmul_rn(dz[k], w.al[k]);
-}
+        for (int k = 0; k < 4; ++k) e[k] = __fmul_rn(dz[k], w.al[k]);
+    }
+};
 
 // One cluster of blocks per token, `seg` weight rows per block: e into shared
 // memory (recomputed when it does not fit), the token's largest |e| over the
 // cluster, then the digit rows.
+// Bound by instruction issue and DRAM in about equal parts: magnitudes are
+// compared as integers (one mask and one maximum a value; Inf and NaN order
+// above every number), and 16-bit digits come out of the low bits of e * inv +
+// 1.5 * 2^23 without a conversion instruction.
 constexpr int kDigitThreads = 256;
+constexpr uint32_t kInfBits = 0x7F800000u;
 
-template <bool GATED, int ACT, int DT>
-__global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params p)
+template <bool GATED, int ACT, int DT, bool VEC>
+__device__ __forceinline__ void grad_digits(const Params& p, float* cache, uint32_t* warp_max, uint32_t* block_max)
 {
     constexpr int D = kDigits<DT>;
     constexpr int kWarps = kDigitThreads / 32;
-    extern __shared__ __align__(16) float cache[];
-    __shared__ float warp_max[kWarps];
-    __shared__ float block_max;                              // NaN: the block met an Inf or NaN
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
     const uint32_t CX = gridDim.x, rank = blockIdx.x;
     const int64_t m = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t r0 = (int64_t)rank * p.seg;
     const int U = (int)((min(r0 + p.seg, (p.R + 3) & ~int64_t(3)) - r0) >> 2);     // units of four rows, may be <= 0
-    const float s = p.acc ? p.x_scale[m] : 0.0f;
-    float mx = 0.0f;
-    bool bad = false;
+    const Segment<GATED, ACT, DT, VEC> sg(p, m, r0);
+    uint32_t mx = 0;
 #pragma unroll 2
     for (int u = tid; u < U; u += kDigitThreads) {
         float e[4];
-        e4<GATED, ACT, DT>(p, m, r0 + 4 * u, s, e);
+        sg.e4(u, e);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float a = fabsf(e[k]);
-            mx = fmaxf(mx, a);
-            bad |= !(a <= 3.4028234e38f);
-        }
+        for (int k = 0; k < 4; ++k) mx = max(mx, __float_as_uint(e[k]) & 0x7FFFFFFFu);
         if (p.cached) *reinterpret_cast<float4*>(cache + 4 * u) = make_float4(e[0], e[1], e[2], e[3]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = __reduce_max_sync(0xffffffffu, mx);
     if (lane == 0) warp_max[tid >> 5] = mx;
-    bad = __syncthreads_or(bad);
-    mx = lane < kWarps ? warp_max[lane] : 0.0f;
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    mx = __shfl_sync(0xffffffffu, mx, 0);
+    __syncthreads();
+    mx = __reduce_max_sync(0xffffffffu, lane < kWarps ? warp_max[lane] : 0u);
     if (CX > 1) {
-        if (tid == 0) block_max = bad ? __uint_as_float(0x7FC00000u) : mx;
+        if (tid == 0) *block_max = mx;
         ptx::cluster_arrive_release();
         ptx::cluster_wait_acquire();
-        float other = 0.0f;
-        if (lane < (int)CX) other = ptx::ld_cluster_f32(ptx::smem_u32(&block_max), (uint32_t)lane);
+        uint32_t other = 0;
+        if (lane < (int)CX) other = ptx::ld_cluster_u32(ptx::smem_u32(block_max), (uint32_t)lane);
+        mx = __reduce_max_sync(0xffffffffu, other);
         ptx::cluster_arrive_release();                       // waited for at the end: the maxima stay readable
-        bad = __any_sync(0xffffffffu, other != other);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) other = fmaxf(other, __shfl_xor_sync(0xffffffffu, other, o));
-        mx = other;
     }
 
     // v = e * inv, dx = sum * sc
+    const bool bad = mx >= kInfBits;
+    const float big = __uint_as_float(mx);
     float inv = 0.0f, sc = 0.0f;
-    if (mx > 0.0f && !bad) {
+    if (mx != 0u && !bad) {
         if constexpr (D == 2) {
-            if (mx >= 7.8886091e-31f) {                      // 2^-100
-                inv = __fdiv_rn(32639.0f, mx);
-                sc = __fdiv_rn(mx, 32639.0f);
+            if (big >= 7.8886091e-31f) {                     // 2^-100
+                inv = __fdiv_rn(32639.0f, big);
+                sc = __fdiv_rn(big, 32639.0f);
             } else {
                 inv = 2.0769187e34f;                         // 2^114
                 sc = 4.8148249e-35f;
             }
         } else {
-            const int ex = (int)(__float_as_uint(mx) >> 23) - 127;      // mx < 2^(ex + 1)
+            const int ex = (int)(mx >> 23) - 127;            // big < 2^(ex + 1)
             const int k = min(29 - ex, 126);
             inv = __uint_as_float((uint32_t)(127 + k) << 23);
             sc = __uint_as_float((uint32_t)(127 - k) << 23);
@@ -260,24 +271,39 @@ __global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params
                 const float4 t = *reinterpret_cast<const float4*>(cache + 4 * u);
                 e[0] = t.x; e[1] = t.y; e[2] = t.z; e[3] = t.w;
             } else {
-                e4<GATED, ACT, DT>(p, m, r0 + 4 * u, s, e);
+                sg.e4(u, e);
             }
         }
-        int32_t v[4];
+        uint32_t v[4];
+        // |v| <= 32639: rint(e inv) in the low bits of the sum
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __float2int_rn(__fmul_rn(e[k], inv));
+        for (int k = 0; k < 4; ++k)
+            v[k] = D == 2 ? __float_as_uint(__fmaf_rn(e[k], inv, quant::kRoundMagic))
+                          : (uint32_t)__float2int_rn(__fmul_rn(e[k], inv));
+        // digit d is byte d of v once 128 was added to every byte below it:
+        // (v - digit) / 256 is (v + 128) >> 8 for a digit in [-128, 127]
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            // the low bytes of the four values; then v = (v - digit) / 256,
-            // which is (v + 128) >> 8 for a digit in [-128, 127]
-            const uint32_t lo = __byte_perm((uint32_t)v[0], (uint32_t)v[1], 0x0040u);
-            const uint32_t hi = __byte_perm((uint32_t)v[2], (uint32_t)v[3], 0x0040u);
+            const uint32_t sel = (uint32_t)d | (uint32_t)(4 + d) << 4;
+            const uint32_t lo = __byte_perm(v[0], v[1], sel), hi = __byte_perm(v[2], v[3], sel);
             *reinterpret_cast<uint32_t*>(dig + d * p.ld + 4 * u) = __byte_perm(lo, hi, 0x5410u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = (v[k] + 128) >> 8;
+            for (int k = 0; k < 4; ++k) v[k] += 128u << (8 * d);
         }
     }
     if (CX > 1) ptx::cluster_wait_acquire();
+}
+
+template <bool GATED, int ACT, int DT>
+__global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params p)
+{
+    extern __shared__ __align__(16) float cache[];
+    __shared__ uint32_t warp_max[kDigitThreads / 32];
+    __shared__ uint32_t block_max;
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    if (p.vec) grad_digits<GATED, ACT, DT, true>(p, cache, warp_max, &block_max);
+    else grad_digits<GATED, ACT, DT, false>(p, cache, warp_max, &block_max);
 }
 
 // Column sums: a block owns the rows of 32 lanes x 4 weight rows, its warps
@@ -286,11 +312,60 @@ __global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params
 constexpr int kColWarps = 8;
 constexpr int kColRows = 128;                                // weight rows per block
 
+// One lane's sums over the tokens m0, m0 + step, ..: kBatch tokens' loads are
+// issued before their arithmetic, without a branch between them (past the last
+// token the first one's values are read again and count as zero).
+template <bool GATED, int ACT, int DT, bool VEC, bool ACC>
+__device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t m0, int64_t step, float (&sa)[4],
+                                            float (&sb)[4])
+{
+    constexpr int C = GATED ? 2 : 4;
+    constexpr int kBatch = 4;
+    using E = typename Elem<DT>::type;
+    const bool hb = p.bias != nullptr;
+    const Rows4 w = load_rows<VEC>(p.alpha + r, hb ? p.bias + r : nullptr, p.R - r);
+    const int64_t c = GATED ? r >> 1 : r;
+    const E* dy = static_cast<const E*>(p.dy) + m0 * p.No + c;
+    const int32_t* acc = ACC ? p.acc + m0 * p.R + r : nullptr;
+    const int64_t left = p.R - r, cleft = p.No - c;
+    if (m0 >= p.M) return;
+    for (int64_t m = m0; m < p.M; m += kBatch * step) {
+        float g[kBatch][C], s[kBatch];
+        int32_t a[kBatch][4];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t at = m + i * step < p.M ? m - m0 + i * step : 0;
+            load_dy<DT, C>(dy + at * p.No, cleft, VEC, g[i]);
+            s[i] = 0.0f;
+            a[i][0] = a[i][1] = a[i][2] = a[i][3] = 0;
+            if constexpr (ACC) {
+                load4(acc + at * p.R, left, VEC, a[i]);
+                s[i] = p.x_scale[m0 + at];
+            }
+        }
+#pragma unroll
+        for (int i = 1; i < kBatch; ++i)
+            if (m + i * step >= p.M) {
+#pragma unroll
+                for (int k = 0; k < C; ++k) g[i][k] = 0.0f;
+                s[i] = 0.0f;
+            }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            float dz[4];
+            dz4<GATED, ACT, C>(a[i], g[i], w, hb, s[i], dz);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sa[k] = __fmaf_rn(dz[k], __fmul_rn((float)a[i][k], s[i]), sa[k]);
+                sb[k] = __fadd_rn(sb[k], dz[k]);
+            }
+        }
+    }
+}
+
 template <bool GATED, int ACT, int DT>
 __global__ void __launch_bounds__(32 * kColWarps) grad_columns_kernel(const Params p)
 {
-    constexpr int C = GATED ? 2 : 4;
-    using E = typename Elem<DT>::type;
     __shared__ float part[kColWarps][2][kColRows];
     __shared__ float total[2][kColRows];
     ptx::pdl_launch_dependents();
@@ -300,30 +375,16 @@ __global__ void __launch_bounds__(32 * kColWarps) grad_columns_kernel(const Para
     const int64_t r = (int64_t)blockIdx.x * kColRows + 4 * lane;
     float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (r < p.R) {
-        const bool hb = p.bias != nullptr;
-        const Rows4 w = load_rows(p, r);
-        const int64_t c = GATED ? r >> 1 : r;
         const int64_t m0 = (int64_t)rank * kColWarps + warp, step = (int64_t)CY * kColWarps;
-        const E* dy = static_cast<const E*>(p.dy) + m0 * p.No + c;
-        const int32_t* ac = p.acc ? p.acc + m0 * p.R + r : nullptr;
-        const int64_t dstep = step * p.No, astep = step * p.R, left = p.R - r, cleft = p.No - c;
-#pragma unroll 4
-        for (int64_t m = m0; m < p.M; m += step) {
-            float g[C], dz[4], s = 0.0f;
-            int32_t a[4] = {0, 0, 0, 0};
-            load_dy<DT, C>(dy, cleft, p.vec, g);
-            if (ac) {
-                load4(ac, left, p.vec, a);
-                s = p.x_scale[m];
-                ac += astep;
+        if constexpr (!GATED && ACT == SHERRY_ACT_NONE) {
+            if (!p.acc) {                                    // dbias alone
+                if (p.vec) column_sums<GATED, ACT, DT, true, false>(p, r, m0, step, sa, sb);
+                else column_sums<GATED, ACT, DT, false, false>(p, r, m0, step, sa, sb);
             }
-            dy += dstep;
-            dz4<GATED, ACT, C>(a, g, w, hb, s, dz);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sa[k] = __fmaf_rn(dz[k], __fmul_rn((float)a[k], s), sa[k]);
-                sb[k] = __fadd_rn(sb[k], dz[k]);
-            }
+        }
+        if (p.acc) {
+            if (p.vec) column_sums<GATED, ACT, DT, true, true>(p, r, m0, step, sa, sb);
+            else column_sums<GATED, ACT, DT, false, true>(p, r, m0, step, sa, sb);
         }
     }
     *reinterpret_cast<float4*>(&part[warp][0][4 * lane]) = make_float4(sa[0], sa[1], sa[2], sa[3]);

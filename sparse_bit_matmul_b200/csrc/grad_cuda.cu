@@ -75,10 +75,28 @@ template <bool GATED, int ACT, int DT>
 int columns(const Params& p, int sms, cudaStream_t stream)
 {
     const int64_t bx = (p.R + kColRows - 1) / kColRows;
-    // Blocks that share the columns: while SMs are left without four blocks
-    // and every warp keeps four tokens.
+    // Blocks that share the columns: of the cluster sizes that leave every
+    // warp four tokens, the one whose last round of resident blocks is
+    // fullest; the smallest such.
+    static std::atomic<int> resident{0};
+    int occ = resident.load(std::memory_order_relaxed);
+    if (occ == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, grad_columns_kernel<GATED, ACT, DT>, 32 * kColWarps, 0) !=
+                cudaSuccess || occ < 1)
+            return SHERRY_ERR_CUDA;
+        resident.store(occ, std::memory_order_relaxed);
+    }
+    const int64_t slots = (int64_t)occ * sms;
     int cy = 1;
-    while (cy < kClusterMax && bx * cy < 4 * (int64_t)sms && p.M >= (int64_t)cy * 2 * kColWarps * 4) cy *= 2;
+    double best = 0.0;
+    for (int y = 1; y <= kClusterMax && (y == 1 || p.M >= (int64_t)y * kColWarps * 4); ++y) {
+        const int64_t blocks = bx * y, rounds = (blocks + slots - 1) / slots;
+        const double full = (double)blocks / (double)(rounds * slots);
+        if (full > best + 0.02) {
+            best = full;
+            cy = y;
+        }
+    }
     return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT>, dim3((unsigned)bx, (unsigned)cy),
                                       dim3(1, (unsigned)cy), 32 * kColWarps, 0, stream, p));
 }

@@ -340,6 +340,12 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t local_addr, uint32_t ct
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa(local_addr, cta)) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t local_addr, uint32_t cta)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa(local_addr, cta)) : "memory");
+    return v;
+}
 // Shared load the compiler may schedule freely (no side effects declared).
 __device__ __forceinline__ uint32_t lds_u32_nv(uint32_t addr)
 {
