@@ -270,6 +270,16 @@ __device__ __forceinline__ void store_strided(char* base, int64_t stride, int cn
     }
 }
 
+template <int O, class T>
+__device__ __forceinline__ void load_strided(const char* base, int64_t stride, int cnt, uint32_t (&v)[O])
+{
+#pragma unroll
+    for (int i = 0; i < O; ++i) {
+        v[i] = i < cnt ? (uint32_t)*reinterpret_cast<const T*>(base) : 0u;
+        base += stride;
+    }
+}
+
 // The kept sums of 16 tokens from m0 on, row n.
 __device__ __forceinline__ void ep_keep16(const EpParams& p, const uint32_t (&v)[16], int64_t m0, int64_t n)
 {
@@ -293,15 +303,13 @@ __device__ __forceinline__ void ep_store16(const EpParams& p, const uint32_t (&v
     const int cnt = col >= p.No ? 0 : left < O ? (int)left : O;
     const int es = ep::elem_size(p.dtype);
     const int64_t at = ((m0 + first) * p.No + col) * es, stride = (int64_t)kStep * p.No * es;
-    float rs[EK == kEpLinear ? O : 1];
+    // as read, widened only when added: all loads are in flight at once
+    [[maybe_unused]] uint32_t rs[EK == kEpLinear ? O : 1];
     if constexpr (EK == kEpLinear) {
         if (p.res) {
             const char* r = static_cast<const char*>(p.res) + at;
-#pragma unroll
-            for (int i = 0; i < O; ++i) {
-                rs[i] = i < cnt ? ep::load_elem(r, 0, p.dtype) : 0.0f;
-                r += stride;
-            }
+            if (p.dtype == SHERRY_F32) load_strided<O, uint32_t>(r, stride, cnt, rs);
+            else load_strided<O, uint16_t>(r, stride, cnt, rs);
         }
     }
     float o[O];
@@ -309,7 +317,9 @@ __device__ __forceinline__ void ep_store16(const EpParams& p, const uint32_t (&v
     if constexpr (EK == kEpLinear) {
         if (p.res) {
 #pragma unroll
-            for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], rs[i]);
+            for (int i = 0; i < O; ++i)
+                o[i] = __fadd_rn(o[i], p.dtype == SHERRY_F32 ? __uint_as_float(rs[i])
+                                                             : ep::from16((uint16_t)rs[i], p.dtype));
         }
     }
     char* base = static_cast<char*>(p.out) + at;
