@@ -217,16 +217,17 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, cudaStream_t stream)
     p.status = device_status_ptr();
     if (!p.status) return SHERRY_ERR_CUDA;
 
-    CUtensorMap map, omap;
+    CUtensorMap map;
+    tc::OutMaps maps;
     st = make_x_map(&map, b, p.M, p.K, ld, BN);
     if (st != SHERRY_OK) return st;
-    std::memset(&omap, 0, sizeof(omap));
+    std::memset(&maps, 0, sizeof(maps));
     p.y_tma = (p.No * ep::elem_size(p.dtype)) % 16 == 0 && aligned16(p.out);
     if (p.res) p.y_tma = p.y_tma && aligned16(p.res);
     if (p.y_tma) {
-        st = make_out_map(&omap, p.out, p.dtype, p.Mo, p.No, EK == tc::kEpGated ? 16 : 32, 16 / D);
+        st = make_out_map(&maps.out, p.out, p.dtype, p.Mo, p.No, EK == tc::kEpGated ? 16 : 32, 16 / D);
         if (st == SHERRY_OK && p.res)
-            st = make_out_map(&p.rmap, const_cast<void*>(p.res), p.dtype, p.Mo, p.No, 32, 16);
+            st = make_out_map(&maps.res, const_cast<void*>(p.res), p.dtype, p.Mo, p.No, 32, 16);
         if (st != SHERRY_OK) return st;
     }
 
@@ -238,7 +239,7 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, cudaStream_t stream)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (st != SHERRY_OK) return st;
-    return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream, map, omap, p));
+    return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream, map, maps, p));
 }
 
 // The token tiles of sherry_gemm_tc (its measurements hold: the loads, decode

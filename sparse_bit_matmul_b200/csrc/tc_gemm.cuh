@@ -190,7 +190,6 @@ struct Params {
 // Parameters of the epilogues other than kEpPlain.  kEpGrad: M counts digit
 // rows (D per token), N is the output's row length, x_scale one per token.
 struct EpParams : Params {
-    CUtensorMap rmap;           // residual boxes of 32 columns x 16 tokens (kEpLinear, with y_tma and res)
     const float* bias;          // [N] or null
     const void* res;            // [Mo][No] or null (kEpLinear)
     void* out;                  // [Mo][No]
@@ -199,13 +198,22 @@ struct EpParams : Params {
     int act;                    // sherry_act
 };
 
+// Tensor maps of the output, and of the residual in boxes of 32 columns x 16
+// tokens (kEpLinear).  Apart from EpParams: taking a map's address makes the
+// compiler read the struct it sits in through memory, field by field.
+struct OutMaps {
+    CUtensorMap out, res;
+};
+
 template <int EK>
 struct ParamsOf {
     using type = EpParams;
+    using maps = OutMaps;
 };
 template <>
 struct ParamsOf<kEpPlain> {
     using type = Params;
+    using maps = CUtensorMap;
 };
 
 // S sums of one weight row (32 lanes: 32 rows), of S consecutive tokens or
@@ -280,23 +288,31 @@ __device__ __forceinline__ void load_strided(const char* base, int64_t stride, i
     }
 }
 
-// The kept sums of 16 tokens from m0 on, row n.
-__device__ __forceinline__ void ep_keep16(const EpParams& p, const uint32_t (&v)[16], int64_t m0, int64_t n)
+// Sums handled at once: kEpLinear has one value per sum where the others have
+// one per two or more, and 16 of them beside a residual do not fit the 96
+// registers that 18 warps leave a thread (with 16, spills made its slices 2.5
+// times as long as kEpGated's).
+template <int EK>
+constexpr int kEpSums = EK == kEpLinear ? 8 : 16;
+
+// The kept sums of S tokens from m0 on, row n.
+template <int S>
+__device__ __forceinline__ void ep_keep(const EpParams& p, const uint32_t (&v)[S], int64_t m0, int64_t n)
 {
     if (!p.acc) return;
     const int64_t left = n < p.N ? p.M - m0 : 0;
-    store_strided<16, uint32_t>(reinterpret_cast<char*>(p.acc + m0 * p.N + n), 4 * p.N, (int)(left < 16 ? left : 16), v);
+    store_strided<S, uint32_t>(reinterpret_cast<char*>(p.acc + m0 * p.N + n), 4 * p.N, (int)(left < S ? left : S), v);
 }
 
-// ep_values of 16 sums, stored element by element: output rows from m0 on,
+// ep_values of S sums, stored element by element: output rows from m0 on,
 // column col (out of range: not stored).  The residual is loaded whole before
 // the first store (it may be the output itself, so a load could not pass a
 // store on its own).
-template <int EK, int D>
-__device__ __forceinline__ void ep_store16(const EpParams& p, const uint32_t (&v)[16], const float* sc, float al,
-                                           float bi, int lane, int64_t m0, int64_t col)
+template <int EK, int D, int S>
+__device__ __forceinline__ void ep_store(const EpParams& p, const uint32_t (&v)[S], const float* sc, float al,
+                                         float bi, int lane, int64_t m0, int64_t col)
 {
-    constexpr int O = EK == kEpGated ? 8 : 16 / D;
+    constexpr int O = EK == kEpGated ? S / 2 : S / D;
     constexpr int kStep = EK == kEpGated ? 2 : 1;            // output rows between values
     const int first = EK == kEpGated ? lane & 1 : 0;
     const int64_t left = (p.Mo - m0 - first + kStep - 1) / kStep;
@@ -313,7 +329,7 @@ __device__ __forceinline__ void ep_store16(const EpParams& p, const uint32_t (&v
         }
     }
     float o[O];
-    ep_values<EK, D, 16, O>(p, v, sc, al, bi, lane, o);
+    ep_values<EK, D, S, O>(p, v, sc, al, bi, lane, o);
     if constexpr (EK == kEpLinear) {
         if (p.res) {
 #pragma unroll
@@ -438,8 +454,9 @@ __device__ __forceinline__ void report(unsigned* status, volatile int* abort_fla
 
 template <int BN, int SC, int WF = kWeightSherry, int EK = kEpPlain, int D = 1>
 __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
-    sherry_gemm_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
-                          const __grid_constant__ typename ParamsOf<EK>::type p)
+    sherry_gemm_tc_kernel(const __grid_constant__ CUtensorMap xmap,
+                          const __grid_constant__ typename ParamsOf<EK>::maps ymap,
+                          const typename ParamsOf<EK>::type p)
 {
     using C = Cfg<BN, SC, WF>;
     static_assert(EK == kEpGrad ? 16 % D == 0 : D == 1, "digits per token");
@@ -883,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                 if constexpr (EK == kEpLinear) {
                     const uint32_t bar = res_bar0 + 8u * slot;
                     ptx::mbar_arrive_expect_tx(bar, (uint32_t)(16 * 32 * ep::elem_size(p.dtype)));
-                    ptx::tma_load_2d(ptx::smem_u32(stg_w + slot * (16 * 32)), &p.rmap, out_x, (int32_t)(tm * BN + 16 * q),
+                    ptx::tma_load_2d(ptx::smem_u32(stg_w + slot * (16 * 32)), &ymap.res, out_x, (int32_t)(tm * BN + 16 * q),
                                      bar);
                 }
             };
@@ -929,22 +946,19 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             int32_t* wsl = p.ws + slot * (int64_t)BN * SHERRY_TILE_ROWS;
             if constexpr (EK != kEpPlain) {
                 if (via_tma) {
-                    // As below, for 16 sums of the lane's row at a time: OT
-                    // output tokens x OW columns per slice, kEpSlots staging
-                    // slots per warp.  A residual box is loaded by TMA into
+                    // As below, in slices of 16 sums x OW output columns with
+                    // kEpSlots staging slots per warp.  A residual box is loaded by TMA into
                     // the slot its outputs will take, up to kEpSlots - 1
                     // slices ahead (the first ones before the accumulators are
                     // complete), and replaced in place.
                     constexpr int OW = EK == kEpGated ? 16 : 32;
-                    constexpr int OT = 16 / D;
-                    constexpr int O = EK == kEpGated ? 8 : OT;
+                    constexpr int S = kEpSums<EK>;
+                    constexpr int O = EK == kEpGated ? S / 2 : S / D;
                     const int scol = EK == kEpGated ? lane >> 1 : lane;
 #pragma unroll 1
                     for (int q = 0; q < nslices; ++q) {
                         const int j0 = 16 * q;
                         const int64_t m0 = (tm * BN + j0) / D;
-                        uint32_t v[16];
-                        ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
                         const uint32_t slot = stage_slice % C::kEpSlots;
                         float* stg = stg_w + slot * (16 * 32);
                         uint16_t* st16 = reinterpret_cast<uint16_t*>(stg);
@@ -967,27 +981,40 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                             if (lane == 0) ptx::bulk_wait_group_read<C::kEpSlots - 1>();
                             __syncwarp();
                         }
-                        ptx::tmem_wait_ld();
-                        if constexpr (EK != kEpGrad) ep_keep16(p, v, m0, n);
-                        float o[O];
-                        ep_values<EK, D, 16, O>(p, v, sc_s + j0 / D, al, bi, lane, o);
-                        if (p.dtype == SHERRY_F32) {
+#pragma unroll 1
+                        for (int part = 0; part < 16; part += S) {
+                            uint32_t v[S];
+                            if constexpr (S == 16) ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
+                            else ptx::tmem_ld_32x32b_x8(lane_base + (uint32_t)(d * BN + j0 + part), v);
+                            ptx::tmem_wait_ld();
+                            if constexpr (EK != kEpGrad) ep_keep<S>(p, v, m0 + part, n);
+                            float o[O];
+                            ep_values<EK, D, S, O>(p, v, sc_s + (j0 + part) / D, al, bi, lane, o);
+                            const int at0 = part * OW + (EK == kEpGated ? (lane & 1) * OW : 0) + scol;
+                            constexpr int kStep = EK == kEpGated ? 2 * OW : OW;
+                            if (p.dtype == SHERRY_F32) {
+                                if (has_res) {
 #pragma unroll
-                            for (int i = 0; i < O; ++i) {
-                                float* at = stg + (EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol;
-                                *at = has_res ? __fadd_rn(o[i], *at) : o[i];
-                            }
-                        } else {
+                                    for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], stg[at0 + i * kStep]);
+                                }
 #pragma unroll
-                            for (int i = 0; i < O; ++i) {
-                                uint16_t* at = st16 + (EK == kEpGated ? 2 * i + (lane & 1) : i) * OW + scol;
-                                *at = ep::to16(has_res ? __fadd_rn(o[i], ep::from16(*at, p.dtype)) : o[i], p.dtype);
+                                for (int i = 0; i < O; ++i) stg[at0 + i * kStep] = o[i];
+                            } else {
+                                if (has_res) {
+                                    uint16_t h[O];
+#pragma unroll
+                                    for (int i = 0; i < O; ++i) h[i] = st16[at0 + i * kStep];
+#pragma unroll
+                                    for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], ep::from16(h[i], p.dtype));
+                                }
+#pragma unroll
+                                for (int i = 0; i < O; ++i) st16[at0 + i * kStep] = ep::to16(o[i], p.dtype);
                             }
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            ptx::tma_store_2d(&ymap, out_x, (int32_t)m0, ptx::smem_u32(stg));
+                            ptx::tma_store_2d(&ymap.out, out_x, (int32_t)m0, ptx::smem_u32(stg));
                             ptx::bulk_commit_group();
                         }
                         if constexpr (EK == kEpLinear) {
@@ -1036,17 +1063,25 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             }
 #pragma unroll 1
             for (int j0 = 0; j0 < (via_tma ? 0 : BN); j0 += 16) {
-                uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
-                ptx::tmem_wait_ld();
                 if constexpr (EK != kEpPlain) {
                     if (complete) {
                         if ((tm * BN + j0) / D >= p.Mo) break;
-                        if constexpr (EK != kEpGrad) ep_keep16(p, v, tm * BN + j0, n);
-                        ep_store16<EK, D>(p, v, sc_s + j0 / D, al, bi, lane, (tm * BN + j0) / D, col);
+                        constexpr int S = kEpSums<EK>;
+#pragma unroll 1
+                        for (int j = j0; j < j0 + 16; j += S) {
+                            uint32_t u[S];
+                            if constexpr (S == 16) ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j), u);
+                            else ptx::tmem_ld_32x32b_x8(lane_base + (uint32_t)(d * BN + j), u);
+                            ptx::tmem_wait_ld();
+                            if constexpr (EK != kEpGrad) ep_keep<S>(p, u, tm * BN + j, n);
+                            ep_store<EK, D, S>(p, u, sc_s + j / D, al, bi, lane, (tm * BN + j) / D, col);
+                        }
                         continue;
                     }
                 }
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
+                ptx::tmem_wait_ld();
 #pragma unroll
                 for (int jj = 0; jj < 16; ++jj) {
                     const int64_t m = tm * BN + j0 + jj;
@@ -1084,26 +1119,33 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                     // trip per 16 tokens, not one per token
                     const int64_t mleft = p.M - cur_tm * BN;
                     const int jn = mleft < BN ? (int)mleft : BN;
-                    for (int j0 = 0; j0 < jn; j0 += 16) {
-                        int32_t v[16];
+                    if constexpr (EK != kEpPlain) {
+                        constexpr int S = kEpSums<EK>;
+#pragma unroll 1
+                        for (int j = 0; j < jn; j += S) {
+                            uint32_t u[S];
 #pragma unroll
-                        for (int jj = 0; jj < 16; ++jj)
-                            v[jj] = (j0 + jj < jn) ? __ldcg(wsl + (j0 + jj) * SHERRY_TILE_ROWS + r) : 0;
-                        if constexpr (EK != kEpPlain) {
-                            uint32_t u[16];
+                            for (int i = 0; i < S; ++i)
+                                u[i] = (j + i < jn) ? (uint32_t)__ldcg(wsl + (j + i) * SHERRY_TILE_ROWS + r) : 0u;
+                            if constexpr (EK != kEpGrad) ep_keep<S>(p, u, cur_tm * BN + j, n);
+                            ep_store<EK, D, S>(p, u, sc_s + j / D, al, bi, lane, (cur_tm * BN + j) / D, col);
 #pragma unroll
-                            for (int jj = 0; jj < 16; ++jj) u[jj] = (uint32_t)v[jj];
-                            if constexpr (EK != kEpGrad) ep_keep16(p, u, cur_tm * BN + j0, n);
-                            ep_store16<EK, D>(p, u, sc_s + j0 / D, al, bi, lane, (cur_tm * BN + j0) / D, col);
+                            for (int i = 0; i < S; ++i)
+                                if (j + i < jn) wsl[(j + i) * SHERRY_TILE_ROWS + r] = 0;
                         }
+                    } else {
+                        for (int j0 = 0; j0 < jn; j0 += 16) {
+                            int32_t v[16];
 #pragma unroll
-                        for (int jj = 0; jj < 16; ++jj) {
-                            const int j = j0 + jj;
-                            if (j >= jn) break;
-                            const int64_t m = cur_tm * BN + j;
-                            wsl[j * SHERRY_TILE_ROWS + r] = 0;
-                            const int32_t af = v[jj] >> C::kAccShift;
-                            if constexpr (EK == kEpPlain) {
+                            for (int jj = 0; jj < 16; ++jj)
+                                v[jj] = (j0 + jj < jn) ? __ldcg(wsl + (j0 + jj) * SHERRY_TILE_ROWS + r) : 0;
+#pragma unroll
+                            for (int jj = 0; jj < 16; ++jj) {
+                                const int j = j0 + jj;
+                                if (j >= jn) break;
+                                const int64_t m = cur_tm * BN + j;
+                                wsl[j * SHERRY_TILE_ROWS + r] = 0;
+                                const int32_t af = v[jj] >> C::kAccShift;
                                 if (n < p.N) {
                                     if (p.acc) p.acc[m * p.N + n] = af;
                                     if (p.y) p.y[m * p.N + n] = __fmul_rn(__fmul_rn((float)af, al), sc_s[j]);
