@@ -293,16 +293,21 @@ def selftest_wait(limit_ns: int, stream=None):
 
 # --------------------------------------------------- feed-forward operators
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}   # sherry_act
+_torch = None
 _DTYPES = {}            # torch dtype -> sherry_dtype, filled on first use
 _split_reserved = set()  # devices whose split-K workspace covers every call
 SPLIT_MAX_M = 1536      # from this many tokens on the split-K workspace no longer grows
 
 
-def _ffn_types():
-    import torch
-    if not _DTYPES:
+def _types():
+    """Imports torch on first use: sherry_dtype by torch dtype."""
+    global _torch
+    if _torch is None:
+        import torch
+        load()
         _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    return torch, _DTYPES
+        _torch = torch
+    return _DTYPES
 
 
 def _need(ok: bool, what: str):
@@ -310,11 +315,27 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _check_tensor(t, name: str, dtype, shape, device):
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: want contiguous {dtype} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}, strides {tuple(t.stride())}")
+def _refuse(name: str, t, want: str):
+    raise ValueError(f"{name}: want a contiguous CUDA tensor {want}, got {t.dtype} {tuple(t.shape)} on {t.device}, "
+                     f"strides {tuple(t.stride())}")
+
+
+def _ptr(t, name: str, dtype, shape, idx: int):
+    """Data pointer of a tensor argument of the given type and shape on device idx (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
+        _refuse(name, t, f"{dtype} {shape} on cuda:{idx}")
     return t.data_ptr()
+
+
+def _matrix(t, name: str):
+    """Shape, sherry_dtype and device index of the [M][.] tensor a feed-forward call starts from."""
+    code = _types().get(t.dtype)
+    shape = t.shape
+    if code is None or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
+        _refuse(name, t, "[M][.] of float32, bfloat16 or float16")
+    return shape[0], shape[1], code, t.get_device()
 
 
 def _activation(act) -> int:
@@ -324,14 +345,8 @@ def _activation(act) -> int:
     return a
 
 
-def _matrix(t, name: str, types):
-    """Shape and sherry_dtype of a [M][.] tensor of a feed-forward call."""
-    code = types.get(t.dtype)
-    shape = t.shape
-    if code is None or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: want a contiguous 2-D CUDA tensor of float32, bfloat16 or float16, got {t.dtype} "
-                         f"{tuple(shape)} on {t.device}, strides {tuple(t.stride())}")
-    return shape[0], shape[1], code
+def _stream_of(idx: int):
+    return _torch._C._cuda_getCurrentRawStream(idx)
 
 
 def _on_device(fn):
@@ -346,27 +361,19 @@ def _on_device(fn):
     return call
 
 
-def _ensure_split(t):
-    """Sets aside the whole split-K workspace (about 15 MB, once per device), so that it never moves
-    under a captured graph."""
-    import torch
-    idx = t.device.index
+def reserve_split(device=None):
+    """Sets aside, host-synchronously, the split-K workspace (about 15 MB) of every linear_epilogue, gated
+    and gradient call on `device` (default: the current one).  The first such call does it too; do it
+    before capturing a graph."""
+    _types()
+    dev = _torch.device("cuda" if device is None else device) if not isinstance(device, int) else \
+        _torch.device("cuda", device)
+    idx = dev.index if dev.index is not None else _torch.cuda.current_device()
     if idx in _split_reserved:
         return
-    if torch.cuda.is_current_stream_capturing():
+    if _torch.cuda.is_current_stream_capturing():
         raise RuntimeError("the workspace is not set aside yet: call reserve_split() before capturing a graph")
-    reserve_split(idx)
-
-
-def reserve_split(device=None):
-    """Sets aside, host-synchronously, the split-K workspace of every linear_epilogue, gated and gradient
-    call on `device` (default: the current one).  The first such call does it too; do it before
-    capturing a graph."""
-    import torch
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device("cuda", device) \
-        if isinstance(device, int) else torch.device(device)
-    idx = dev.index if dev.index is not None else torch.cuda.current_device()
-    with torch.cuda.device(idx):
+    with _torch.cuda.device(idx):
         _check(load().sherry_reserve(SPLIT_MAX_M, 1), "sherry_reserve")
     _split_reserved.add(idx)
 
@@ -409,49 +416,46 @@ def repack_gated_t(gate_dev, up_dev, N: int, K: int, out=None):
 
 
 def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s):
-    torch, types = _ffn_types()
-    M, K, dt = _matrix(x, "x", types)
+    M, K, dt, idx = _matrix(x, "x")
+    if idx != _torch.cuda.current_device():
+        with _torch.cuda.device(idx):
+            return _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s)
     a = _activation(act)
-    R = 2 * N if gated else N
-    dev = x.device
     if N <= 0 or K <= 0 or K % 32:
         raise ValueError(f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
-    wp = _check_tensor(w_native, "w_native", torch.uint8, (-(-R // 128) * -(-K // 128) * 2560,), dev)
-    ap = _check_tensor(alpha, "alpha", torch.float32, (R,), dev)
-    bp = None if bias is None else _check_tensor(bias, "bias", torch.float32, (R,), dev)
-    rp = None if residual is None else _check_tensor(residual, "residual", x.dtype, (M, N), dev)
+    R = 2 * N if gated else N
+    wp = _ptr(w_native, "w_native", _torch.uint8, (-(-R // 128) * -(-K // 128) * 2560,), idx)
+    ap = _ptr(alpha, "alpha", _torch.float32, (R,), idx)
+    bp = _ptr(bias, "bias", _torch.float32, (R,), idx)
+    rp = _ptr(residual, "residual", x.dtype, (M, N), idx)
+    cp = _ptr(acc, "acc", _torch.int32, (M, R), idx)
+    qp = _ptr(out_q, "out_q", _torch.int8, (M, K), idx)
+    sp = _ptr(out_s, "out_s", _torch.float32, (M,), idx)
+    op = _ptr(out, "out", x.dtype, (M, N), idx)
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=dev)
+        out = x.new_empty((M, N))
         op = out.data_ptr()
-    else:
-        op = _check_tensor(out, "out", x.dtype, (M, N), dev)
-    cp = None if acc is None else _check_tensor(acc, "acc", torch.int32, (M, R), dev)
-    qp = None if out_q is None else _check_tensor(out_q, "out_q", torch.int8, (M, K), dev)
-    sp = None if out_s is None else _check_tensor(out_s, "out_s", torch.float32, (M,), dev)
     if M == 0:
         return out
-    if M > 1 or qp is not None:
-        # the call's own activation buffers: nothing is shared with other streams or graphs
+    if M > 1 and qp is None or qp is not None and sp is None:
+        # the call's own buffer for the int8 activations and their scales: nothing is shared with other
+        # streams or graphs
+        own = w_native.new_empty(M * K + 4 * M)         # K % 32 == 0: the scales are aligned
         if qp is None:
-            q = torch.empty((M, K), dtype=torch.int8, device=dev)
-            qp = q.data_ptr()
+            qp = own.data_ptr()
         if sp is None:
-            s = torch.empty(M, dtype=torch.float32, device=dev)
-            sp = s.data_ptr()
-    if dev.index not in _split_reserved:
-        _ensure_split(x)
-    L = _lib or load()
-    st = torch.cuda.current_stream(dev).cuda_stream
+            sp = own.data_ptr() + M * K
+    if idx not in _split_reserved:
+        reserve_split(idx)
     if gated:
-        rc = L.sherry_gated(x.data_ptr(), dt, wp, ap, bp, a, op, cp, qp, sp, M, N, K, st)
+        rc = _lib.sherry_gated(x.data_ptr(), dt, wp, ap, bp, a, op, cp, qp, sp, M, N, K, _stream_of(idx))
     else:
-        rc = L.sherry_linear_epilogue(x.data_ptr(), dt, wp, ap, bp, a, rp, op, cp, qp, sp, M, N, K, st)
+        rc = _lib.sherry_linear_epilogue(x.data_ptr(), dt, wp, ap, bp, a, rp, op, cp, qp, sp, M, N, K, _stream_of(idx))
     if rc != OK:
         _check(rc, "sherry_gated" if gated else "sherry_linear_epilogue")
     return out
 
 
-@_on_device
 def linear_epilogue(x, w_native, alpha, N: int, bias=None, act: str = "none", residual=None, out=None, acc=None,
                     out_q=None, out_s=None):
     """y [M][N] = act(linear(x) + bias) + residual in one contraction (sherry_linear_epilogue).
@@ -463,7 +467,6 @@ def linear_epilogue(x, w_native, alpha, N: int, bias=None, act: str = "none", re
     return _forward(False, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s)
 
 
-@_on_device
 def gated(x, w_native, alpha, N: int, bias=None, act: str = "silu", out=None, acc=None, out_q=None, out_s=None):
     """h [M][N] = act(gate(x)) * up(x) in one contraction (sherry_gated).
 
@@ -473,47 +476,48 @@ def gated(x, w_native, alpha, N: int, bias=None, act: str = "silu", out=None, ac
 
 
 def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales):
-    torch, types = _ffn_types()
-    M, N, dt = _matrix(dy, "dy", types)
+    M, N, dt, idx = _matrix(dy, "dy")
+    if idx != _torch.cuda.current_device():
+        with _torch.cuda.device(idx):
+            return _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales)
     a = _activation(act)
-    R = 2 * N if gated else N
-    dev = dy.device
     if N <= 0 or K <= 0 or K % 32:
         raise ValueError(f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
-    _need(want_dx or want_scales, "nothing to compute")
-    need_acc = gated or a != 0 or want_scales
-    _need(acc is not None or not need_acc, "acc: needed for this gradient")
+    _need(want_dx or want_scales, "nothing to compute: want_dx and want_scales are both False")
+    _need(acc is not None or not (gated or a != 0 or want_scales), "acc: needed for this gradient")
     _need(acc is None or x_scale is not None, "x_scale: needed with acc")
-    ap = _check_tensor(alpha, "alpha", torch.float32, (R,), dev)
-    bp = None if bias is None else _check_tensor(bias, "bias", torch.float32, (R,), dev)
-    cp = None if acc is None else _check_tensor(acc, "acc", torch.int32, (M, R), dev)
-    sp = None if x_scale is None else _check_tensor(x_scale, "x_scale", torch.float32, (M,), dev)
-    dx = wp = xp = kp = dalpha = dbias = None
+    R = 2 * N if gated else N
+    _need(alpha is not None and (w_t is not None or not want_dx), "alpha, and for dx w_t, are needed")
+    ap = _ptr(alpha, "alpha", _torch.float32, (R,), idx)
+    bp = _ptr(bias, "bias", _torch.float32, (R,), idx)
+    cp = _ptr(acc, "acc", _torch.int32, (M, R), idx)
+    sp = _ptr(x_scale, "x_scale", _torch.float32, (M,), idx)
+    dx = dalpha = dbias = wp = xp = kp = dap = dbp = None
     if want_dx:
-        wp = _check_tensor(w_t, "w_t", torch.uint8, (-(-R // 128) * -(-K // 128) * 4096,), dev)
-        dx = out if out is not None else torch.empty((M, K), dtype=dy.dtype, device=dev)
-        xp = dx.data_ptr() if out is None else _check_tensor(out, "out", dy.dtype, (M, K), dev)
+        wp = _ptr(w_t, "w_t", _torch.uint8, (-(-R // 128) * -(-K // 128) * 4096,), idx)
+        xp = _ptr(out, "out", dy.dtype, (M, K), idx)
+        dx = out
+        if dx is None:
+            dx = dy.new_empty((M, K))
+            xp = dx.data_ptr()
     if want_scales:
-        make = torch.empty if M else torch.zeros
-        dalpha = make(R, dtype=torch.float32, device=dev)
-        dbias = make(R, dtype=torch.float32, device=dev)
+        make = _torch.empty_like if M else _torch.zeros_like
+        dalpha, dbias = make(alpha), make(alpha)
+        dap, dbp = dalpha.data_ptr(), dbias.data_ptr()
     if M == 0:
         return dx, dalpha, dbias
-    L = _lib or load()
     if want_dx:
-        work = torch.empty(L.sherry_grad_work_bytes(dt, M, R), dtype=torch.uint8, device=dev)
+        work = w_t.new_empty(_lib.sherry_grad_work_bytes(dt, M, R))
         kp = work.data_ptr()
-        if dev.index not in _split_reserved:
-            _ensure_split(dy)
-    fn = L.sherry_gated_grad if gated else L.sherry_linear_grad
-    rc = fn(dy.data_ptr(), dt, cp, sp, wp, ap, bp, a, xp, None if dalpha is None else dalpha.data_ptr(),
-            None if dbias is None else dbias.data_ptr(), kp, M, N, K, torch.cuda.current_stream(dev).cuda_stream)
+        if idx not in _split_reserved:
+            reserve_split(idx)
+    fn = _lib.sherry_gated_grad if gated else _lib.sherry_linear_grad
+    rc = fn(dy.data_ptr(), dt, cp, sp, wp, ap, bp, a, xp, dap, dbp, kp, M, N, K, _stream_of(idx))
     if rc != OK:
         _check(rc, "sherry_gated_grad" if gated else "sherry_linear_grad")
     return dx, dalpha, dbias
 
 
-@_on_device
 def linear_backward(dy, w_t, alpha, K: int, acc=None, x_scale=None, bias=None, act: str = "none", out=None,
                     want_dx: bool = True, want_scales: bool = True):
     """Gradients of linear_epilogue: (dx [M][K] of dy's type, dalpha fp32 [N], dbias fp32 [N]).
@@ -525,7 +529,6 @@ def linear_backward(dy, w_t, alpha, K: int, acc=None, x_scale=None, bias=None, a
     return _backward(False, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales)
 
 
-@_on_device
 def gated_backward(dh, w_t, alpha, K: int, acc, x_scale, bias=None, act: str = "silu", out=None,
                    want_dx: bool = True, want_scales: bool = True):
     """Gradients of gated: (dx [M][K], dalpha fp32 [2N], dbias fp32 [2N], interleaved).  w_t from
