@@ -18,6 +18,7 @@
 #include "grad.cuh"
 #include "quant.cuh"
 #include "tc_gemm.cuh"
+#include "tile_plan.h"
 
 namespace sherry {
 namespace {
@@ -192,7 +193,7 @@ int make_out_map(CUtensorMap* map, void* out, int dtype, int64_t Mo, int64_t No,
 // One tensor-core launch.  b: int8 rows [p.M][p.K], ld bytes apart.  p holds
 // the problem; tiles, workspace and status are filled in here.
 template <int BN, int SC, int WF, int EK, int D>
-int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, cudaStream_t stream)
+int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan, cudaStream_t stream)
 {
     using C = tc::Cfg<BN, SC, WF>;
     DeviceInfo di;
@@ -203,10 +204,11 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, cudaStream_t stream)
     p.TN = sherry_row_tiles(p.N);
     p.Kc = sherry_k_chunks(p.K);
     p.U = p.TM * p.TN * p.Kc;
-    const int64_t grid = tc_grid(p.TM * p.TN, p.U, di.sms, p.Kc, BN);
+    const int64_t grid = plan.grid;
+    p.whole = plan.whole;
     p.ws = nullptr;
     p.counters = nullptr;
-    if ((p.TM * p.TN) % grid != 0) {
+    if (!p.whole) {
         void* ws = nullptr;
         const size_t ws_acc = (size_t)grid * BN * SHERRY_TILE_ROWS * sizeof(int32_t);
         st = get_workspace(ws_acc + (size_t)grid * sizeof(uint32_t), &ws);
@@ -242,28 +244,34 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, cudaStream_t stream)
     return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream, map, maps, p));
 }
 
-// The token tiles of sherry_gemm_tc (its measurements hold: the loads, decode
-// and MMAs are the same).
 template <int EK>
-int launch_forward_tc(const int8_t* b, const tc::EpParams& p, cudaStream_t s)
+int launch_forward_tc(const int8_t* b, const tc::EpParams& p, int sms, cudaStream_t s)
 {
     constexpr int W = tc::kWeightSherry;
-    if (p.M <= 16) return launch_tc<16, 4, W, EK, 1>(b, p.K, p, s);
-    if (p.M <= 32) return launch_tc<32, 4, W, EK, 1>(b, p.K, p, s);
-    if (p.M <= 64) return launch_tc<64, 4, W, EK, 1>(b, p.K, p, s);
-    if (p.M < 1536) return launch_tc<128, 2, W, EK, 1>(b, p.K, p, s);
-    return launch_tc<192, 1, W, EK, 1>(b, p.K, p, s);
+    const TilePlan plan = plan_tiles(p.M, sherry_row_tiles(p.N), sherry_k_chunks(p.K), sms);
+    switch (plan.bn) {
+    case 16: return launch_tc<16, 4, W, EK, 1>(b, p.K, p, plan, s);
+    case 32: return launch_tc<32, 4, W, EK, 1>(b, p.K, p, plan, s);
+    case 64: return launch_tc<64, 4, W, EK, 1>(b, p.K, p, plan, s);
+    case 128: return launch_tc<128, 2, W, EK, 1>(b, p.K, p, plan, s);
+    default: return launch_tc<192, 1, W, EK, 1>(b, p.K, p, plan, s);
+    }
 }
 
+// kWeightT2 chunks are 4 KB: two-chunk stages from 64 rows on keep at least
+// three stages in the ring.
 template <int D>
-int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, cudaStream_t s)
+int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, int sms, cudaStream_t s)
 {
     constexpr int W = tc::kWeightT2, EK = tc::kEpGrad;
-    if (p.M <= 16) return launch_tc<16, 4, W, EK, D>(b, ld, p, s);
-    if (p.M <= 32) return launch_tc<32, 4, W, EK, D>(b, ld, p, s);
-    if (p.M <= 64) return launch_tc<64, 2, W, EK, D>(b, ld, p, s);
-    if (p.M < 1536) return launch_tc<128, 2, W, EK, D>(b, ld, p, s);
-    return launch_tc<192, 1, W, EK, D>(b, ld, p, s);
+    const TilePlan plan = plan_tiles(p.M, sherry_row_tiles(p.N), sherry_k_chunks(p.K), sms);
+    switch (plan.bn) {
+    case 16: return launch_tc<16, 4, W, EK, D>(b, ld, p, plan, s);
+    case 32: return launch_tc<32, 4, W, EK, D>(b, ld, p, plan, s);
+    case 64: return launch_tc<64, 2, W, EK, D>(b, ld, p, plan, s);
+    case 128: return launch_tc<128, 2, W, EK, D>(b, ld, p, plan, s);
+    default: return launch_tc<192, 1, W, EK, D>(b, ld, p, plan, s);
+    }
 }
 
 template <int MT, bool FUSED, int RT, class XT>
@@ -371,7 +379,8 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     p.No = No;
     p.dtype = dtype;
     p.act = act;
-    return gated ? launch_forward_tc<tc::kEpGated>(x_i8, p, s) : launch_forward_tc<tc::kEpLinear>(x_i8, p, s);
+    return gated ? launch_forward_tc<tc::kEpGated>(x_i8, p, di.sms, s)
+                 : launch_forward_tc<tc::kEpLinear>(x_i8, p, di.sms, s);
 }
 
 // Row stride of the digit rows: whole 16-byte units (TMA).
@@ -436,7 +445,7 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     p.Mo = M;
     p.No = K;
     p.dtype = dtype;
-    return D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, s) : launch_grad_tc<4>(g.dig, g.ld, p, s);
+    return D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, di.sms, s) : launch_grad_tc<4>(g.dig, g.ld, p, di.sms, s);
 }
 
 int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)

@@ -86,6 +86,19 @@ __device__ __forceinline__ void load4(const T* p, int64_t left, bool vec, T (&v)
     }
 }
 
+// Sums of four rows: pairs of a gated weight are 8-byte aligned in any case.
+template <bool GATED>
+__device__ __forceinline__ void load_acc(const int32_t* p, int64_t left, bool vec, int32_t (&a)[4])
+{
+    if (!GATED || vec) {
+        load4(p, left, vec, a);
+    } else {
+        const int2 t = *reinterpret_cast<const int2*>(p);
+        const int2 u = left > 2 ? *reinterpret_cast<const int2*>(p + 2) : make_int2(0, 0);
+        a[0] = t.x; a[1] = t.y; a[2] = u.x; a[3] = u.y;
+    }
+}
+
 // C values of dy (2 or 4) from p, which has `left` of them.
 template <int DT, int C>
 __device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int64_t left, bool vec, float (&g)[C])
@@ -186,7 +199,7 @@ struct Segment {
         float g[C], dz[4];
         int32_t a[4] = {0, 0, 0, 0};
         load_dy<DT, C>(dy + C * u, cols - C * u, VEC, g);
-        if (acc) load4(acc + 4 * u, rows - 4 * u, VEC, a);
+        if (acc) load_acc<GATED>(acc + 4 * u, rows - 4 * u, VEC, a);
         const Rows4 w = load_rows<VEC>(alpha + 4 * u, bias ? bias + 4 * u : nullptr, rows - 4 * u);
         dz4<GATED, ACT, C>(a, g, w, bias != nullptr, s, dz);
 #pragma unroll
@@ -312,59 +325,78 @@ __global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params
 constexpr int kColWarps = 8;
 constexpr int kColRows = 128;                                // weight rows per block
 
-// One lane's sums over the tokens m0, m0 + step, ..: kBatch tokens' loads are
-// issued before their arithmetic, without a branch between them (past the last
-// token the first one's values are read again and count as zero).
+// One lane's sums over the tokens m0, m0 + step, ..: the loads of B tokens are
+// issued before their arithmetic, without a branch between them; advances m
+// and the pointers while B tokens are left.
+template <bool GATED, int ACT, int DT, bool VEC, bool ACC>
+struct Column {
+    static constexpr int C = GATED ? 2 : 4;
+    using E = typename Elem<DT>::type;
+    const E* dy;
+    const int32_t* acc;
+    const float* s;
+    int64_t dstep, astep, step;
+    int64_t m;                  // next token
+    int rows, cols;             // left in the arrays' rows
+    Rows4 w;
+    bool hb;
+
+    template <int B>
+    __device__ __forceinline__ void run(int64_t M, float (&sa)[4], float (&sb)[4])
+    {
+        for (; m + (B - 1) * step < M; m += B * step) {
+            float g[B][C], sc[B];
+            int32_t a[B][4];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                load_dy<DT, C>(dy, cols, VEC, g[i]);
+                dy += dstep;
+                sc[i] = 0.0f;
+                a[i][0] = a[i][1] = a[i][2] = a[i][3] = 0;
+                if constexpr (ACC) {
+                    load_acc<GATED>(acc, rows, VEC, a[i]);
+                    acc += astep;
+                    sc[i] = *s;
+                    s += step;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                float dz[4];
+                dz4<GATED, ACT, C>(a[i], g[i], w, hb, sc[i], dz);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    sa[k] = __fmaf_rn(dz[k], __fmul_rn((float)a[i][k], sc[i]), sa[k]);
+                    sb[k] = __fadd_rn(sb[k], dz[k]);
+                }
+            }
+        }
+    }
+};
+
 template <bool GATED, int ACT, int DT, bool VEC, bool ACC>
 __device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t m0, int64_t step, float (&sa)[4],
                                             float (&sb)[4])
 {
-    constexpr int C = GATED ? 2 : 4;
-    constexpr int kBatch = 4;
-    using E = typename Elem<DT>::type;
-    const bool hb = p.bias != nullptr;
-    const Rows4 w = load_rows<VEC>(p.alpha + r, hb ? p.bias + r : nullptr, p.R - r);
-    const int64_t c = GATED ? r >> 1 : r;
-    const E* dy = static_cast<const E*>(p.dy) + m0 * p.No + c;
-    const int32_t* acc = ACC ? p.acc + m0 * p.R + r : nullptr;
-    const int64_t left = p.R - r, cleft = p.No - c;
-    if (m0 >= p.M) return;
-    for (int64_t m = m0; m < p.M; m += kBatch * step) {
-        float g[kBatch][C], s[kBatch];
-        int32_t a[kBatch][4];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int64_t at = m + i * step < p.M ? m - m0 + i * step : 0;
-            load_dy<DT, C>(dy + at * p.No, cleft, VEC, g[i]);
-            s[i] = 0.0f;
-            a[i][0] = a[i][1] = a[i][2] = a[i][3] = 0;
-            if constexpr (ACC) {
-                load4(acc + at * p.R, left, VEC, a[i]);
-                s[i] = p.x_scale[m0 + at];
-            }
-        }
-#pragma unroll
-        for (int i = 1; i < kBatch; ++i)
-            if (m + i * step >= p.M) {
-#pragma unroll
-                for (int k = 0; k < C; ++k) g[i][k] = 0.0f;
-                s[i] = 0.0f;
-            }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            float dz[4];
-            dz4<GATED, ACT, C>(a[i], g[i], w, hb, s[i], dz);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sa[k] = __fmaf_rn(dz[k], __fmul_rn((float)a[i][k], s[i]), sa[k]);
-                sb[k] = __fadd_rn(sb[k], dz[k]);
-            }
-        }
-    }
+    Column<GATED, ACT, DT, VEC, ACC> c;
+    const int64_t col = GATED ? r >> 1 : r;
+    c.dy = static_cast<const typename Elem<DT>::type*>(p.dy) + m0 * p.No + col;
+    c.acc = ACC ? p.acc + m0 * p.R + r : nullptr;
+    c.s = ACC ? p.x_scale + m0 : nullptr;
+    c.step = step;
+    c.dstep = step * p.No;
+    c.astep = step * p.R;
+    c.m = m0;
+    c.rows = (int)min(p.R - r, int64_t(4));
+    c.cols = (int)min(p.No - col, int64_t(4));
+    c.hb = p.bias != nullptr;
+    c.w = load_rows<VEC>(p.alpha + r, c.hb ? p.bias + r : nullptr, p.R - r);
+    c.template run<4>(p.M, sa, sb);
+    c.template run<1>(p.M, sa, sb);
 }
 
 template <bool GATED, int ACT, int DT>
-__global__ void __launch_bounds__(32 * kColWarps) grad_columns_kernel(const Params p)
+__global__ void __launch_bounds__(32 * kColWarps, 3) grad_columns_kernel(const Params p)
 {
     __shared__ float part[kColWarps][2][kColRows];
     __shared__ float total[2][kColRows];

@@ -37,9 +37,6 @@ int make_x_map(CUtensorMap* map, const int8_t* x, int64_t M, int64_t K, int64_t 
 // The device status word of the current device.
 unsigned* device_status_ptr();
 
-// CTAs of a tensor-core launch (see the definition).
-int64_t tc_grid(int64_t T, int64_t U, int64_t sms, int64_t Kc, int bn);
-
 // Buffers set aside by sherry_reserve on the current device
 // (SHERRY_ERR_WORKSPACE when smaller than asked for): the split-K workspace,
 // and the int8 activations with their scales.

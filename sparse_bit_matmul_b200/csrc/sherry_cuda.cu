@@ -18,6 +18,7 @@
 #include "decode.cuh"
 #include "quant.cuh"
 #include "tc_gemm.cuh"
+#include "tile_plan.h"
 #include "w4a8_gemv.cuh"
 
 namespace sherry {
@@ -295,10 +296,6 @@ int get_workspace(size_t bytes, void** out)
 
 namespace {
 
-// Token tile of the tensor-core kernel for M tokens (the dispatch of
-// sherry_gemm_tc, sherry_w4a8_gemm_tc and the feed-forward entry points).
-int tc_token_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M < 1536 ? 128 : 192; }
-
 // Split-K workspace for every launch of up to M tokens on `sms` SMs: the
 // partial-sum slots of at most one CTA per SM, BN tokens x 128 rows each, and
 // one arrival counter per CTA.
@@ -370,6 +367,7 @@ int launch_tc(const int8_t* x, const float* xs, const void* wn, const float* alp
     p.TN = sherry_row_tiles(N);
     p.Kc = sherry_k_chunks(K);
     p.U = p.TM * p.TN * p.Kc;
+    p.whole = 0;
     const int64_t grid = tc_grid(p.TM * p.TN, p.U, di.sms, p.Kc, BN);
     // the workspace is touched only by tiles whose K range is split across
     // CTAs: the last T mod G tiles (none when every CTA takes whole tiles)
@@ -653,6 +651,7 @@ int launch_tc_noalloc(const int8_t* x, const float* xs, const void* wn, const fl
     p.TN = sherry_row_tiles(N);
     p.Kc = sherry_k_chunks(K);
     p.U = p.TM * p.TN * p.Kc;
+    p.whole = 0;
     const int64_t grid = std::min<int64_t>(tc_grid(p.TM * p.TN, p.U, di.sms, p.Kc, BN), kNoAllocMaxCtas);
     p.ws = scratch;
     p.counters = reinterpret_cast<uint32_t*>(scratch + kNoAllocAccWords);

@@ -185,6 +185,7 @@ struct Params {
     int64_t TM, TN, Kc;         // token tiles, row tiles, K chunks
     int64_t U;                  // total units TM*TN*Kc
     int y_tma;                  // y rows 16-byte multiples: complete tiles leave through TMA stores
+    int whole;                  // leftover tiles are not split: one each to the first CTAs
 };
 
 // Parameters of the epilogues other than kEpPlain.  kEpGrad: M counts digit
@@ -357,7 +358,9 @@ __device__ __forceinline__ void ep_store(const EpParams& p, const uint32_t (&v)[
 // that no share is empty), walked first.  Then every CTA walks F = T div G whole tiles of
 // its own.  So every CTA gets the same number of units within one, the
 // tiles summed across CTAs come first (their reductions overlap the later
-// tiles), and every CTA ends on whole tiles.  All roles walk this sequence.
+// tiles), and every CTA ends on whole tiles.  With `whole` the last R tiles
+// are not cut: each of the first R CTAs walks one of them first, and no tile is
+// summed across CTAs.  All roles walk this sequence.
 struct SegWalk {
     int64_t Kc, tile, cb, ce, end_u, r1_tile, r1_end_tile;
     int range;                                  // 0 split share, 1 own tiles, 2 done
@@ -370,7 +373,10 @@ struct SegWalk {
         r1_tile = b * F;
         r1_end_tile = (b + 1) * F;
         int64_t a0, a1;
-        if (RU >= G) {
+        if (p.whole) {
+            a0 = L0 + Kc * b;
+            a1 = b < R ? a0 + Kc : a0;
+        } else if (RU >= G) {
             a0 = L0 + RU * b / G;
             a1 = L0 + RU * (b + 1) / G;
         } else {
