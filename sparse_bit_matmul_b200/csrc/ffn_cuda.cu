@@ -261,10 +261,9 @@ int launch_forward_tc(const int8_t* b, const tc::EpParams& p, int sms, cudaStrea
 // kWeightT2 chunks are 4 KB: two-chunk stages from 64 rows on keep at least
 // three stages in the ring.
 template <int D>
-int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, int sms, cudaStream_t s)
+int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, const TilePlan& plan, cudaStream_t s)
 {
     constexpr int W = tc::kWeightT2, EK = tc::kEpGrad;
-    const TilePlan plan = plan_tiles(p.M, sherry_row_tiles(p.N), sherry_k_chunks(p.K), sms);
     switch (plan.bn) {
     case 16: return launch_tc<16, 4, W, EK, D>(b, ld, p, plan, s);
     case 32: return launch_tc<32, 4, W, EK, D>(b, ld, p, plan, s);
@@ -426,15 +425,16 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.vec = R % 4 == 0 && aligned16(dy) && aligned16(acc) && aligned16(alpha) && aligned16(bias);
     g.dalpha = dalpha;
     g.dbias = dbias;
-    if (dx) {
-        st = grad::launch_digits(g, gated, act, dtype, di.sms, s);
-        if (st != SHERRY_OK) return st;
-    }
-    if (dalpha || dbias) {
+    if (!dx) return grad::launch_columns(g, gated, act, dtype, di.sms, s);
+    const TilePlan plan = plan_tiles(M * D, sherry_row_tiles(K), sherry_k_chunks(R), di.sms);
+    const bool columns = dalpha || dbias;
+    g.beside = columns && grad::columns_beside(R, M, plan.grid, di.sms);
+    st = grad::launch_digits(g, gated, act, dtype, di.sms, s);
+    if (st != SHERRY_OK) return st;
+    if (columns && !g.beside) {
         st = grad::launch_columns(g, gated, act, dtype, di.sms, s);
         if (st != SHERRY_OK) return st;
     }
-    if (!dx) return SHERRY_OK;
     tc::EpParams p = {};
     p.wnative = static_cast<const uint8_t*>(wt);
     p.x_scale = g.dscale;
@@ -445,7 +445,9 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     p.Mo = M;
     p.No = K;
     p.dtype = dtype;
-    return D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, di.sms, s) : launch_grad_tc<4>(g.dig, g.ld, p, di.sms, s);
+    st = D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, plan, s) : launch_grad_tc<4>(g.dig, g.ld, p, plan, s);
+    if (st != SHERRY_OK || !g.beside) return st;
+    return grad::launch_columns(g, gated, act, dtype, di.sms, s);
 }
 
 int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)

@@ -44,6 +44,7 @@ struct Params {
     int vec;                    // rows and bases allow 16-byte loads of four rows' values
     float* dalpha;              // [R] or null
     float* dbias;               // [R] or null
+    int beside;                 // the column sums run beside the dx product of the same call
 };
 
 template <int DT>
@@ -76,13 +77,13 @@ template <class T>
 __device__ __forceinline__ void load4(const T* p, int64_t left, bool vec, T (&v)[4])
 {
     if (vec) {
-        const uint4 t = *reinterpret_cast<const uint4*>(p);
+        const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p));
         const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) memcpy(&v[k], &w[k], 4);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = k < left ? p[k] : T(0);
+        for (int k = 0; k < 4; ++k) v[k] = k < left ? __ldcg(p + k) : T(0);
     }
 }
 
@@ -93,8 +94,8 @@ __device__ __forceinline__ void load_acc(const int32_t* p, int64_t left, bool ve
     if (!GATED || vec) {
         load4(p, left, vec, a);
     } else {
-        const int2 t = *reinterpret_cast<const int2*>(p);
-        const int2 u = left > 2 ? *reinterpret_cast<const int2*>(p + 2) : make_int2(0, 0);
+        const int2 t = __ldcg(reinterpret_cast<const int2*>(p));
+        const int2 u = left > 2 ? __ldcg(reinterpret_cast<const int2*>(p + 2)) : make_int2(0, 0);
         a[0] = t.x; a[1] = t.y; a[2] = u.x; a[3] = u.y;
     }
 }
@@ -108,18 +109,18 @@ __device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int64_
         if constexpr (DT == SHERRY_F32) {
 #pragma unroll
             for (int k = 0; k < C; k += 2) {
-                const float2 t = *reinterpret_cast<const float2*>(p + k);
+                const float2 t = __ldcg(reinterpret_cast<const float2*>(p + k));
                 g[k] = t.x;
                 g[k + 1] = t.y;
             }
         } else {
             uint32_t t[C / 2];
             if constexpr (C == 4) {
-                const uint2 w = *reinterpret_cast<const uint2*>(p);
+                const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
                 t[0] = w.x;
                 t[1] = w.y;
             } else {
-                t[0] = *reinterpret_cast<const uint32_t*>(p);
+                t[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
             }
 #pragma unroll
             for (int k = 0; k < C / 2; ++k) {
@@ -129,7 +130,7 @@ __device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int64_
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < C; ++k) g[k] = k < left ? widen<DT>(p[k]) : 0.0f;
+        for (int k = 0; k < C; ++k) g[k] = k < left ? widen<DT>(__ldcg(p + k)) : 0.0f;
     }
 }
 
@@ -322,7 +323,18 @@ __global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params
 // Column sums: a block owns the rows of 32 lanes x 4 weight rows, its warps
 // (and the blocks of its cluster, which share the columns) take the tokens in
 // turn, and the partial sums meet in a fixed order.
-constexpr int kColWarps = 8;
+// With `beside` the kernel is launched behind the dx product and does not wait
+// for it: every block of the product lets it start only after its own wait, so
+// the digits kernel and all before it are complete, and what this kernel reads
+// (through L2) and overwrites is free.  Its first block waits for the product
+// at its end, so that the kernel's completion still means all of the call's.
+// Used where the SMs without a CTA of the product hold all of its blocks (M=129
+// 4096x4096 f32: 23.6 -> 19.4 us for the call) or a warp has at most eight
+// tokens (M=5 K=1024, gated to 2816, bf16: 13.6 -> 11.4 us); longer ones on the
+// same SMs slow the product by more than they save (M=2048 K=14336 N=4096: 197
+// -> 211 us), and run before it instead.
+constexpr int kColWarps = 4;
+constexpr int kColBlocks = 6;                                // resident per SM (registers)
 constexpr int kColRows = 128;                                // weight rows per block
 
 // One lane's sums over the tokens m0, m0 + step, ..: the loads of B tokens are
@@ -356,7 +368,7 @@ struct Column {
                 if constexpr (ACC) {
                     load_acc<GATED>(acc, rows, VEC, a[i]);
                     acc += astep;
-                    sc[i] = *s;
+                    sc[i] = __ldcg(s);
                     s += step;
                 }
             }
@@ -391,17 +403,18 @@ __device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t 
     c.cols = (int)min(p.No - col, int64_t(4));
     c.hb = p.bias != nullptr;
     c.w = load_rows<VEC>(p.alpha + r, c.hb ? p.bias + r : nullptr, p.R - r);
-    c.template run<4>(p.M, sa, sb);
+    constexpr int kBatch = GATED ? 4 : 3;                    // what 80 registers hold
+    c.template run<kBatch>(p.M, sa, sb);
     c.template run<1>(p.M, sa, sb);
 }
 
 template <bool GATED, int ACT, int DT>
-__global__ void __launch_bounds__(32 * kColWarps, 3) grad_columns_kernel(const Params p)
+__global__ void __launch_bounds__(32 * kColWarps, kColBlocks) grad_columns_kernel(const Params p)
 {
     __shared__ float part[kColWarps][2][kColRows];
     __shared__ float total[2][kColRows];
     ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
+    if (!p.beside) ptx::pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t CY = gridDim.y, rank = blockIdx.y;
     const int64_t r = (int64_t)blockIdx.x * kColRows + 4 * lane;
@@ -422,28 +435,40 @@ __global__ void __launch_bounds__(32 * kColWarps, 3) grad_columns_kernel(const P
     *reinterpret_cast<float4*>(&part[warp][0][4 * lane]) = make_float4(sa[0], sa[1], sa[2], sa[3]);
     *reinterpret_cast<float4*>(&part[warp][1][4 * lane]) = make_float4(sb[0], sb[1], sb[2], sb[3]);
     __syncthreads();
-    static_assert(32 * kColWarps == 2 * kColRows, "one thread per sum");
-    const int which = threadIdx.x / kColRows, i = threadIdx.x % kColRows;
-    float t = 0.0f;
+    static_assert(32 * kColWarps == kColRows, "one thread per row");
+    const int i = threadIdx.x;
+    float t[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < kColWarps; ++w) t = __fadd_rn(t, part[w][which][i]);
+    for (int w = 0; w < kColWarps; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) t[k] = __fadd_rn(t[k], part[w][k][i]);
     if (CY > 1) {
-        total[which][i] = t;
+        total[0][i] = t[0];
+        total[1][i] = t[1];
         ptx::cluster_arrive_release();
         ptx::cluster_wait_acquire();
         if (rank == 0)
-            for (uint32_t y = 1; y < CY; ++y) t = __fadd_rn(t, ptx::ld_cluster_f32(ptx::smem_u32(&total[which][i]), y));
+            for (uint32_t y = 1; y < CY; ++y)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    t[k] = __fadd_rn(t[k], ptx::ld_cluster_f32(ptx::smem_u32(&total[k][i]), y));
         ptx::cluster_arrive_release();                       // the sums stay readable until read
         ptx::cluster_wait_acquire();
-        if (rank != 0) return;
     }
     const int64_t n = (int64_t)blockIdx.x * kColRows + i;
-    float* out = which ? p.dbias : p.dalpha;
-    if (out && n < p.R) out[n] = t;
+    if (rank == 0 && n < p.R) {
+        if (p.dalpha) p.dalpha[n] = t[0];
+        if (p.dbias) p.dbias[n] = t[1];
+    }
+    // one block's wait keeps the grid from completing before the product; the
+    // others leave their places to the blocks behind them
+    if (p.beside && blockIdx.x == 0 && rank == 0) ptx::pdl_wait();
 }
 
 // Host: the two launches of a gradient call (grad_cuda.cu).
 int launch_digits(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream);
+// Whether the column sums of a call run beside its product of `ctas` CTAs.
+bool columns_beside(int64_t R, int64_t M, int64_t ctas, int sms);
 int launch_columns(const Params& p, bool gated, int act, int dtype, int sms, cudaStream_t stream);
 
 }  // namespace grad

@@ -17,6 +17,8 @@ constexpr int kSegMin = 1024;               // weight rows worth a block of thei
 constexpr int kSegMax = 8192;               // above, a block's 32 KB keep its neighbours off the SM
 constexpr int kClusterMax = 8;
 
+int columns_cluster(int64_t R, int64_t M, int sms);
+
 template <class K>
 cudaError_t launch_cluster(K kernel, dim3 grid, dim3 cluster, int threads, size_t smem, cudaStream_t stream,
                            const Params& p)
@@ -75,28 +77,7 @@ template <bool GATED, int ACT, int DT>
 int columns(const Params& p, int sms, cudaStream_t stream)
 {
     const int64_t bx = (p.R + kColRows - 1) / kColRows;
-    // Blocks that share the columns: of the cluster sizes that leave every
-    // warp four tokens, the one whose last round of resident blocks is
-    // fullest; the smallest such.
-    static std::atomic<int> resident{0};
-    int occ = resident.load(std::memory_order_relaxed);
-    if (occ == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, grad_columns_kernel<GATED, ACT, DT>, 32 * kColWarps, 0) !=
-                cudaSuccess || occ < 1)
-            return SHERRY_ERR_CUDA;
-        resident.store(occ, std::memory_order_relaxed);
-    }
-    const int64_t slots = (int64_t)occ * sms;
-    int cy = 1;
-    double best = 0.0;
-    for (int y = 1; y <= kClusterMax && (y == 1 || p.M >= (int64_t)y * kColWarps * 4); ++y) {
-        const int64_t blocks = bx * y, rounds = (blocks + slots - 1) / slots;
-        const double full = (double)blocks / (double)(rounds * slots);
-        if (full > best + 0.02) {
-            best = full;
-            cy = y;
-        }
-    }
+    const int cy = columns_cluster(p.R, p.M, sms);
     return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT>, dim3((unsigned)bx, (unsigned)cy),
                                       dim3(1, (unsigned)cy), 32 * kColWarps, 0, stream, p));
 }
@@ -122,7 +103,32 @@ int of_act(bool dig, const Params& p, int act, int dtype, int sms, cudaStream_t 
     }
 }
 
+// Blocks that share the columns: of the cluster sizes that leave every warp
+// four tokens, the one whose last round of resident blocks is fullest; the
+// smallest such.
+int columns_cluster(int64_t R, int64_t M, int sms)
+{
+    const int64_t bx = (R + kColRows - 1) / kColRows, slots = (int64_t)kColBlocks * sms;
+    int cy = 1;
+    double best = 0.0;
+    for (int y = 1; y <= kClusterMax && (y == 1 || M >= (int64_t)y * kColWarps * 4); ++y) {
+        const int64_t blocks = bx * y, rounds = (blocks + slots - 1) / slots;
+        const double full = (double)blocks / (double)(rounds * slots);
+        if (full > best + 0.02) {
+            best = full;
+            cy = y;
+        }
+    }
+    return cy;
+}
+
 }  // namespace
+
+bool columns_beside(int64_t R, int64_t M, int64_t ctas, int sms)
+{
+    if (M <= 8 * kColWarps) return true;
+    return (R + kColRows - 1) / kColRows * columns_cluster(R, M, sms) <= kColBlocks * (sms - ctas);
+}
 
 int launch_digits(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream)
 {

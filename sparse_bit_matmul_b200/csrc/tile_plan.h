@@ -59,8 +59,10 @@ inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms)
         } else {
             if (T % sms == 0) continue;
             grid = sms;
-            const double after = tile * (double)(T / sms);   // whole tiles behind the sums hide part of them
-            split = tile * (double)T / (double)sms + e + std::max(0.0, sums - after / 8.0);
+            // the sums hold up the epilogue warps; only a long tile behind
+            // them hides that (all of it from about 60 us on)
+            const double shown = std::min(1.0, std::max(0.0, 1.0 - (tile - 15.0) / 45.0));
+            split = tile * (double)T / (double)sms + e + sums * shown;
         }
         if (split < best_us) {
             best_us = split;
