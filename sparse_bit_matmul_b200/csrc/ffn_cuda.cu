@@ -192,10 +192,10 @@ int make_out_map(CUtensorMap* map, void* out, int dtype, int64_t Mo, int64_t No,
 
 // One tensor-core launch.  b: int8 rows [p.M][p.K], ld bytes apart.  p holds
 // the problem; tiles, workspace and status are filled in here.
-template <int BN, int SC, int WF, int EK, int D>
+template <int BN, int SC, int WF, int EK, int D, int EG = 1>
 int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan, cudaStream_t stream)
 {
-    using C = tc::Cfg<BN, SC, WF>;
+    using C = tc::Cfg<BN, SC, WF, EG>;
     DeviceInfo di;
     int st = device_info(&di);
     if (st != SHERRY_OK) return st;
@@ -235,7 +235,7 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
 
     const int smem = std::max(C::kSmemBytes, 120 * 1024);    // one CTA per SM
     if (smem > di.max_smem_optin) return SHERRY_ERR_DEVICE;
-    auto kernel = tc::sherry_gemm_tc_kernel<BN, SC, WF, EK, D>;
+    auto kernel = tc::sherry_gemm_tc_kernel<BN, SC, WF, EK, D, EG>;
     static std::atomic<uint64_t> done{0};
     st = once_per_device(done, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -244,11 +244,26 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
     return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream, map, maps, p));
 }
 
+// Weight of an epilogue for plan_tiles, beside a bare linear layer's: the
+// activation's instructions, the residual, fp32 stores, kept sums.
+double epilogue_weight(const tc::EpParams& p, bool gated)
+{
+    const double act = p.act == SHERRY_ACT_NONE                                  ? 0.0
+                       : p.act == SHERRY_ACT_RELU || p.act == SHERRY_ACT_RELU2   ? 0.1
+                       : p.act == SHERRY_ACT_GELU                                ? 0.7
+                                                                                 : 0.55;
+    const double w = 1.0 + act + (p.res ? 0.5 : 0.0) + (p.dtype == SHERRY_F32 ? 0.3 : 0.0) + (p.acc ? 0.4 : 0.0);
+    return gated ? 0.55 * w : w;
+}
+
 template <int EK>
 int launch_forward_tc(const int8_t* b, const tc::EpParams& p, int sms, cudaStream_t s)
 {
     constexpr int W = tc::kWeightSherry;
-    const TilePlan plan = plan_tiles(p.M, sherry_row_tiles(p.N), sherry_k_chunks(p.K), sms);
+    const TilePlan plan = plan_tiles(p.M, sherry_row_tiles(p.N), sherry_k_chunks(p.K), sms,
+                                     epilogue_weight(p, EK == tc::kEpGated), false);
+    if (plan.eg == 2) return plan.bn == 64 ? launch_tc<64, 4, W, EK, 1, 2>(b, p.K, p, plan, s)
+                                           : launch_tc<128, 2, W, EK, 1, 2>(b, p.K, p, plan, s);
     switch (plan.bn) {
     case 16: return launch_tc<16, 4, W, EK, 1>(b, p.K, p, plan, s);
     case 32: return launch_tc<32, 4, W, EK, 1>(b, p.K, p, plan, s);
@@ -264,6 +279,7 @@ template <int D>
 int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, const TilePlan& plan, cudaStream_t s)
 {
     constexpr int W = tc::kWeightT2, EK = tc::kEpGrad;
+    if (plan.eg == 2) return launch_tc<192, 1, W, EK, D, 2>(b, ld, p, plan, s);
     switch (plan.bn) {
     case 16: return launch_tc<16, 4, W, EK, D>(b, ld, p, plan, s);
     case 32: return launch_tc<32, 4, W, EK, D>(b, ld, p, plan, s);
@@ -426,7 +442,7 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.dalpha = dalpha;
     g.dbias = dbias;
     if (!dx) return grad::launch_columns(g, gated, act, dtype, di.sms, s);
-    const TilePlan plan = plan_tiles(M * D, sherry_row_tiles(K), sherry_k_chunks(R), di.sms);
+    const TilePlan plan = plan_tiles(M * D, sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true);
     const bool columns = dalpha || dbias;
     g.beside = columns && grad::columns_beside(R, M, plan.grid, di.sms);
     st = grad::launch_digits(g, gated, act, dtype, di.sms, s);

@@ -335,6 +335,9 @@ __global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params
 // -> 211 us), and run before it instead.
 constexpr int kColWarps = 4;
 constexpr int kColBlocks = 6;                                // resident per SM (registers)
+// Many tokens and so few rows that clusters of eight blocks leave SMs idle:
+// blocks of 16 warps.
+constexpr int kColWarpsWide = 16;
 constexpr int kColRows = 128;                                // weight rows per block
 
 // One lane's sums over the tokens m0, m0 + step, ..: the loads of B tokens are
@@ -408,10 +411,11 @@ __device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t 
     c.template run<1>(p.M, sa, sb);
 }
 
-template <bool GATED, int ACT, int DT>
-__global__ void __launch_bounds__(32 * kColWarps, kColBlocks) grad_columns_kernel(const Params p)
+template <bool GATED, int ACT, int DT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 1)
+    grad_columns_kernel(const Params p)
 {
-    __shared__ float part[kColWarps][2][kColRows];
+    __shared__ float part[WARPS][2][kColRows];
     __shared__ float total[2][kColRows];
     ptx::pdl_launch_dependents();
     if (!p.beside) ptx::pdl_wait();
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(32 * kColWarps, kColBlocks) grad_columns_kerne
     const int64_t r = (int64_t)blockIdx.x * kColRows + 4 * lane;
     float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (r < p.R) {
-        const int64_t m0 = (int64_t)rank * kColWarps + warp, step = (int64_t)CY * kColWarps;
+        const int64_t m0 = (int64_t)rank * WARPS + warp, step = (int64_t)CY * WARPS;
         if constexpr (!GATED && ACT == SHERRY_ACT_NONE) {
             if (!p.acc) {                                    // dbias alone
                 if (p.vec) column_sums<GATED, ACT, DT, true, false>(p, r, m0, step, sa, sb);
@@ -435,19 +439,24 @@ __global__ void __launch_bounds__(32 * kColWarps, kColBlocks) grad_columns_kerne
     *reinterpret_cast<float4*>(&part[warp][0][4 * lane]) = make_float4(sa[0], sa[1], sa[2], sa[3]);
     *reinterpret_cast<float4*>(&part[warp][1][4 * lane]) = make_float4(sb[0], sb[1], sb[2], sb[3]);
     __syncthreads();
-    static_assert(32 * kColWarps == kColRows, "one thread per row");
+    static_assert(32 * WARPS >= kColRows, "one thread per row");
     const int i = threadIdx.x;
+    const bool mine = i < kColRows;
     float t[2] = {0.0f, 0.0f};
+    if (mine) {
 #pragma unroll
-    for (int w = 0; w < kColWarps; ++w)
+        for (int w = 0; w < WARPS; ++w)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) t[k] = __fadd_rn(t[k], part[w][k][i]);
+            for (int k = 0; k < 2; ++k) t[k] = __fadd_rn(t[k], part[w][k][i]);
+    }
     if (CY > 1) {
-        total[0][i] = t[0];
-        total[1][i] = t[1];
+        if (mine) {
+            total[0][i] = t[0];
+            total[1][i] = t[1];
+        }
         ptx::cluster_arrive_release();
         ptx::cluster_wait_acquire();
-        if (rank == 0)
+        if (rank == 0 && mine)
             for (uint32_t y = 1; y < CY; ++y)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(32 * kColWarps, kColBlocks) grad_columns_kerne
         ptx::cluster_wait_acquire();
     }
     const int64_t n = (int64_t)blockIdx.x * kColRows + i;
-    if (rank == 0 && n < p.R) {
+    if (rank == 0 && mine && n < p.R) {
         if (p.dalpha) p.dalpha[n] = t[0];
         if (p.dbias) p.dbias[n] = t[1];
     }

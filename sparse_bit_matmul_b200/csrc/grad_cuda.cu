@@ -19,6 +19,11 @@ constexpr int kClusterMax = 8;
 
 int columns_cluster(int64_t R, int64_t M, int sms);
 
+bool columns_wide(int64_t R, int64_t M, int sms)
+{
+    return M >= 4 * kColWarpsWide * 2 && (R + kColRows - 1) / kColRows * kClusterMax < sms;
+}
+
 template <class K>
 cudaError_t launch_cluster(K kernel, dim3 grid, dim3 cluster, int threads, size_t smem, cudaStream_t stream,
                            const Params& p)
@@ -76,10 +81,15 @@ int digits(Params p, int sms, cudaStream_t stream)
 template <bool GATED, int ACT, int DT>
 int columns(const Params& p, int sms, cudaStream_t stream)
 {
-    const int64_t bx = (p.R + kColRows - 1) / kColRows;
-    const int cy = columns_cluster(p.R, p.M, sms);
-    return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT>, dim3((unsigned)bx, (unsigned)cy),
-                                      dim3(1, (unsigned)cy), 32 * kColWarps, 0, stream, p));
+    const unsigned bx = (unsigned)((p.R + kColRows - 1) / kColRows);
+    if (columns_wide(p.R, p.M, sms)) {
+        const unsigned cy = (unsigned)std::min<int64_t>(kClusterMax, p.M / (4 * kColWarpsWide));
+        return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarpsWide>, dim3(bx, cy), dim3(1, cy),
+                                          32 * kColWarpsWide, 0, stream, p));
+    }
+    const unsigned cy = (unsigned)columns_cluster(p.R, p.M, sms);
+    return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarps>, dim3(bx, cy), dim3(1, cy),
+                                      32 * kColWarps, 0, stream, p));
 }
 
 template <bool GATED, int ACT>
@@ -127,6 +137,7 @@ int columns_cluster(int64_t R, int64_t M, int sms)
 bool columns_beside(int64_t R, int64_t M, int64_t ctas, int sms)
 {
     if (M <= 8 * kColWarps) return true;
+    if (columns_wide(R, M, sms)) return false;
     return (R + kColRows - 1) / kColRows * columns_cluster(R, M, sms) <= kColBlocks * (sms - ctas);
 }
 

@@ -33,7 +33,7 @@
 // so that the fixed cost of a stage's barriers is paid once per SC chunks.
 //
 // Warp roles (576 threads; 448 for 192-token tiles with two-chunk stages,
-// which have two decoder groups):
+// which have two decoder groups; EG = 2 has eight epilogue warps from warp 10):
 //   warp 0       producer: per stage one bulk copy of the codes (completing
 //                the stage's code barrier, which the decoders wait for) and
 //                one 2D TMA of the activation tile per chunk (completing its
@@ -98,16 +98,20 @@ constexpr int kEpLinear = 1;         // + bias, activation, residual; any elemen
 constexpr int kEpGated = 2;          // rows 2n, 2n + 1: act(z[2n]) * z[2n + 1]
 constexpr int kEpGrad = 3;           // joins the digits of fixed-point gradients
 
-template <int BN, int SC, int WF = kWeightSherry>
+// EG = 2: two epilogue groups take the segments in turn (each keeps to one of
+// the two accumulators), in place of the third decoder group.  For tiles of
+// few chunks, whose time is the epilogue's.
+template <int BN, int SC, int WF = kWeightSherry, int EG = 1>
 struct Cfg {
     static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128 || BN == 192, "BN");
     // 192-token tiles: two 192-column accumulators leave 128 TMEM columns:
     // four one-chunk A slots (SC = 1, three decoder groups, the form used)
     // or two two-chunk slots (SC = 2, then only two groups: the rings must be
     // at least as deep as the number of groups)
-    static constexpr int kDecGroups = (BN == 192 && SC == 2) ? 2 : 3;
+    static constexpr int kDecGroups = (BN == 192 && SC == 2) || EG == 2 ? 2 : 3;
     static constexpr int kEpiWarp0 = kDecWarp0 + 4 * kDecGroups;
-    static constexpr int kThreads = 32 * (kEpiWarp0 + 4);
+    static constexpr int kThreads = 32 * (kEpiWarp0 + 4 * EG);
+    static_assert(EG == 1 || EG == 2, "EG");
     static_assert(SC >= 1 && SC <= 4, "SC");
     static_assert(WF == kWeightSherry || WF == kWeightInt4 || WF == kWeightT2, "WF");
     // weight bytes of one (row tile, K chunk) block
@@ -120,7 +124,11 @@ struct Cfg {
     static constexpr int kBStageBytes = SC * kBChunkBytes;
     static constexpr int kCodeStageBytes = SC * kChunkWBytes;
     static constexpr int kStageBytes = kBStageBytes + kCodeStageBytes;
-    static constexpr int kStagesRaw = (192 * 1024) / kStageBytes;
+    // output staging for TMA stores, per epilogue group: per warp two slices of
+    // [kSlice tokens][32 rows] fp32
+    static constexpr int kSlice = BN < 32 ? BN : 32;
+    static constexpr int kStagingBytes = 4 * 2 * kSlice * 32 * 4;
+    static constexpr int kStagesRaw = (192 * 1024 - (EG - 1) * (kStagingBytes + 4096)) / kStageBytes;
     static constexpr int kStagesCap = kStagesRaw > 12 ? 12 : kStagesRaw;
     // A whole number of rounds of decoder groups: stage s is then always
     // decoded by group s mod kDecGroups (see the ring rules below).
@@ -153,16 +161,13 @@ struct Cfg {
     static constexpr int kOffBars = kOffCodes + kStages * kCodeStageBytes;
     static constexpr int kNumBars = 3 * kStages + 2 * kAStages + 2 * kDBufs + 1;
     static constexpr int kOffMisc = kOffBars + 8 * kNumBars;
-    static constexpr int kMiscBytes = 64 + 2 * BN * 4;   // tmem holder, flags, token scales [2][BN]
-    // output staging for TMA stores: per epilogue warp two slices of
-    // [kSlice tokens][32 rows] fp32
-    static constexpr int kSlice = BN < 32 ? BN : 32;
+    static constexpr int kMiscBytes = 64 + EG * 2 * BN * 4;   // tmem holder, flags, token scales [EG][2][BN]
     static constexpr int kOffStaging = (kOffMisc + kMiscBytes + 127) & ~127;
-    static constexpr int kStagingBytes = 4 * 2 * kSlice * 32 * 4;
+    static_assert(EG == 1 || kDBufs == 2, "one accumulator per epilogue group");
     // the other epilogues cut a warp's staging into slots of 16 sums x 32
     // rows: two at BN = 16 (one slice a tile), else four
     static constexpr int kEpSlots = kStagingBytes / (4 * 16 * 32 * 4);
-    static constexpr int kSmemBytes = kOffStaging + kStagingBytes + 1024;   // + alignment slack
+    static constexpr int kSmemBytes = kOffStaging + EG * kStagingBytes + 1024;   // + alignment slack
     // dynamic plus static (the table of the code path, 1 KB as compiled)
     // within the 227 KB per-block limit
     static_assert(kSmemBytes + (WF == kWeightSherry ? 1024 : 0) <= 232448, "shared memory");
@@ -458,17 +463,18 @@ __device__ __forceinline__ void report(unsigned* status, volatile int* abort_fla
     *abort_flag = 1;
 }
 
-template <int BN, int SC, int WF = kWeightSherry, int EK = kEpPlain, int D = 1>
-__global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
+template <int BN, int SC, int WF = kWeightSherry, int EK = kEpPlain, int D = 1, int EG = 1>
+__global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
     sherry_gemm_tc_kernel(const __grid_constant__ CUtensorMap xmap,
                           const __grid_constant__ typename ParamsOf<EK>::maps ymap,
                           const typename ParamsOf<EK>::type p)
 {
-    using C = Cfg<BN, SC, WF>;
+    using C = Cfg<BN, SC, WF, EG>;
+    static_assert(EK != kEpPlain || EG == 1, "EG");
     static_assert(EK == kEpGrad ? 16 % D == 0 : D == 1, "digits per token");
     // kEpLinear: a barrier per staging slot of each epilogue warp, for the
     // residual boxes loaded into it
-    __shared__ __align__(8) uint64_t res_bars[EK == kEpLinear ? 4 * C::kEpSlots : 1];
+    __shared__ __align__(8) uint64_t res_bars[EK == kEpLinear ? EG * 4 * C::kEpSlots : 1];
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(128) uint32_t table[32];
     // 1024-byte aligned start, computed by pointer arithmetic so that the
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
         }
         ptx::mbar_init(drain_bar, 1);
         if constexpr (EK == kEpLinear)
-            for (int i = 0; i < 4 * C::kEpSlots; ++i) ptx::mbar_init(ptx::smem_u32(&res_bars[i]), 1);
+            for (int i = 0; i < EG * 4 * C::kEpSlots; ++i) ptx::mbar_init(ptx::smem_u32(&res_bars[i]), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -867,19 +873,27 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
         const int quad = warp & 3;
         const int r = quad * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-        const int etid = threadIdx.x - C::kEpiWarp0 * 32;     // 0..127
-        int64_t seg = 0;
-        int d = 0;
+        const int grp = EG == 1 ? 0 : (warp - C::kEpiWarp0) / 4;
+        const int etid = (threadIdx.x - C::kEpiWarp0 * 32) & 127;
+        const uint32_t ebar = 1u + (uint32_t)grp;   // the group's named barrier
+        int64_t seg = 0;                           // this group's segments so far
+        int d = grp;
         uint32_t dph = 0;
         uint32_t stage_slice = 0;                  // output slices staged so far
         [[maybe_unused]] uint32_t res_phase = 0;   // parity of each slot's residual barrier
         [[maybe_unused]] bool res_ok = true;
         [[maybe_unused]] const uint32_t res_bar0 =
-            ptx::smem_u32(&res_bars[EK == kEpLinear ? quad * C::kEpSlots : 0]);
+            ptx::smem_u32(&res_bars[EK == kEpLinear ? (4 * grp + quad) * C::kEpSlots : 0]);
         [[maybe_unused]] float* const stg_w =
-            reinterpret_cast<float*>(smem + C::kOffStaging) + quad * (C::kEpSlots * 16 * 32);
+            reinterpret_cast<float*>(smem + C::kOffStaging) + (4 * grp + quad) * (C::kEpSlots * 16 * 32);
         SegWalk w(p, blockIdx.x, G);
+        [[maybe_unused]] int turn = 0;             // segment index modulo EG
         for (; !w.done(); w.next()) {
+            if constexpr (EG > 1) {
+                const bool mine = turn == grp;
+                turn = (turn + 1 == EG) ? 0 : turn + 1;
+                if (!mine) continue;
+            }
             const int64_t tile = w.tile;
             const int64_t tm = tile / p.TN, tn = tile - tm * p.TN;
             const int64_t n = tn * SHERRY_TILE_ROWS + r;
@@ -887,7 +901,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             // the tile's token scales and this row's alpha do not depend on
             // the MMAs: fetch them into shared memory (double-buffered by
             // segment) before waiting for the accumulators
-            float* sc_s = reinterpret_cast<float*>(smem + C::kOffMisc + 64) + (seg & 1) * BN;
+            float* sc_s = reinterpret_cast<float*>(smem + C::kOffMisc + 64) + (2 * grp + (int)(seg & 1)) * BN;
             int64_t Mo = p.M;                          // scales: one per token
             if constexpr (EK != kEpPlain) Mo = p.Mo;
             for (int i = etid; i < BN / D; i += 128) {
@@ -931,7 +945,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             // every epilogue thread waits; the AND over the 128 of them makes
             // the leave-or-stay decision uniform
             bool ok = !*abort_flag && ptx::mbar_wait_bounded(dfull_bar(d), dph, kWaitLimitNs);
-            ok = ptx::named_bar_and(1, 128, ok);
+            ok = ptx::named_bar_and(ebar, 128, ok);
             if (!ok) {
                 if (etid == 0) report(p.status, abort_flag, SHERRY_DEV_TIMEOUT_EPILOGUE);
                 if constexpr (EK == kEpLinear) {
@@ -996,7 +1010,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                             uint32_t v[S];
                             if constexpr (S == 16) ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
                             else ptx::tmem_ld_32x32b_x8(lane_base + (uint32_t)(d * BN + j0 + part), v);
-                            ptx::tmem_wait_ld();
+                            ptx::tmem_wait_ld_of(v);
                             if constexpr (EK != kEpGrad) ep_keep<S>(p, v, m0 + part, n);
                             float o[O];
                             ep_values<EK, D, S, O>(p, v, sc_s + (j0 + part) / D, al, bi, lane, o);
@@ -1082,7 +1096,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                             uint32_t u[S];
                             if constexpr (S == 16) ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j), u);
                             else ptx::tmem_ld_32x32b_x8(lane_base + (uint32_t)(d * BN + j), u);
-                            ptx::tmem_wait_ld();
+                            ptx::tmem_wait_ld_of(u);
                             if constexpr (EK != kEpGrad) ep_keep<S>(p, u, tm * BN + j, n);
                             ep_store<EK, D, S>(p, u, sc_s + j / D, al, bi, lane, (tm * BN + j) / D, col);
                         }
@@ -1112,18 +1126,23 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(dempty_bar(d));
             ++seg;
-            if (++d == C::kDBufs) { d = 0; dph ^= 1u; }
+            if constexpr (EG > 1) {
+                dph ^= 1u;                             // the group keeps its accumulator
+            } else if (++d == C::kDBufs) {
+                d = 0;
+                dph ^= 1u;
+            }
             const int64_t cur_tm = tm;
             if (!complete) {
                 __threadfence();
-                ptx::named_bar_sync(1, 128);
+                ptx::named_bar_sync(ebar, 128);
                 if (etid == 0) {
                     const uint32_t old = atomicAdd(p.counters + slot, 1u);
-                    *last_flag = (old == (uint32_t)(nparts - 1)) ? 1 : 0;
+                    last_flag[grp] = (old == (uint32_t)(nparts - 1)) ? 1 : 0;
                 }
                 __syncwarp();
-                ptx::named_bar_sync(1, 128);
-                if (*last_flag) {
+                ptx::named_bar_sync(ebar, 128);
+                if (last_flag[grp]) {
                     __threadfence();
                     // 16 independent L2 loads in flight per batch: one round
                     // trip per 16 tokens, not one per token
@@ -1166,7 +1185,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF>::kThreads, 1)
                     if (etid == 0) atomicExch(p.counters + slot, 0u);
                 }
                 __syncwarp();
-                ptx::named_bar_sync(1, 128);
+                ptx::named_bar_sync(ebar, 128);
             }
         }
         // shared memory stays valid until every TMA store has read it

@@ -11,44 +11,57 @@ namespace sherry {
 // the feed-forward entry points).
 inline int tc_token_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M < 1536 ? 128 : 192; }
 
-// Token tile and grid of a tensor-core launch with M rows of int8 (tokens or
-// digit rows), TN row tiles and Kc chunks, by the time each choice is
-// estimated to take.  Per CTA: c(BN) us a chunk and e(BN) us for the epilogue
-// of its last tile; whole tiles run in rounds of one per SM, and a round lasts
-// no less than an epilogue; splitting the leftover tiles (or, with fewer tiles
-// than SMs, every tile S ways) evens out the chunks but costs the sums through
-// the workspace.  Constants fitted on one B200 to about 900 forced launches of 160
-// shapes (forward and gradients, M 5 to 2048, 4 to 112 chunks): the choice is
-// on average 0.8 % and at most 16 % above the best of them, the rule of
-// sherry_gemm_tc 26 % (K = 1056, N = 2000, M = 1400: 21 us instead of 45;
-// K = 4096, N = 4096, M = 700: 25.5 instead of 42.5).
+// Token tile, epilogue groups and grid of a tensor-core launch with M rows of
+// int8 (tokens or digit rows), TN row tiles and Kc chunks, by the time each
+// choice is estimated to take.  Per CTA: c us a chunk and e us for the
+// epilogue of a tile (w: the weight of the epilogue's arithmetic, 1 for a bare
+// linear layer).  Whole tiles run in rounds of one per SM; but for the last, a
+// round lasts as long as its chunks, or as its epilogue and the part of the
+// chunks' issue that does not fit beside it.  A second epilogue group cuts the
+// epilogue's share to a third and, one decoder group fewer, slows the chunks.
+// Splitting the leftover tiles (or, with fewer tiles than SMs, every tile S
+// ways) evens out the chunks but costs the sums through the workspace.
+// Constants fitted on one B200 to about 1200 forced launches of 220 shapes
+// (forward and gradients, M 5 to 2048, 1 to 112 chunks): the choice is on
+// average 1.3 % and at most 16 % above the best of them; the rule of
+// sherry_gemm_tc was 26 % above it (K = 1056, N = 2000, M = 1400: 21 us instead
+// of 45; K = 4096, N = 4096, M = 700: 25.5 instead of 42.5), and one epilogue
+// group 20 to 40 % on long batches of few chunks (M = 2048, N = 4096, gelu with
+// residual, fp32: K = 768 68 -> 46 us, K = 4096 89 -> 72 us).
 struct TilePlan {
     int bn = 16;
+    int eg = 1;
     int64_t grid = 1;
     int whole = 1;
 };
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms)
+// grad: the launch reads the transposed weight (kEpGrad).
+inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, double w, bool grad)
 {
     struct Tile {
-        int bn;
+        int bn, eg;
         double chunk_us;
     };
-    constexpr Tile kTiles[] = {{16, 0.155}, {32, 0.150}, {64, 0.177}, {128, 0.248}, {192, 0.300}};
+    // two epilogue groups: the tiles that measured best with them
+    const Tile kTiles[] = {{16, 1, 0.159},  {32, 1, 0.154},  {64, 1, 0.172},
+                           {128, 1, 0.221}, {192, 1, 0.260}, {grad ? 192 : 64, 2, grad ? 0.291 : 0.205},
+                           {128, 2, grad ? 1e9 : 0.263}};
     TilePlan best;
     double best_us = 1e300;
     for (const Tile& t : kTiles) {
         const int64_t T = ceil_div(M, t.bn) * TN;
-        const double e = 0.6 + 0.004 * t.bn, sums = 3.4 + 0.08 * t.bn, tile = t.chunk_us * (double)Kc;
-        const double whole = (double)(ceil_div(T, sms) - 1) * std::max(tile, e) + tile + e;
+        const double e = (0.1 + 0.026 * t.bn) * w, chunks = t.chunk_us * (double)Kc;
+        const double steady = std::max(chunks, (t.eg == 2 ? 0.34 * e : e) + 0.65 * chunks);
+        const double whole = (double)(ceil_div(T, sms) - 1) * steady + chunks + e;
         if (whole < best_us) {
             best_us = whole;
-            best = {t.bn, std::min(T, sms), 1};
+            best = {t.bn, t.eg, std::min(T, sms), 1};
         }
         // split launches stay within the workspace of sherry_reserve(M, ..)
-        if (t.bn > tc_token_tile(M)) continue;
+        if (t.eg == 2 || t.bn > tc_token_tile(M)) continue;
+        const double sums = 3.6 + 0.075 * t.bn;
         double split;
         int64_t grid;
         if (T < sms) {
@@ -61,12 +74,12 @@ inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms)
             grid = sms;
             // the sums hold up the epilogue warps; only a long tile behind
             // them hides that (all of it from about 60 us on)
-            const double shown = std::min(1.0, std::max(0.0, 1.0 - (tile - 15.0) / 45.0));
-            split = tile * (double)T / (double)sms + e + sums * shown;
+            const double shown = std::min(1.0, std::max(0.0, 1.0 - (chunks - 15.0) / 45.0));
+            split = steady * (double)T / (double)sms + e + sums * shown;
         }
         if (split < best_us) {
             best_us = split;
-            best = {t.bn, grid, 0};
+            best = {t.bn, 1, grid, 0};
         }
     }
     return best;

@@ -14,9 +14,9 @@
 
 using namespace sherry;
 
-static int check(int64_t M, int64_t TN, int64_t Kc, int64_t sms)
+static int check(int64_t M, int64_t TN, int64_t Kc, int64_t sms, double w, bool grad)
 {
-    const TilePlan pl = plan_tiles(M, TN, Kc, sms);
+    const TilePlan pl = plan_tiles(M, TN, Kc, sms, w, grad);
     tc::Params p{};
     p.TM = (M + pl.bn - 1) / pl.bn;
     p.TN = TN;
@@ -26,6 +26,8 @@ static int check(int64_t M, int64_t TN, int64_t Kc, int64_t sms)
     const char* what = nullptr;
     if (pl.grid < 1 || pl.grid > sms || pl.grid > p.U) what = "grid";
     if (!pl.whole && pl.bn > tc_token_tile(M)) what = "split tile larger than the reserved slots";
+    // the instantiated kernels
+    if (pl.eg == 2 && !(grad ? pl.bn == 192 : pl.bn == 64 || pl.bn == 128)) what = "no such kernel";
     std::vector<uint8_t> seen(p.U, 0);
     for (int64_t b = 0; b < pl.grid && !what; ++b)
         for (tc::SegWalk w(p, b, pl.grid); !w.done() && !what; w.next()) {
@@ -54,17 +56,22 @@ int main()
     const int64_t tns[] = {1, 2, 7, 16, 32, 40, 112, 149, 224};
     const int64_t kcs[] = {1, 2, 4, 9, 17, 32, 79, 112};
     const int64_t smss[] = {148, 132, 5, 1};
-    int n = 0, split = 0;
+    int n = 0, split = 0, two = 0;
     for (int64_t M : ms)
         for (int64_t TN : tns)
             for (int64_t Kc : kcs)
                 for (int64_t sms : smss) {
-                    if (check(M, TN, Kc, sms)) return 1;
-                    ++n;
-                    split += !plan_tiles(M, TN, Kc, sms).whole;
+                    for (int k = 0; k < 3; ++k) {
+                        const double w = k == 0 ? 1.0 : k == 1 ? 2.5 : 0.3;
+                        const bool grad = k == 2;
+                        if (check(M, TN, Kc, sms, w, grad)) return 1;
+                        ++n;
+                        split += !plan_tiles(M, TN, Kc, sms, w, grad).whole;
+                        two += plan_tiles(M, TN, Kc, sms, w, grad).eg == 2;
+                    }
                 }
-    if (split == 0 || split == n) {
-        std::printf("only one kind of launch: %d of %d split\n", split, n);
+    if (split == 0 || split == n || two == 0 || two == n) {
+        std::printf("only one kind of launch: %d split, %d with two epilogue groups of %d\n", split, two, n);
         return 1;
     }
     std::printf("ok %d shapes, %d split\n", n, split);

@@ -89,7 +89,9 @@ def run_forward(gated, M, K, N, dt, act, bias, residual, x=None):
 # token counts of every path: fused decode, decode, each token tile, split and whole tiles
 SHAPES = [(1, 32, 1), (1, 256, 128), (1, 4096, 1999), (2, 96, 5), (2, 1056, 130), (3, 160, 7), (16, 4096, 256),
           (17, 288, 129), (33, 1056, 130), (64, 512, 64), (65, 96, 1), (127, 4096, 300), (200, 2080, 1001),
-          (1600, 160, 72), (1537, 288, 1003)]
+          (1600, 160, 72), (1537, 288, 1003),
+          # long batches of few chunks: two epilogue groups
+          (2100, 64, 2504), (2100, 160, 2501)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
@@ -239,7 +241,9 @@ def run_backward(gated, M, K, N, dt, act, bias, dy=None):
 
 
 GRAD_SHAPES = [(1, 32, 1), (1, 4096, 300), (2, 96, 5), (7, 160, 130), (9, 1056, 131), (17, 288, 64), (40, 4096, 257),
-               (100, 512, 1001), (390, 2080, 129), (800, 160, 72)]
+               (100, 512, 1001), (390, 2080, 129), (800, 160, 72),
+               # few rows and many tokens: wide column blocks, two epilogue groups
+               (1500, 4096, 100), (2049, 4064, 91)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
