@@ -71,10 +71,15 @@ __device__ __forceinline__ float pre_act(int32_t acc, float al, float s, bool ha
     return has_bias ? __fadd_rn(z, b) : z;
 }
 
-// Four values from p, which has `left` of them (16-byte aligned when vec and
-// left >= 4).
+// A thread's unit is four weight rows.  Where rows and bases allow it (VEC) they
+// are consecutive and read 16 bytes at a time.  Elsewhere the k-th is k * step
+// rows on (gated: the two pairs are `step` pairs apart), step the number of
+// threads side by side, so that every load of a warp is one contiguous piece:
+// four consecutive rows a thread measured two to three times the L2 traffic.
+
+// Four values, p[k * step] of the `left` there are from p on.
 template <class T>
-__device__ __forceinline__ void load4(const T* p, int64_t left, bool vec, T (&v)[4])
+__device__ __forceinline__ void load4(const T* p, int left, bool vec, int step, T (&v)[4])
 {
     if (vec) {
         const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p));
@@ -83,26 +88,26 @@ __device__ __forceinline__ void load4(const T* p, int64_t left, bool vec, T (&v)
         for (int k = 0; k < 4; ++k) memcpy(&v[k], &w[k], 4);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = k < left ? __ldcg(p + k) : T(0);
+        for (int k = 0; k < 4; ++k) v[k] = k * step < left ? __ldcg(p + k * step) : T(0);
     }
 }
 
-// Sums of four rows: pairs of a gated weight are 8-byte aligned in any case.
+// The same for rows that come in pairs (8-byte aligned when they are sums).
 template <bool GATED>
-__device__ __forceinline__ void load_acc(const int32_t* p, int64_t left, bool vec, int32_t (&a)[4])
+__device__ __forceinline__ void load_acc(const int32_t* p, int left, bool vec, int step, int32_t (&a)[4])
 {
     if (!GATED || vec) {
-        load4(p, left, vec, a);
+        load4(p, left, vec, step, a);
     } else {
-        const int2 t = __ldcg(reinterpret_cast<const int2*>(p));
-        const int2 u = left > 2 ? __ldcg(reinterpret_cast<const int2*>(p + 2)) : make_int2(0, 0);
+        const int2 t = 0 < left ? __ldcg(reinterpret_cast<const int2*>(p)) : make_int2(0, 0);
+        const int2 u = 2 * step < left ? __ldcg(reinterpret_cast<const int2*>(p + 2 * step)) : make_int2(0, 0);
         a[0] = t.x; a[1] = t.y; a[2] = u.x; a[3] = u.y;
     }
 }
 
-// C values of dy (2 or 4) from p, which has `left` of them.
+// C values of dy (2 or 4), p[k * step] of the `left` there are.
 template <int DT, int C>
-__device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int64_t left, bool vec, float (&g)[C])
+__device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int left, bool vec, int step, float (&g)[C])
 {
     using E = typename Elem<DT>::type;
     if (vec) {
@@ -129,26 +134,42 @@ __device__ __forceinline__ void load_dy(const typename Elem<DT>::type* p, int64_
             }
         }
     } else {
+        E h[C];
 #pragma unroll
-        for (int k = 0; k < C; ++k) g[k] = k < left ? widen<DT>(__ldcg(p + k)) : 0.0f;
+        for (int k = 0; k < C; ++k) h[k] = k * step < left ? __ldcg(p + k * step) : E(0);
+#pragma unroll
+        for (int k = 0; k < C; ++k) g[k] = widen<DT>(h[k]);
     }
 }
 
-// What four consecutive weight rows (of `left` from there on) need of alpha and bias.
+// What a unit's rows need of alpha and bias.
 struct Rows4 {
     float al[4], b[4];
 };
-template <bool VEC>
-__device__ __forceinline__ Rows4 load_rows(const float* alpha, const float* bias, int64_t left)
+template <bool GATED, bool VEC>
+__device__ __forceinline__ void load_row_values(const float* p, int left, int step, float (&v)[4])
+{
+    if constexpr (GATED && !VEC) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = 2 * (k >> 1) * step + (k & 1);
+            v[k] = at < left ? __ldcg(p + at) : 0.0f;
+        }
+    } else {
+        load4(p, left, VEC, step, v);
+    }
+}
+template <bool GATED, bool VEC>
+__device__ __forceinline__ Rows4 load_rows(const float* alpha, const float* bias, int left, int step)
 {
     Rows4 w;
-    load4(alpha, left, VEC, w.al);
+    load_row_values<GATED, VEC>(alpha, left, step, w.al);
     w.b[0] = w.b[1] = w.b[2] = w.b[3] = 0.0f;
-    if (bias) load4(bias, left, VEC, w.b);
+    if (bias) load_row_values<GATED, VEC>(bias, left, step, w.b);
     return w;
 }
 
-// dz of four consecutive weight rows of one token, from their sums a and the
+// dz of a unit of one token, from its sums a and the
 // token's dy (two columns when gated)
 template <bool GATED, int ACT, int C>
 __device__ __forceinline__ void dz4(const int32_t (&a)[4], const float (&g)[C], const Rows4& w, bool hb, float s,
@@ -173,7 +194,7 @@ __device__ __forceinline__ void dz4(const int32_t (&a)[4], const float (&g)[C], 
     }
 }
 
-// e of units of four rows of one token's segment: unit u from row 4 u on.
+// e of units of one token's segment: from row `at` (gated: pair `at`) on.
 template <bool GATED, int ACT, int DT, bool VEC>
 struct Segment {
     static constexpr int C = GATED ? 2 : 4;
@@ -195,13 +216,14 @@ struct Segment {
         rows = (int)(p.R - r0);
         cols = (int)(p.No - c0);
     }
-    __device__ __forceinline__ void e4(int u, float (&e)[4]) const
+    __device__ __forceinline__ void e4(int at, int step, float (&e)[4]) const
     {
+        const int r = GATED ? 2 * at : at;
         float g[C], dz[4];
         int32_t a[4] = {0, 0, 0, 0};
-        load_dy<DT, C>(dy + C * u, cols - C * u, VEC, g);
-        if (acc) load_acc<GATED>(acc + 4 * u, rows - 4 * u, VEC, a);
-        const Rows4 w = load_rows<VEC>(alpha + 4 * u, bias ? bias + 4 * u : nullptr, rows - 4 * u);
+        load_dy<DT, C>(dy + at, cols - at, VEC, step, g);
+        if (acc) load_acc<GATED>(acc + r, rows - r, VEC, step, a);
+        const Rows4 w = load_rows<GATED, VEC>(alpha + r, bias ? bias + r : nullptr, rows - r, step);
         dz4<GATED, ACT, C>(a, g, w, bias != nullptr, s, dz);
 #pragma unroll
         for (int k = 0; k < 4; ++k) e[k] = __fmul_rn(dz[k], w.al[k]);
@@ -230,13 +252,27 @@ __device__ __forceinline__ void grad_digits(const Params& p, float* cache, uint3
     const int U = (int)((min(r0 + p.seg, (p.R + 3) & ~int64_t(3)) - r0) >> 2);     // units of four rows, may be <= 0
     const Segment<GATED, ACT, DT, VEC> sg(p, m, r0);
     uint32_t mx = 0;
+    // units: rows (gated: pairs) i * kUnit + .. of 4 U; strided ones only go to
+    // the cache
+    constexpr int kUnit = GATED ? 2 : 4;
+    const bool strided = !VEC && p.cached;
+    const int step = strided ? kDigitThreads : 1;
 #pragma unroll 2
-    for (int u = tid; u < U; u += kDigitThreads) {
+    for (int i = tid; i < U * (strided ? kUnit : 1); i += kDigitThreads * (strided ? kUnit : 1)) {
+        const int at = strided ? i : kUnit * i;
         float e[4];
-        sg.e4(u, e);
+        sg.e4(at, step, e);
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx = max(mx, __float_as_uint(e[k]) & 0x7FFFFFFFu);
-        if (p.cached) *reinterpret_cast<float4*>(cache + 4 * u) = make_float4(e[0], e[1], e[2], e[3]);
+        if (strided) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int to = GATED ? 2 * (at + (k >> 1) * step) + (k & 1) : at + k * step;
+                if (to < 4 * U) cache[to] = e[k];
+            }
+        } else if (p.cached) {
+            *reinterpret_cast<float4*>(cache + 4 * i) = make_float4(e[0], e[1], e[2], e[3]);
+        }
     }
     mx = __reduce_max_sync(0xffffffffu, mx);
     if (lane == 0) warp_max[tid >> 5] = mx;
@@ -285,7 +321,7 @@ __device__ __forceinline__ void grad_digits(const Params& p, float* cache, uint3
                 const float4 t = *reinterpret_cast<const float4*>(cache + 4 * u);
                 e[0] = t.x; e[1] = t.y; e[2] = t.z; e[3] = t.w;
             } else {
-                sg.e4(u, e);
+                sg.e4(kUnit * u, 1, e);
             }
         }
         uint32_t v[4];
@@ -355,6 +391,7 @@ struct Column {
     int rows, cols;             // left in the arrays' rows
     Rows4 w;
     bool hb;
+    static constexpr int kLanes = VEC ? 1 : 32;              // rows (pairs) between a unit's
 
     template <int B>
     __device__ __forceinline__ void run(int64_t M, float (&sa)[4], float (&sb)[4])
@@ -364,12 +401,12 @@ struct Column {
             int32_t a[B][4];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                load_dy<DT, C>(dy, cols, VEC, g[i]);
+                load_dy<DT, C>(dy, cols, VEC, kLanes, g[i]);
                 dy += dstep;
                 sc[i] = 0.0f;
                 a[i][0] = a[i][1] = a[i][2] = a[i][3] = 0;
                 if constexpr (ACC) {
-                    load_acc<GATED>(acc, rows, VEC, a[i]);
+                    load_acc<GATED>(acc, rows, VEC, kLanes, a[i]);
                     acc += astep;
                     sc[i] = __ldcg(s);
                     s += step;
@@ -402,10 +439,10 @@ __device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t 
     c.dstep = step * p.No;
     c.astep = step * p.R;
     c.m = m0;
-    c.rows = (int)min(p.R - r, int64_t(4));
-    c.cols = (int)min(p.No - col, int64_t(4));
+    c.rows = (int)min(p.R - r, int64_t(kColRows));
+    c.cols = (int)min(p.No - col, int64_t(kColRows));
     c.hb = p.bias != nullptr;
-    c.w = load_rows<VEC>(p.alpha + r, c.hb ? p.bias + r : nullptr, p.R - r);
+    c.w = load_rows<GATED, VEC>(p.alpha + r, c.hb ? p.bias + r : nullptr, c.rows, c.kLanes);
     constexpr int kBatch = GATED ? 4 : 3;                    // what 80 registers hold
     c.template run<kBatch>(p.M, sa, sb);
     c.template run<1>(p.M, sa, sb);
@@ -421,7 +458,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 
     if (!p.beside) ptx::pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t CY = gridDim.y, rank = blockIdx.y;
-    const int64_t r = (int64_t)blockIdx.x * kColRows + 4 * lane;
+    // the lane's first row: four in a row, or every 32nd (gated: pair)
+    const int64_t r = (int64_t)blockIdx.x * kColRows + lane * (p.vec ? 4 : GATED ? 2 : 1);
     float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (r < p.R) {
         const int64_t m0 = (int64_t)rank * WARPS + warp, step = (int64_t)CY * WARPS;
@@ -436,8 +474,17 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 
             else column_sums<GATED, ACT, DT, false, true>(p, r, m0, step, sa, sb);
         }
     }
-    *reinterpret_cast<float4*>(&part[warp][0][4 * lane]) = make_float4(sa[0], sa[1], sa[2], sa[3]);
-    *reinterpret_cast<float4*>(&part[warp][1][4 * lane]) = make_float4(sb[0], sb[1], sb[2], sb[3]);
+    if (p.vec) {
+        *reinterpret_cast<float4*>(&part[warp][0][4 * lane]) = make_float4(sa[0], sa[1], sa[2], sa[3]);
+        *reinterpret_cast<float4*>(&part[warp][1][4 * lane]) = make_float4(sb[0], sb[1], sb[2], sb[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = GATED ? 2 * (lane + 32 * (k >> 1)) + (k & 1) : lane + 32 * k;
+            part[warp][0][at] = sa[k];
+            part[warp][1][at] = sb[k];
+        }
+    }
     __syncthreads();
     static_assert(32 * WARPS >= kColRows, "one thread per row");
     const int i = threadIdx.x;
