@@ -426,6 +426,8 @@ def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q,
     R = 2 * N if gated else N
     wp = _ptr(w_native, "w_native", _torch.uint8, (-(-R // 128) * -(-K // 128) * 2560,), idx)
     ap = _ptr(alpha, "alpha", _torch.float32, (R,), idx)
+    if wp is None or ap is None:
+        raise ValueError("w_native and alpha are needed")
     bp = _ptr(bias, "bias", _torch.float32, (R,), idx)
     rp = _ptr(residual, "residual", x.dtype, (M, N), idx)
     cp = _ptr(acc, "acc", _torch.int32, (M, R), idx)

@@ -401,9 +401,11 @@ inline bool plan_rt(int64_t N, int64_t Kc, int64_t M, int sms, int budget, int r
 
 // One row per thread for one token when its codes stay resident; several rows
 // per thread otherwise (and whenever the first choice finds no plan).
-inline bool plan_within(int64_t N, int64_t Kc, int64_t M, int sms, int budget, Plan* out)
+// first: the rows per thread to try first (0: rt_first).
+inline bool plan_within(int64_t N, int64_t Kc, int64_t M, int sms, int budget, Plan* out, int first = 0)
 {
-    if (rt_first(M) != rt_max(M) && plan_rt(N, Kc, M, sms, budget, rt_first(M), out) && out->NS == out->CPT)
+    if (first == 0) first = rt_first(M);
+    if (first != rt_max(M) && plan_rt(N, Kc, M, sms, budget, first, out) && out->NS == out->CPT)
         return true;
     return plan_rt(N, Kc, M, sms, budget, rt_max(M), out);
 }
@@ -411,9 +413,21 @@ inline bool plan_within(int64_t N, int64_t Kc, int64_t M, int sms, int budget, P
 // The plan of a launch: within kSmemBudget (two CTAs per SM, so the next
 // layer's CTA can start its weight fetch beside this one) when possible, else
 // within kSmemBudgetMax (one CTA per SM).
-inline bool plan(int64_t N, int64_t Kc, int64_t M, int sms, Plan* out)
+inline bool plan(int64_t N, int64_t Kc, int64_t M, int sms, Plan* out, int first = 0)
 {
-    return plan_within(N, Kc, M, sms, kSmemBudget, out) || plan_within(N, Kc, M, sms, kSmemBudgetMax, out);
+    return plan_within(N, Kc, M, sms, kSmemBudget, out, first) ||
+           plan_within(N, Kc, M, sms, kSmemBudgetMax, out, first);
+}
+
+// Rows per thread of the feed-forward launches with one token: with many rows
+// per SM, several rows share a thread's activation loads (one B200, gated:
+// 28672 rows K = 4096 11.6 us with one row, 10.9 with two, 10.75 with four;
+// 11264 rows K = 2048 5.3, 4.95, 5.3); with few, one row per thread keeps more
+// threads busy (4096 rows K = 14336 9.05, 10.1, 9.9).
+inline int ep_rt_first(int64_t N, int64_t M, int sms)
+{
+    if (M != 1) return 0;
+    return N >= 128 * (int64_t)sms ? 4 : N >= 64 * (int64_t)sms ? 2 : 1;
 }
 
 // This thread's copies of one ring step: the 16-byte pieces (4 rows of one

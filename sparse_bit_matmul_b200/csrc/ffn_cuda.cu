@@ -339,7 +339,8 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     if (st != SHERRY_OK) return st;
 
     decode::Plan pl;
-    const bool few = M <= SHERRY_GEMM_DECODE_AUTO_MAX_M && decode::plan(R, sherry_k_chunks(K), M, di.sms, &pl);
+    const bool few = M <= SHERRY_GEMM_DECODE_AUTO_MAX_M && decode::plan(R, sherry_k_chunks(K), M, di.sms, &pl,
+                                                                           decode::ep_rt_first(R, M, di.sms));
     decode::EpParams d = {};
     if (few) {
         d.wnative = static_cast<const uint8_t*>(wn);
