@@ -664,14 +664,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     // instead of queueing in front of this CTA's activation reads
     ptx::pdl_launch_dependents();
 
-    // outputs of this CTA: one per (token, row) or (token, row pair)
-    int O = M * Rc;
-    [[maybe_unused]] int Rw = Rc;                            // outputs per token
+    // EP: outputs of this CTA, one per (token, row) or (token, row pair), and the
+    // bias and residual of this thread's first
+    [[maybe_unused]] int Oe = 0, Rw = 0;
     [[maybe_unused]] float pre_b0 = 0.0f, pre_b1 = 0.0f, pre_r = 0.0f;
     if constexpr (EP) {
-        if (p.gated) Rw = Rc >> 1;
-        O = M * Rw;
-        if (tid < O) {
+        Rw = p.gated ? Rc >> 1 : Rc;                         // outputs per token
+        Oe = M * Rw;
+        if (tid < Oe) {
             const int m = tid / Rw, ii = tid - m * Rw;
             if (p.gated) {
                 if (p.bias) {
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     }
     __syncthreads();
     if constexpr (EP) {
-        for (int idx = tid; idx < O; idx += nthr) {
+        for (int idx = tid; idx < Oe; idx += nthr) {
             const int m = idx / Rw, ii = idx - m * Rw;
             const int i0 = p.gated ? 2 * ii : ii;
             const int64_t n = r0 + i0;
@@ -840,6 +840,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
             ep::store_elem(p.out, m * (p.gated ? p.N >> 1 : p.N) + (p.gated ? n >> 1 : n), y, p.dtype);
         }
     } else {
+        const int O = M * Rc;
         // output o = (token m, row i): one thread sums its P partials
         for (int idx = tid; idx < O; idx += nthr) {
             const int m = idx / Rc, ii = idx - m * Rc;
