@@ -345,6 +345,11 @@ def _activation(act) -> int:
     return a
 
 
+@functools.lru_cache(maxsize=256)
+def _work_bytes(dtype: int, M: int, R: int) -> int:
+    return int(load().sherry_grad_work_bytes(dtype, M, R))
+
+
 def _stream_of(idx: int):
     return _torch._C._cuda_getCurrentRawStream(idx)
 
@@ -509,7 +514,7 @@ def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, w
     if M == 0:
         return dx, dalpha, dbias
     if want_dx:
-        work = w_t.new_empty(_lib.sherry_grad_work_bytes(dt, M, R))
+        work = w_t.new_empty(_work_bytes(dt, M, R))
         kp = work.data_ptr()
         if idx not in _split_reserved:
             reserve_split(idx)

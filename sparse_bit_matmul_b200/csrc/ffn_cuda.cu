@@ -444,14 +444,8 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.dbias = dbias;
     if (!dx) return grad::launch_columns(g, gated, act, dtype, di.sms, s);
     const TilePlan plan = plan_tiles(M * D, sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true);
-    const bool columns = dalpha || dbias;
-    g.beside = columns && grad::columns_beside(R, M, plan.grid, di.sms);
-    st = grad::launch_digits(g, gated, act, dtype, di.sms, s);
+    st = grad::launch_ahead(g, gated, act, dtype, di.sms, s);
     if (st != SHERRY_OK) return st;
-    if (columns && !g.beside) {
-        st = grad::launch_columns(g, gated, act, dtype, di.sms, s);
-        if (st != SHERRY_OK) return st;
-    }
     tc::EpParams p = {};
     p.wnative = static_cast<const uint8_t*>(wt);
     p.x_scale = g.dscale;
@@ -462,9 +456,7 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     p.Mo = M;
     p.No = K;
     p.dtype = dtype;
-    st = D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, plan, s) : launch_grad_tc<4>(g.dig, g.ld, p, plan, s);
-    if (st != SHERRY_OK || !g.beside) return st;
-    return grad::launch_columns(g, gated, act, dtype, di.sms, s);
+    return D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, plan, s) : launch_grad_tc<4>(g.dig, g.ld, p, plan, s);
 }
 
 int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)

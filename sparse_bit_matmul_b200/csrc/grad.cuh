@@ -44,7 +44,6 @@ struct Params {
     int vec;                    // rows and bases allow 16-byte loads of four rows' values
     float* dalpha;              // [R] or null
     float* dbias;               // [R] or null
-    int beside;                 // the column sums run beside the dx product of the same call
 };
 
 template <int DT>
@@ -241,12 +240,11 @@ constexpr int kDigitThreads = 256;
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 template <bool GATED, int ACT, int DT, bool VEC>
-__device__ __forceinline__ void grad_digits(const Params& p, float* cache, uint32_t* warp_max, uint32_t* block_max)
+__device__ __forceinline__ void grad_digits(const Params& p, int64_t m, uint32_t rank, uint32_t CX, float* cache,
+                                            uint32_t* warp_max, uint32_t* block_max)
 {
     constexpr int D = kDigits<DT>;
     constexpr int kWarps = kDigitThreads / 32;
-    const uint32_t CX = gridDim.x, rank = blockIdx.x;
-    const int64_t m = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t r0 = (int64_t)rank * p.seg;
     const int U = (int)((min(r0 + p.seg, (p.R + 3) & ~int64_t(3)) - r0) >> 2);     // units of four rows, may be <= 0
@@ -345,30 +343,27 @@ __device__ __forceinline__ void grad_digits(const Params& p, float* cache, uint3
 }
 
 template <bool GATED, int ACT, int DT>
-__global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params p)
+__device__ __forceinline__ void digits_block(const Params& p, int64_t m, uint32_t rank, uint32_t CX)
 {
     extern __shared__ __align__(16) float cache[];
     __shared__ uint32_t warp_max[kDigitThreads / 32];
     __shared__ uint32_t block_max;
+    if (p.vec) grad_digits<GATED, ACT, DT, true>(p, m, rank, CX, cache, warp_max, &block_max);
+    else grad_digits<GATED, ACT, DT, false>(p, m, rank, CX, cache, warp_max, &block_max);
+}
+
+// grid (blocks per token, tokens)
+template <bool GATED, int ACT, int DT>
+__global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params p)
+{
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    if (p.vec) grad_digits<GATED, ACT, DT, true>(p, cache, warp_max, &block_max);
-    else grad_digits<GATED, ACT, DT, false>(p, cache, warp_max, &block_max);
+    digits_block<GATED, ACT, DT>(p, blockIdx.y, blockIdx.x, gridDim.x);
 }
 
 // Column sums: a block owns the rows of 32 lanes x 4 weight rows, its warps
 // (and the blocks of its cluster, which share the columns) take the tokens in
 // turn, and the partial sums meet in a fixed order.
-// With `beside` the kernel is launched behind the dx product and does not wait
-// for it: every block of the product lets it start only after its own wait, so
-// the digits kernel and all before it are complete, and what this kernel reads
-// (through L2) and overwrites is free.  Its first block waits for the product
-// at its end, so that the kernel's completion still means all of the call's.
-// Used where the SMs without a CTA of the product hold all of its blocks (M=129
-// 4096x4096 f32: 23.6 -> 19.4 us for the call) or a warp has at most eight
-// tokens (M=5 K=1024, gated to 2816, bf16: 13.6 -> 11.4 us); longer ones on the
-// same SMs slow the product by more than they save (M=2048 K=14336 N=4096: 197
-// -> 211 us), and run before it instead.
 constexpr int kColWarps = 4;
 constexpr int kColBlocks = 6;                                // resident per SM (registers)
 // Many tokens and so few rows that clusters of eight blocks leave SMs idle:
@@ -449,17 +444,13 @@ __device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t 
 }
 
 template <bool GATED, int ACT, int DT, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 1)
-    grad_columns_kernel(const Params p)
+__device__ __forceinline__ void columns_block(const Params& p, int64_t bx, uint32_t rank, uint32_t CY)
 {
     __shared__ float part[WARPS][2][kColRows];
     __shared__ float total[2][kColRows];
-    ptx::pdl_launch_dependents();
-    if (!p.beside) ptx::pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t CY = gridDim.y, rank = blockIdx.y;
     // the lane's first row: four in a row, or every 32nd (gated: pair)
-    const int64_t r = (int64_t)blockIdx.x * kColRows + lane * (p.vec ? 4 : GATED ? 2 : 1);
+    const int64_t r = bx * kColRows + lane * (p.vec ? 4 : GATED ? 2 : 1);
     float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (r < p.R) {
         const int64_t m0 = (int64_t)rank * WARPS + warp, step = (int64_t)CY * WARPS;
@@ -511,20 +502,43 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 
         ptx::cluster_arrive_release();                       // the sums stay readable until read
         ptx::cluster_wait_acquire();
     }
-    const int64_t n = (int64_t)blockIdx.x * kColRows + i;
+    const int64_t n = bx * kColRows + i;
     if (rank == 0 && mine && n < p.R) {
         if (p.dalpha) p.dalpha[n] = t[0];
         if (p.dbias) p.dbias[n] = t[1];
     }
-    // one block's wait keeps the grid from completing before the product; the
-    // others leave their places to the blocks behind them
-    if (p.beside && blockIdx.x == 0 && rank == 0) ptx::pdl_wait();
 }
 
-// Host: the two launches of a gradient call (grad_cuda.cu).
-int launch_digits(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream);
-// Whether the column sums of a call run beside its product of `ctas` CTAs.
-bool columns_beside(int64_t R, int64_t M, int64_t ctas, int sms);
+// grid (row blocks, blocks that share the columns)
+template <bool GATED, int ACT, int DT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 1)
+    grad_columns_kernel(const Params p)
+{
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    columns_block<GATED, ACT, DT, WARPS>(p, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+// Both in one launch, for few tokens, where a launch costs more than the work
+// (M=5 K=1024, gated to 2816, bf16: 13.6 -> BOTH_US us for the call): clusters of
+// `cluster` blocks, the first `tokens` of them (all M, or none) the tokens'
+// digits, the others column sums, whose order does not depend on whether the
+// digits are wanted.
+constexpr int64_t kBothMaxTokens = 256;
+
+template <bool GATED, int ACT, int DT>
+__global__ void __launch_bounds__(kDigitThreads) grad_both_kernel(const Params p, uint32_t tokens, uint32_t cluster)
+{
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    const uint32_t id = blockIdx.x / cluster, rank = blockIdx.x - id * cluster;
+    if (id < tokens) digits_block<GATED, ACT, DT>(p, id, rank, cluster);
+    else columns_block<GATED, ACT, DT, kDigitThreads / 32>(p, id - tokens, rank, cluster);
+}
+
+// Host (grad_cuda.cu): what a gradient call launches ahead of its product, and
+// the column sums alone.
+int launch_ahead(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream);
 int launch_columns(const Params& p, bool gated, int act, int dtype, int sms, cudaStream_t stream);
 
 }  // namespace grad

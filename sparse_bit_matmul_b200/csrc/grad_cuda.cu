@@ -17,16 +17,9 @@ constexpr int kSegMin = 1024;               // weight rows worth a block of thei
 constexpr int kSegMax = 8192;               // above, a block's 32 KB keep its neighbours off the SM
 constexpr int kClusterMax = 8;
 
-int columns_cluster(int64_t R, int64_t M, int sms);
-
-bool columns_wide(int64_t R, int64_t M, int sms)
-{
-    return M >= 4 * kColWarpsWide * 2 && (R + kColRows - 1) / kColRows * kClusterMax < sms;
-}
-
-template <class K>
-cudaError_t launch_cluster(K kernel, dim3 grid, dim3 cluster, int threads, size_t smem, cudaStream_t stream,
-                           const Params& p)
+template <class... A, class... B>
+cudaError_t launch_cluster(void (*kernel)(A...), dim3 grid, dim3 cluster, int threads, size_t smem, cudaStream_t stream,
+                           B... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -42,75 +35,7 @@ cudaError_t launch_cluster(K kernel, dim3 grid, dim3 cluster, int threads, size_
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-template <bool GATED, int ACT, int DT>
-int digits(Params p, int sms, cudaStream_t stream)
-{
-    auto kernel = grad_digits_kernel<GATED, ACT, DT>;
-    static std::atomic<uint64_t> done{0};
-    const int st = once_per_device(done, [&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheMax);
-    });
-    if (st != SHERRY_OK) return st;
-    // Blocks per token: so many that a block holds at most kSegMax rows, and
-    // more while the grid leaves SMs without four blocks.
-    int cx = 1;
-    while (cx < kClusterMax && (p.ld > (int64_t)cx * kSegMax || (p.M * cx < 4 * (int64_t)sms && p.ld >= (int64_t)cx * 2 * kSegMin)))
-        cx *= 2;
-    p.seg = (int)(((p.ld + cx - 1) / cx + 15) & ~int64_t(15));
-    const int64_t need = 4 * std::min<int64_t>(p.seg, (p.R + 3) & ~int64_t(3));
-    p.cached = need <= kCacheMax;
-    // tokens in grid.y: at most 65535 a launch
-    Params q = p;
-    for (int64_t m0 = 0; m0 < p.M; m0 += 65535) {
-        const int64_t left = p.M - m0, n = left < 65535 ? left : 65535;
-        q.dy = static_cast<const uint8_t*>(p.dy) + m0 * p.No * (DT == SHERRY_F32 ? 4 : 2);
-        q.acc = p.acc ? p.acc + m0 * p.R : nullptr;
-        q.x_scale = p.x_scale ? p.x_scale + m0 : nullptr;
-        q.dig = p.dig + m0 * kDigits<DT> * p.ld;
-        q.dscale = p.dscale + m0;
-        const cudaError_t e = launch_cluster(kernel, dim3((unsigned)cx, (unsigned)n), dim3((unsigned)cx, 1), kDigitThreads,
-                                             p.cached ? (size_t)need : 0, stream, q);
-        if (e != cudaSuccess) return cuda_status(e);
-    }
-    return SHERRY_OK;
-}
-
-template <bool GATED, int ACT, int DT>
-int columns(const Params& p, int sms, cudaStream_t stream)
-{
-    const unsigned bx = (unsigned)((p.R + kColRows - 1) / kColRows);
-    if (columns_wide(p.R, p.M, sms)) {
-        const unsigned cy = (unsigned)std::min<int64_t>(kClusterMax, p.M / (4 * kColWarpsWide));
-        return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarpsWide>, dim3(bx, cy), dim3(1, cy),
-                                          32 * kColWarpsWide, 0, stream, p));
-    }
-    const unsigned cy = (unsigned)columns_cluster(p.R, p.M, sms);
-    return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarps>, dim3(bx, cy), dim3(1, cy),
-                                      32 * kColWarps, 0, stream, p));
-}
-
-template <bool GATED, int ACT>
-int of_type(bool dig, const Params& p, int dtype, int sms, cudaStream_t s)
-{
-    if (dtype == SHERRY_F32) return dig ? digits<GATED, ACT, SHERRY_F32>(p, sms, s) : columns<GATED, ACT, SHERRY_F32>(p, sms, s);
-    if (dtype == SHERRY_BF16) return dig ? digits<GATED, ACT, SHERRY_BF16>(p, sms, s) : columns<GATED, ACT, SHERRY_BF16>(p, sms, s);
-    return dig ? digits<GATED, ACT, SHERRY_F16>(p, sms, s) : columns<GATED, ACT, SHERRY_F16>(p, sms, s);
-}
-
-template <bool GATED>
-int of_act(bool dig, const Params& p, int act, int dtype, int sms, cudaStream_t s)
-{
-    switch (act) {
-    case SHERRY_ACT_NONE: return of_type<GATED, SHERRY_ACT_NONE>(dig, p, dtype, sms, s);
-    case SHERRY_ACT_RELU: return of_type<GATED, SHERRY_ACT_RELU>(dig, p, dtype, sms, s);
-    case SHERRY_ACT_RELU2: return of_type<GATED, SHERRY_ACT_RELU2>(dig, p, dtype, sms, s);
-    case SHERRY_ACT_SILU: return of_type<GATED, SHERRY_ACT_SILU>(dig, p, dtype, sms, s);
-    case SHERRY_ACT_GELU: return of_type<GATED, SHERRY_ACT_GELU>(dig, p, dtype, sms, s);
-    default: return of_type<GATED, SHERRY_ACT_GELU_TANH>(dig, p, dtype, sms, s);
-    }
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Blocks that share the columns: of the cluster sizes that leave every warp
@@ -132,16 +57,126 @@ int columns_cluster(int64_t R, int64_t M, int sms)
     return cy;
 }
 
-}  // namespace
+int64_t row_blocks(int64_t R) { return (R + kColRows - 1) / kColRows; }
 
-bool columns_beside(int64_t R, int64_t M, int64_t ctas, int sms)
+bool columns_wide(int64_t R, int64_t M, int sms)
 {
-    if (M <= 8 * kColWarps) return true;
-    if (columns_wide(R, M, sms)) return false;
-    return (R + kColRows - 1) / kColRows * columns_cluster(R, M, sms) <= kColBlocks * (sms - ctas);
+    return M >= 4 * kColWarpsWide * 2 && row_blocks(R) * kClusterMax < sms;
 }
 
-int launch_digits(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream)
+// Blocks per token: so many that a block holds at most kSegMax rows, and more
+// while the grid leaves SMs without four blocks.  Fills in p's segments;
+// returns the block's shared memory for e.
+int64_t split_rows(Params& p, int sms, int* blocks)
+{
+    int cx = 1;
+    while (cx < kClusterMax &&
+           (p.ld > (int64_t)cx * kSegMax || (p.M * cx < 4 * (int64_t)sms && p.ld >= (int64_t)cx * 2 * kSegMin)))
+        cx *= 2;
+    p.seg = (int)(((p.ld + cx - 1) / cx + 15) & ~int64_t(15));
+    const int64_t need = 4 * std::min<int64_t>(p.seg, (p.R + 3) & ~int64_t(3));
+    p.cached = need <= kCacheMax;
+    *blocks = cx;
+    return p.cached ? need : 0;
+}
+
+template <class K>
+int allow_cache(K kernel, std::atomic<uint64_t>& done)
+{
+    return once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheMax);
+    });
+}
+
+template <bool GATED, int ACT, int DT>
+int digits(Params p, int sms, cudaStream_t stream)
+{
+    auto kernel = grad_digits_kernel<GATED, ACT, DT>;
+    static std::atomic<uint64_t> done{0};
+    const int st = allow_cache(kernel, done);
+    if (st != SHERRY_OK) return st;
+    int cx = 1;
+    const int64_t smem = split_rows(p, sms, &cx);
+    // tokens in grid.y: at most 65535 a launch
+    Params q = p;
+    for (int64_t m0 = 0; m0 < p.M; m0 += 65535) {
+        const int64_t left = p.M - m0, n = left < 65535 ? left : 65535;
+        q.dy = static_cast<const uint8_t*>(p.dy) + m0 * p.No * (DT == SHERRY_F32 ? 4 : 2);
+        q.acc = p.acc ? p.acc + m0 * p.R : nullptr;
+        q.x_scale = p.x_scale ? p.x_scale + m0 : nullptr;
+        q.dig = p.dig + m0 * kDigits<DT> * p.ld;
+        q.dscale = p.dscale + m0;
+        const cudaError_t e = launch_cluster(kernel, dim3((unsigned)cx, (unsigned)n), dim3((unsigned)cx, 1), kDigitThreads,
+                                             (size_t)smem, stream, q);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    return SHERRY_OK;
+}
+
+// Few tokens: the column sums, and with dx the digits, in one launch.
+template <bool GATED, int ACT, int DT>
+int both(Params p, bool dx, int sms, cudaStream_t stream)
+{
+    auto kernel = grad_both_kernel<GATED, ACT, DT>;
+    static std::atomic<uint64_t> done{0};
+    const int st = allow_cache(kernel, done);
+    if (st != SHERRY_OK) return st;
+    int c = 1;
+    const int64_t smem = split_rows(p, sms, &c), tokens = dx ? p.M : 0;
+    return cuda_status(launch_cluster(kernel, dim3((unsigned)(c * (tokens + row_blocks(p.R)))), dim3((unsigned)c, 1),
+                                      kDigitThreads, (size_t)smem, stream, p, (uint32_t)tokens, (uint32_t)c));
+}
+
+template <bool GATED, int ACT, int DT>
+int columns(const Params& p, int sms, cudaStream_t stream)
+{
+    if (p.M <= kBothMaxTokens) return both<GATED, ACT, DT>(p, false, sms, stream);
+    const unsigned bx = (unsigned)row_blocks(p.R);
+    if (columns_wide(p.R, p.M, sms)) {
+        const unsigned cy = (unsigned)std::min<int64_t>(kClusterMax, p.M / (4 * kColWarpsWide));
+        return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarpsWide>, dim3(bx, cy), dim3(1, cy),
+                                          32 * kColWarpsWide, 0, stream, p));
+    }
+    const unsigned cy = (unsigned)columns_cluster(p.R, p.M, sms);
+    return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarps>, dim3(bx, cy), dim3(1, cy),
+                                      32 * kColWarps, 0, stream, p));
+}
+
+template <bool GATED, int ACT, int DT>
+int ahead(const Params& p, int sms, cudaStream_t stream)
+{
+    if (p.dalpha || p.dbias) {
+        if (p.M <= kBothMaxTokens) return both<GATED, ACT, DT>(p, true, sms, stream);
+        const int st = columns<GATED, ACT, DT>(p, sms, stream);
+        if (st != SHERRY_OK) return st;
+    }
+    return digits<GATED, ACT, DT>(p, sms, stream);
+}
+
+template <bool GATED, int ACT>
+int of_type(bool dx, const Params& p, int dtype, int sms, cudaStream_t s)
+{
+    if (dtype == SHERRY_F32) return dx ? ahead<GATED, ACT, SHERRY_F32>(p, sms, s) : columns<GATED, ACT, SHERRY_F32>(p, sms, s);
+    if (dtype == SHERRY_BF16) return dx ? ahead<GATED, ACT, SHERRY_BF16>(p, sms, s) : columns<GATED, ACT, SHERRY_BF16>(p, sms, s);
+    return dx ? ahead<GATED, ACT, SHERRY_F16>(p, sms, s) : columns<GATED, ACT, SHERRY_F16>(p, sms, s);
+}
+
+template <bool GATED>
+int of_act(bool dx, const Params& p, int act, int dtype, int sms, cudaStream_t s)
+{
+    switch (act) {
+    case SHERRY_ACT_NONE: return of_type<GATED, SHERRY_ACT_NONE>(dx, p, dtype, sms, s);
+    case SHERRY_ACT_RELU: return of_type<GATED, SHERRY_ACT_RELU>(dx, p, dtype, sms, s);
+    case SHERRY_ACT_RELU2: return of_type<GATED, SHERRY_ACT_RELU2>(dx, p, dtype, sms, s);
+    case SHERRY_ACT_SILU: return of_type<GATED, SHERRY_ACT_SILU>(dx, p, dtype, sms, s);
+    case SHERRY_ACT_GELU: return of_type<GATED, SHERRY_ACT_GELU>(dx, p, dtype, sms, s);
+    default: return of_type<GATED, SHERRY_ACT_GELU_TANH>(dx, p, dtype, sms, s);
+    }
+}
+
+}  // namespace
+
+int launch_ahead(Params p, bool gated, int act, int dtype, int sms, cudaStream_t stream)
 {
     return gated ? of_act<true>(true, p, act, dtype, sms, stream) : of_act<false>(true, p, act, dtype, sms, stream);
 }

@@ -553,10 +553,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
     // read (the producer: activations; the epilogue: scales, y, acc and the
     // split-K workspace) wait for it to complete; the decoders and the MMA
     // warp only use this CTA's shared and tensor memory.
-    // kEpGrad lets its dependents start only once its own wait is over (in the
-    // producer): the column sums that run beside it read what the kernels
-    // before the digits wrote.
-    if constexpr (EK != kEpGrad) ptx::pdl_launch_dependents();
+    ptx::pdl_launch_dependents();
 
     if (warp == kProducerWarp) {
         // Converged warp, elected-lane issue and a non-blocking test of the
@@ -589,7 +586,6 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             }
         }
         ptx::pdl_wait();
-        if constexpr (EK == kEpGrad) ptx::pdl_launch_dependents();
         int s = 0;
         uint32_t ph = 0;
         bool ready = false;                      // empty(s) already seen complete
