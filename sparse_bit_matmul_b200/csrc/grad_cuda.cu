@@ -145,12 +145,12 @@ int columns(const Params& p, int sms, cudaStream_t stream)
 template <bool GATED, int ACT, int DT>
 int ahead(const Params& p, int sms, cudaStream_t stream)
 {
-    if (p.dalpha || p.dbias) {
-        if (p.M <= kBothMaxTokens) return both<GATED, ACT, DT>(p, true, sms, stream);
-        const int st = columns<GATED, ACT, DT>(p, sms, stream);
-        if (st != SHERRY_OK) return st;
-    }
-    return digits<GATED, ACT, DT>(p, sms, stream);
+    const bool sums = p.dalpha || p.dbias;
+    if (sums && p.M <= kBothMaxTokens) return both<GATED, ACT, DT>(p, true, sms, stream);
+    // the digits first (M=2048 K=14336 N=4096 bf16: 199 us for the call, 210 the
+    // other way round)
+    const int st = digits<GATED, ACT, DT>(p, sms, stream);
+    return st != SHERRY_OK || !sums ? st : columns<GATED, ACT, DT>(p, sms, stream);
 }
 
 template <bool GATED, int ACT>

@@ -167,6 +167,7 @@ struct Cfg {
     // the other epilogues cut a warp's staging into slots of 16 sums x 32
     // rows: two at BN = 16 (one slice a tile), else four
     static constexpr int kEpSlots = kStagingBytes / (4 * 16 * 32 * 4);
+    static_assert(kEpSlots == 2 || kEpSlots == 4, "rings of 1, 2 or 4 slots");
     static constexpr int kSmemBytes = kOffStaging + EG * kStagingBytes + 1024;   // + alignment slack
     // dynamic plus static (the table of the code path, 1 KB as compiled)
     // within the 227 KB per-block limit
@@ -313,10 +314,10 @@ __device__ __forceinline__ void ep_keep(const EpParams& p, const uint32_t (&v)[S
 // ep_values of S sums, stored element by element: output rows from m0 on,
 // column col (out of range: not stored).  The residual is loaded whole before
 // the first store (it may be the output itself, so a load could not pass a
-// store on its own).
+// store on its own), from staged [token][32 columns] when given.
 template <int EK, int D, int S>
 __device__ __forceinline__ void ep_store(const EpParams& p, const uint32_t (&v)[S], const float* sc, float al,
-                                         float bi, int lane, int64_t m0, int64_t col)
+                                         float bi, int lane, int64_t m0, int64_t col, const float* staged = nullptr)
 {
     constexpr int O = EK == kEpGated ? S / 2 : S / D;
     constexpr int kStep = EK == kEpGated ? 2 : 1;            // output rows between values
@@ -328,7 +329,12 @@ __device__ __forceinline__ void ep_store(const EpParams& p, const uint32_t (&v)[
     // as read, widened only when added: all loads are in flight at once
     [[maybe_unused]] uint32_t rs[EK == kEpLinear ? O : 1];
     if constexpr (EK == kEpLinear) {
-        if (p.res) {
+        if (staged) {
+#pragma unroll
+            for (int i = 0; i < O; ++i)
+                rs[i] = p.dtype == SHERRY_F32 ? __float_as_uint(staged[i * 32 + lane])
+                                              : reinterpret_cast<const uint16_t*>(staged)[i * 32 + lane];
+        } else if (p.res) {
             const char* r = static_cast<const char*>(p.res) + at;
             if (p.dtype == SHERRY_F32) load_strided<O, uint32_t>(r, stride, cnt, rs);
             else load_strided<O, uint16_t>(r, stride, cnt, rs);
@@ -1145,19 +1151,75 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                     const int64_t mleft = p.M - cur_tm * BN;
                     const int jn = mleft < BN ? (int)mleft : BN;
                     if constexpr (EK != kEpPlain) {
+                        // The slot comes back through the warp's staging
+                        // slots, 16 tokens x its 32 rows each, `ring` copies
+                        // ahead, and with it an aligned residual (then half
+                        // of the slots are its): one round trip per tile
+                        // instead of one per slice (64000 -> FINAL_CYCLES cycles for
+                        // 192 tokens with a residual).
                         constexpr int S = kEpSums<EK>;
+                        const int nq = (jn + 15) >> 4;
+                        const bool res_ring = EK == kEpLinear && p.res && p.y_tma;
+                        const int ring = res_ring ? C::kEpSlots / 2 : C::kEpSlots;
+                        const uint32_t stg_a = ptx::smem_u32(stg_w);
+                        const int es = ep::elem_size(p.dtype);
+                        auto fetch = [&](int q) {
+                            if (q < nq) {
+                                // 16-byte piece `lane` of every group of four
+                                // tokens; tokens past jn: zeros of the slot
+                                const uint32_t to = stg_a + (uint32_t)(q % ring) * (16 * 32 * 4);
+                                const int32_t* from = wsl + (16 * q + (lane >> 3)) * SHERRY_TILE_ROWS + 32 * quad + 4 * (lane & 7);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    ptx::cp_async16(to + (uint32_t)(k * 4 * 32 * 4 + 16 * lane), from + k * (4 * SHERRY_TILE_ROWS));
+                                if constexpr (EK == kEpLinear) {
+                                    if (res_ring) {
+                                        // rows of 32 es bytes: 2 es pieces each, whole inside the residual or outside
+                                        const uint32_t rto = to + (uint32_t)ring * (16 * 32 * 4);
+                                        const int64_t c0 = tn * SHERRY_TILE_ROWS + quad * 32;
+                                        for (int i = lane; i < 16 * 2 * es; i += 32) {
+                                            const int t = i / (2 * es), piece = i - t * (2 * es);
+                                            const int64_t m = cur_tm * BN + 16 * q + t, c = c0 + piece * (16 / es);
+                                            if (m < p.Mo && c < p.No)
+                                                ptx::cp_async16(rto + 16u * (uint32_t)i,
+                                                                static_cast<const char*>(p.res) + (m * p.No + c) * es);
+                                        }
+                                    }
+                                }
+                            }
+                            ptx::cp_async_commit();
+                        };
+                        if (lane == 0) ptx::bulk_wait_group_read<0>();   // earlier output stores left the slots
+                        __syncwarp();
 #pragma unroll 1
-                        for (int j = 0; j < jn; j += S) {
-                            uint32_t u[S];
+                        for (int q = 0; q < ring; ++q) fetch(q);
+#pragma unroll 1
+                        for (int q = 0; q < nq; ++q) {
+                            if (ring == 4) ptx::cp_async_wait_group<3>();
+                            else if (ring == 2) ptx::cp_async_wait_group<1>();
+                            else ptx::cp_async_wait_group<0>();
+                            __syncwarp();                    // every lane's pieces are in
+                            const float* slot_f = stg_w + (q % ring) * (16 * 32);
+                            const float* slot_r = res_ring ? slot_f + ring * (16 * 32) : nullptr;
+                            const int re = p.dtype == SHERRY_F32 ? 32 : 16;   // floats of a staged residual row
+#pragma unroll 1
+                            for (int j = 0; j < 16; j += S) {
+                                uint32_t u[S];
 #pragma unroll
-                            for (int i = 0; i < S; ++i)
-                                u[i] = (j + i < jn) ? (uint32_t)__ldcg(wsl + (j + i) * SHERRY_TILE_ROWS + r) : 0u;
-                            if constexpr (EK != kEpGrad) ep_keep<S>(p, u, cur_tm * BN + j, n);
-                            ep_store<EK, D, S>(p, u, sc_s + j / D, al, bi, lane, (cur_tm * BN + j) / D, col);
-#pragma unroll
-                            for (int i = 0; i < S; ++i)
-                                if (j + i < jn) wsl[(j + i) * SHERRY_TILE_ROWS + r] = 0;
+                                for (int i = 0; i < S; ++i) {
+                                    u[i] = __float_as_uint(slot_f[(j + i) * 32 + lane]);
+                                    if (16 * q + j + i < jn) wsl[(16 * q + j + i) * SHERRY_TILE_ROWS + r] = 0;
+                                }
+                                const int64_t m0 = cur_tm * BN + 16 * q + j;
+                                if constexpr (EK != kEpGrad) ep_keep<S>(p, u, m0, n);
+                                ep_store<EK, D, S>(p, u, sc_s + (16 * q + j) / D, al, bi, lane, m0 / D, col,
+                                                   slot_r ? slot_r + j * re : nullptr);
+                            }
+                            __syncwarp();                    // every lane has read the slot
+                            fetch(q + ring);
                         }
+                        ptx::cp_async_wait_group<0>();
+                        __syncwarp();
                     } else {
                         for (int j0 = 0; j0 < jn; j0 += 16) {
                             int32_t v[16];
