@@ -314,10 +314,10 @@ __device__ __forceinline__ void ep_keep(const EpParams& p, const uint32_t (&v)[S
 // ep_values of S sums, stored element by element: output rows from m0 on,
 // column col (out of range: not stored).  The residual is loaded whole before
 // the first store (it may be the output itself, so a load could not pass a
-// store on its own), from staged [token][32 columns] when given.
+// store on its own).
 template <int EK, int D, int S>
 __device__ __forceinline__ void ep_store(const EpParams& p, const uint32_t (&v)[S], const float* sc, float al,
-                                         float bi, int lane, int64_t m0, int64_t col, const float* staged = nullptr)
+                                         float bi, int lane, int64_t m0, int64_t col)
 {
     constexpr int O = EK == kEpGated ? S / 2 : S / D;
     constexpr int kStep = EK == kEpGated ? 2 : 1;            // output rows between values
@@ -329,12 +329,7 @@ __device__ __forceinline__ void ep_store(const EpParams& p, const uint32_t (&v)[
     // as read, widened only when added: all loads are in flight at once
     [[maybe_unused]] uint32_t rs[EK == kEpLinear ? O : 1];
     if constexpr (EK == kEpLinear) {
-        if (staged) {
-#pragma unroll
-            for (int i = 0; i < O; ++i)
-                rs[i] = p.dtype == SHERRY_F32 ? __float_as_uint(staged[i * 32 + lane])
-                                              : reinterpret_cast<const uint16_t*>(staged)[i * 32 + lane];
-        } else if (p.res) {
+        if (p.res) {
             const char* r = static_cast<const char*>(p.res) + at;
             if (p.dtype == SHERRY_F32) load_strided<O, uint32_t>(r, stride, cnt, rs);
             else load_strided<O, uint16_t>(r, stride, cnt, rs);
@@ -358,6 +353,40 @@ __device__ __forceinline__ void ep_store(const EpParams& p, const uint32_t (&v)[
 #pragma unroll
         for (int i = 0; i < O; ++i) h[i] = ep::to16(o[i], p.dtype);
         store_strided<O, uint16_t>(base, stride, cnt, h);
+    }
+}
+
+// ep_values of S sums into a staging slot of 16 sums x 32 rows (sums part ..
+// part + S - 1 of the slot): outputs [token][column], replacing the residual
+// there in place when has_res.
+template <int EK, int D, int S>
+__device__ __forceinline__ void ep_stage(const EpParams& p, const uint32_t (&v)[S], const float* sc, float al,
+                                         float bi, int lane, float* stg, int part, bool has_res)
+{
+    constexpr int O = EK == kEpGated ? S / 2 : S / D;
+    constexpr int OW = EK == kEpGated ? 16 : 32;             // columns of the slot
+    constexpr int kStep = EK == kEpGated ? 2 * OW : OW;
+    float o[O];
+    ep_values<EK, D, S, O>(p, v, sc, al, bi, lane, o);
+    const int at0 = part / D * OW + (EK == kEpGated ? (lane & 1) * OW + (lane >> 1) : lane);
+    if (p.dtype == SHERRY_F32) {
+        if (has_res) {
+#pragma unroll
+            for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], stg[at0 + i * kStep]);
+        }
+#pragma unroll
+        for (int i = 0; i < O; ++i) stg[at0 + i * kStep] = o[i];
+    } else {
+        uint16_t* st16 = reinterpret_cast<uint16_t*>(stg);
+        if (has_res) {
+            uint16_t h[O];
+#pragma unroll
+            for (int i = 0; i < O; ++i) h[i] = st16[at0 + i * kStep];
+#pragma unroll
+            for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], ep::from16(h[i], p.dtype));
+        }
+#pragma unroll
+        for (int i = 0; i < O; ++i) st16[at0 + i * kStep] = ep::to16(o[i], p.dtype);
     }
 }
 
@@ -972,22 +1001,18 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             int32_t* wsl = p.ws + slot * (int64_t)BN * SHERRY_TILE_ROWS;
             if constexpr (EK != kEpPlain) {
                 if (via_tma) {
-                    // As below, in slices of 16 sums x OW output columns with
+                    // As below, in slices of 16 sums x 32 rows with
                     // kEpSlots staging slots per warp.  A residual box is loaded by TMA into
                     // the slot its outputs will take, up to kEpSlots - 1
                     // slices ahead (the first ones before the accumulators are
                     // complete), and replaced in place.
-                    constexpr int OW = EK == kEpGated ? 16 : 32;
                     constexpr int S = kEpSums<EK>;
-                    constexpr int O = EK == kEpGated ? S / 2 : S / D;
-                    const int scol = EK == kEpGated ? lane >> 1 : lane;
 #pragma unroll 1
                     for (int q = 0; q < nslices; ++q) {
                         const int j0 = 16 * q;
                         const int64_t m0 = (tm * BN + j0) / D;
                         const uint32_t slot = stage_slice % C::kEpSlots;
                         float* stg = stg_w + slot * (16 * 32);
-                        uint16_t* st16 = reinterpret_cast<uint16_t*>(stg);
                         if (has_res) {
                             if constexpr (EK == kEpLinear) {
                                 // every box issued is waited for; after a wait
@@ -1014,28 +1039,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                             else ptx::tmem_ld_32x32b_x8(lane_base + (uint32_t)(d * BN + j0 + part), v);
                             ptx::tmem_wait_ld_of(v);
                             if constexpr (EK != kEpGrad) ep_keep<S>(p, v, m0 + part, n);
-                            float o[O];
-                            ep_values<EK, D, S, O>(p, v, sc_s + (j0 + part) / D, al, bi, lane, o);
-                            const int at0 = part * OW + (EK == kEpGated ? (lane & 1) * OW : 0) + scol;
-                            constexpr int kStep = EK == kEpGated ? 2 * OW : OW;
-                            if (p.dtype == SHERRY_F32) {
-                                if (has_res) {
-#pragma unroll
-                                    for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], stg[at0 + i * kStep]);
-                                }
-#pragma unroll
-                                for (int i = 0; i < O; ++i) stg[at0 + i * kStep] = o[i];
-                            } else {
-                                if (has_res) {
-                                    uint16_t h[O];
-#pragma unroll
-                                    for (int i = 0; i < O; ++i) h[i] = st16[at0 + i * kStep];
-#pragma unroll
-                                    for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], ep::from16(h[i], p.dtype));
-                                }
-#pragma unroll
-                                for (int i = 0; i < O; ++i) st16[at0 + i * kStep] = ep::to16(o[i], p.dtype);
-                            }
+                            ep_stage<EK, D, S>(p, v, sc_s + (j0 + part) / D, al, bi, lane, stg, part, has_res);
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
@@ -1151,31 +1155,35 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                     const int64_t mleft = p.M - cur_tm * BN;
                     const int jn = mleft < BN ? (int)mleft : BN;
                     if constexpr (EK != kEpPlain) {
-                        // The slot comes back through the warp's staging
-                        // slots, 16 tokens x its 32 rows each, `ring` copies
-                        // ahead, and with it an aligned residual (then half
-                        // of the slots are its): one round trip per tile
-                        // instead of one per slice (64000 -> FINAL_CYCLES cycles for
-                        // 192 tokens with a residual).
+                        // The sums come back through the first half of the
+                        // warp's staging slots, 16 tokens x its 32 rows each,
+                        // one slice ahead, and with them an aligned residual
+                        // into the second half, where the outputs then take
+                        // its place and leave through TMA stores (unaligned
+                        // ones element by element).  192 tokens with a
+                        // residual: 64000 cycles when every slice waited for
+                        // its sums and its residual, FINAL_CYCLES so.
                         constexpr int S = kEpSums<EK>;
+                        constexpr int kRing = C::kEpSlots / 2;
+                        constexpr int kSlotFloats = 16 * 32;
                         const int nq = (jn + 15) >> 4;
-                        const bool res_ring = EK == kEpLinear && p.res && p.y_tma;
-                        const int ring = res_ring ? C::kEpSlots / 2 : C::kEpSlots;
+                        const bool res_in = EK == kEpLinear && p.res && p.y_tma;
                         const uint32_t stg_a = ptx::smem_u32(stg_w);
                         const int es = ep::elem_size(p.dtype);
+                        const int piece0 = (lane >> 3) * SHERRY_TILE_ROWS + 32 * quad + 4 * (lane & 7);
                         auto fetch = [&](int q) {
                             if (q < nq) {
                                 // 16-byte piece `lane` of every group of four
                                 // tokens; tokens past jn: zeros of the slot
-                                const uint32_t to = stg_a + (uint32_t)(q % ring) * (16 * 32 * 4);
-                                const int32_t* from = wsl + (16 * q + (lane >> 3)) * SHERRY_TILE_ROWS + 32 * quad + 4 * (lane & 7);
+                                const uint32_t to = stg_a + (uint32_t)(q % kRing) * (kSlotFloats * 4);
+                                const int32_t* from = wsl + 16 * q * SHERRY_TILE_ROWS + piece0;
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     ptx::cp_async16(to + (uint32_t)(k * 4 * 32 * 4 + 16 * lane), from + k * (4 * SHERRY_TILE_ROWS));
                                 if constexpr (EK == kEpLinear) {
-                                    if (res_ring) {
+                                    if (res_in) {
                                         // rows of 32 es bytes: 2 es pieces each, whole inside the residual or outside
-                                        const uint32_t rto = to + (uint32_t)ring * (16 * 32 * 4);
+                                        const uint32_t rto = to + (uint32_t)kRing * (kSlotFloats * 4);
                                         const int64_t c0 = tn * SHERRY_TILE_ROWS + quad * 32;
                                         for (int i = lane; i < 16 * 2 * es; i += 32) {
                                             const int t = i / (2 * es), piece = i - t * (2 * es);
@@ -1191,34 +1199,48 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                         };
                         if (lane == 0) ptx::bulk_wait_group_read<0>();   // earlier output stores left the slots
                         __syncwarp();
-#pragma unroll 1
-                        for (int q = 0; q < ring; ++q) fetch(q);
+                        fetch(0);
 #pragma unroll 1
                         for (int q = 0; q < nq; ++q) {
-                            if (ring == 4) ptx::cp_async_wait_group<3>();
-                            else if (ring == 2) ptx::cp_async_wait_group<1>();
-                            else ptx::cp_async_wait_group<0>();
+                            if constexpr (kRing > 1) {
+                                // into the slots of slice q - 1: its sums are
+                                // read, its outputs gone once their store has read them
+                                if (lane == 0) ptx::bulk_wait_group_read<0>();
+                                __syncwarp();
+                                fetch(q + 1);
+                                ptx::cp_async_wait_group<1>();
+                            } else {
+                                ptx::cp_async_wait_group<0>();
+                            }
                             __syncwarp();                    // every lane's pieces are in
-                            const float* slot_f = stg_w + (q % ring) * (16 * 32);
-                            const float* slot_r = res_ring ? slot_f + ring * (16 * 32) : nullptr;
-                            const int re = p.dtype == SHERRY_F32 ? 32 : 16;   // floats of a staged residual row
+                            const float* in = stg_w + (q % kRing) * kSlotFloats;
+                            float* stg = stg_w + (kRing + q % kRing) * kSlotFloats;
+                            const int64_t m0 = cur_tm * BN + 16 * q;
 #pragma unroll 1
-                            for (int j = 0; j < 16; j += S) {
+                            for (int part = 0; part < 16; part += S) {
                                 uint32_t u[S];
 #pragma unroll
-                                for (int i = 0; i < S; ++i) {
-                                    u[i] = __float_as_uint(slot_f[(j + i) * 32 + lane]);
-                                    if (16 * q + j + i < jn) wsl[(16 * q + j + i) * SHERRY_TILE_ROWS + r] = 0;
-                                }
-                                const int64_t m0 = cur_tm * BN + 16 * q + j;
-                                if constexpr (EK != kEpGrad) ep_keep<S>(p, u, m0, n);
-                                ep_store<EK, D, S>(p, u, sc_s + (16 * q + j) / D, al, bi, lane, m0 / D, col,
-                                                   slot_r ? slot_r + j * re : nullptr);
+                                for (int i = 0; i < S; ++i) u[i] = __float_as_uint(in[(part + i) * 32 + lane]);
+                                if constexpr (EK != kEpGrad) ep_keep<S>(p, u, m0 + part, n);
+                                const float* sc = sc_s + (16 * q + part) / D;
+                                if (p.y_tma) ep_stage<EK, D, S>(p, u, sc, al, bi, lane, stg, part, res_in);
+                                else ep_store<EK, D, S>(p, u, sc, al, bi, lane, (m0 + part) / D, col);
                             }
-                            __syncwarp();                    // every lane has read the slot
-                            fetch(q + ring);
+                            // the slot's words are zero again for the next call
+                            int4* z = reinterpret_cast<int4*>(wsl + 16 * q * SHERRY_TILE_ROWS + piece0);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) z[k * SHERRY_TILE_ROWS] = make_int4(0, 0, 0, 0);
+                            if (p.y_tma) ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (p.y_tma && lane == 0) {
+                                ptx::tma_store_2d(&ymap.out, out_x, (int32_t)(m0 / D), ptx::smem_u32(stg));
+                                ptx::bulk_commit_group();
+                            }
+                            if constexpr (kRing == 1) fetch(q + 1);
                         }
+                        // whole tiles take the slots in an order of their own
                         ptx::cp_async_wait_group<0>();
+                        if (lane == 0) ptx::bulk_wait_group_read<0>();
                         __syncwarp();
                     } else {
                         for (int j0 = 0; j0 < jn; j0 += 16) {
