@@ -253,7 +253,7 @@ double epilogue_weight(const tc::EpParams& p, bool gated)
                        : p.act == SHERRY_ACT_GELU                                ? 0.7
                                                                                  : 0.55;
     const double w = 1.0 + act + (p.res ? 0.5 : 0.0) + (p.dtype == SHERRY_F32 ? 0.3 : 0.0) + (p.acc ? 0.4 : 0.0);
-    return gated ? 0.55 * w : w;
+    return gated ? 0.75 * w : w;
 }
 
 template <int EK>
