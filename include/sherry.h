@@ -443,7 +443,8 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  * shape or on the order of any sum across blocks: the same call gives the
  * same bits.
  * Tensors are dense row-major.  Workspace, concurrency and errors are those
- * of sherry_linear; an output may not overlap an input, except y == residual.
+ * of sherry_linear.  An output that overlaps an input or another output is
+ * refused, but for y == residual.
  * =========================================================================== */
 
 /* sherry_quant_act for x of any element type (x [M][K], 16-byte aligned). */
@@ -470,7 +471,7 @@ int sherry_repack_gated(const uint8_t* gate_dev, const uint8_t* up_dev, int64_t 
  *            sherry_linear_ex: given, they hold the quantised activations;
  *            x_i8 == NULL uses the reserved buffer.  x_scale alone may be
  *            given (kept for the gradient).
- * Wnative, alpha, and what may run before the call: as sherry_linear_ex; bias
+ * Wnative and what may run before the call: as sherry_linear_ex; alpha, bias
  * and residual may be written by the kernel launched just before.
  */
 int sherry_linear_epilogue(const void* x, int x_dtype, const void* Wnative, const float* alpha,

@@ -444,7 +444,7 @@ def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q,
         op = out.data_ptr()
     if M == 0:
         return out
-    if M > 1 and qp is None or qp is not None and sp is None:
+    if qp is None and (M > 1 or K > 65536) or qp is not None and sp is None:
         # the call's own buffer for the int8 activations and their scales: nothing is shared with other
         # streams or graphs
         own = w_native.new_empty(M * K + 4 * M)         # K % 32 == 0: the scales are aligned

@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     const int fpi = (R4 > 0 && tid < P * R4) ? tid % R4 : -1;
     const int fpart = R4 > 0 ? tid / R4 : 0;
     const int first = CPT < NS ? CPT : NS;                 // steps fetched before the wait
-    {
+    if constexpr (!EP) {
         const uint32_t alpha_s = s_base + off_alpha(M, P, R);
         for (int ii = tid; ii < Rc; ii += nthr) cp_async4(alpha_s + 4u * (uint32_t)ii, p.alpha + r0 + ii);
     }
@@ -627,6 +627,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
         else ptx::sts_u32(tab.addr + 4u * (uint32_t)tid, expand_code((uint32_t)tid));
     }
     ptx::pdl_wait();
+    // EP: alpha may be what the previous kernel wrote (the scales of a layer in
+    // training), so it is read after the wait, beside the activations
+    [[maybe_unused]] float first_alpha = 0.0f;
+    if constexpr (EP) first_alpha = tid < Rc ? p.alpha[r0 + tid] : 0.0f;
 
     // ---- activations -------------------------------------------------------------
     // qbuf holds token m's K chunk c at byte m * QK + c * S.
@@ -647,6 +651,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
                 *reinterpret_cast<uint4*>(qbuf + m * QK + (i >> 3) * S + 16 * (i & 7)) = v;
             }
         if (tid < M) scale_s[tid] = p.x_scale[tid];
+    }
+    if constexpr (EP) {
+        float* alpha_w = reinterpret_cast<float*>(smem + off_alpha(M, P, R));
+        if (tid < Rc) alpha_w[tid] = first_alpha;
+        for (int ii = tid + nthr; ii < Rc; ii += nthr) alpha_w[ii] = p.alpha[r0 + ii];
     }
     // zero the activation tail of the last chunk: its padding codes decode to nonzero weights
     {

@@ -172,6 +172,13 @@ bool aligned_elem(const void* p, int dtype)
     return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(ep::elem_size(dtype) - 1)) == 0;
 }
 
+// Whether two buffers share a byte (null: no).
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 // out [Mo][No]: boxes of box_n columns x box_m rows, for complete tiles
 int make_out_map(CUtensorMap* map, void* out, int dtype, int64_t Mo, int64_t No, int box_n, int box_m)
 {
@@ -334,6 +341,10 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     if (!sherry_shape_ok(M, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x) || !aligned16(wn) || (x_i8 && !aligned16(x_i8))) return SHERRY_ERR_INVALID_ARG;
     if (!aligned_elem(out, dtype) || (res && !aligned_elem(res, dtype))) return SHERRY_ERR_INVALID_ARG;
+    const int64_t es = ep::elem_size(dtype), xb = M * K * es, ob = M * No * es, ab = 4 * M * R;
+    if (overlap(out, ob, x, xb) || (out != res && overlap(out, ob, res, ob)) || overlap(acc, ab, x, xb) ||
+        overlap(acc, ab, out, ob) || overlap(acc, ab, res, ob) || overlap(x_i8, M * K, x, xb) || overlap(x_i8, M * K, out, ob))
+        return SHERRY_ERR_INVALID_ARG;
     DeviceInfo di;
     int st = device_info(&di);
     if (st != SHERRY_OK) return st;
@@ -422,6 +433,11 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     if (!sherry_shape_ok(M, R, K) || R > kGradMaxRows || M > SHERRY_MAX_DIM / 4) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned_elem(dy, dtype) || (reinterpret_cast<uintptr_t>(acc) & 7u)) return SHERRY_ERR_INVALID_ARG;
     if (dx && (!aligned16(wt) || !aligned16(work) || !aligned_elem(dx, dtype))) return SHERRY_ERR_INVALID_ARG;
+    const int64_t es = ep::elem_size(dtype), yb = M * No * es, xb = M * K * es, rb = 4 * R;
+    if (overlap(dx, xb, dy, yb) || overlap(dx, xb, acc, M * rb) || overlap(dalpha, rb, alpha, rb) ||
+        overlap(dalpha, rb, bias, rb) || overlap(dbias, rb, alpha, rb) || overlap(dbias, rb, bias, rb) ||
+        overlap(dalpha, rb, dbias, rb))
+        return SHERRY_ERR_INVALID_ARG;
     DeviceInfo di;
     int st = device_info(&di);
     if (st != SHERRY_OK) return st;

@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 
 }
 
 // Both in one launch, for few tokens, where a launch costs more than the work
-// (M=5 K=1024, gated to 2816, bf16: 13.6 -> BOTH_US us for the call): clusters of
+// (M=5 K=1024, gated to 2816, bf16: 13.6 -> 11.3 us for the call, 21.9 -> 19.2 us with the host): clusters of
 // `cluster` blocks, the first `tokens` of them (all M, or none) the tokens'
 // digits, the others column sums, whose order does not depend on whether the
 // digits are wanted.

@@ -962,8 +962,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             [[maybe_unused]] bool has_res = false;
             [[maybe_unused]] int res_upto = 0;         // slices whose residual box was issued
             if constexpr (EK == kEpLinear) {
-                has_res = via_tma && p.res;
-                has_res = has_res && res_ok;
+                has_res = via_tma && p.res && res_ok;
                 if (has_res) {
                     res_upto = nslices < C::kEpSlots - 1 ? nslices : C::kEpSlots - 1;
                     if (lane == 0) {
@@ -1001,11 +1000,11 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             int32_t* wsl = p.ws + slot * (int64_t)BN * SHERRY_TILE_ROWS;
             if constexpr (EK != kEpPlain) {
                 if (via_tma) {
-                    // As below, in slices of 16 sums x 32 rows with
-                    // kEpSlots staging slots per warp.  A residual box is loaded by TMA into
-                    // the slot its outputs will take, up to kEpSlots - 1
-                    // slices ahead (the first ones before the accumulators are
-                    // complete), and replaced in place.
+                    // As below, in slices of 16 sums x 32 rows with kEpSlots
+                    // staging slots per warp.  A residual box is loaded by
+                    // TMA into the slot its outputs will take, up to
+                    // kEpSlots - 1 slices ahead (the first ones before the
+                    // accumulators are complete), and replaced in place.
                     constexpr int S = kEpSums<EK>;
 #pragma unroll 1
                     for (int q = 0; q < nslices; ++q) {
@@ -1161,8 +1160,9 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                         // into the second half, where the outputs then take
                         // its place and leave through TMA stores (unaligned
                         // ones element by element).  192 tokens with a
-                        // residual: 64000 cycles when every slice waited for
-                        // its sums and its residual, FINAL_CYCLES so.
+                        // residual: 64000 cycles beside the decoders when every
+                        // slice waited for its sums and its residual, 44000
+                        // so.
                         constexpr int S = kEpSums<EK>;
                         constexpr int kRing = C::kEpSlots / 2;
                         constexpr int kSlotFloats = 16 * 32;

@@ -150,3 +150,30 @@ def test_block_shapes_must_chain(lib):
         sbm.GatedFFN.from_weights(W, W, np.ones((32, 32), dtype=np.float32))
     with pytest.raises(ValueError):
         sbm.GatedFFN.from_weights(W, W, np.ones((32, 64), dtype=np.float32), act="tanh")
+
+
+def test_overlapping_buffers_are_refused(lib):
+    L = sbm.load()
+    at = lambda k: ctypes.c_void_p((1 << 20) + k)  # noqa: E731
+    # bf16, M = 2, K = 32, N = 4: x 128 bytes, y and residual 16, acc 32
+    far = at(1 << 16)
+    kw = dict(M=2, N=4, K=32, x=at(0), y=far)
+    for bad in (dict(kw, y=at(0)), dict(kw, y=at(126)), dict(kw, acc=at(64)), dict(kw, acc=far),
+                dict(kw, res=at((1 << 16) + 2)), dict(kw, q=at(16), s=at(1 << 17)), dict(kw, res=at(1 << 18), acc=at(1 << 18))):
+        assert _linear(L, **bad) == INVALID, bad
+    kw = dict(M=2, N=4, K=32, dy=at(0), dx=far, acc=at(1 << 17), da=at(1 << 18), db=at(1 << 19), alpha=at(1 << 21),
+              work=at(1 << 22), wt=at(1 << 23), s=at(1 << 24))
+    for bad in (dict(kw, dx=at(0)), dict(kw, dx=at((1 << 17) + 16)), dict(kw, da=at(1 << 21)), dict(kw, db=at((1 << 18) + 8)),
+                dict(kw, bias=at(1 << 18)), dict(kw, bias=at((1 << 19) - 4))):
+        assert _grad(L, "sherry_linear_grad", **bad) == INVALID, bad
+
+
+def test_feed_forward_sources_never_allocate_or_synchronise():
+    """The asynchronous entry points of ffn_cuda.cu and grad_cuda.cu call nothing that allocates, frees,
+    clears or waits."""
+    import os
+    import re
+    src = os.path.join(os.path.dirname(sbm.SO_PATH), "csrc")
+    for name in ("ffn_cuda.cu", "grad_cuda.cu", "host_common.h", "tile_plan.h"):
+        text = open(os.path.join(src, name)).read()
+        assert not re.search(r"cuda(Malloc|Free|Memset|Memcpy|DeviceSynchronize|StreamSynchronize|EventSynchronize)", text), name

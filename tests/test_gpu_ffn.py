@@ -188,6 +188,83 @@ def test_binding_refusals():
         sbm.linear_backward(dy, w_t, alpha, 160, want_dx=False, want_scales=False)
 
 
+def test_one_token_of_a_very_long_row():
+    """K beyond what the decode kernel holds: quantiser and tensor cores."""
+    run_forward(False, 1, 700000, 8, "bf16", "none", True, True)
+    run_forward(True, 1, 700000, 4, "f32", "silu", False, False)
+
+
+def test_scales_written_just_before():
+    """alpha, bias and residual written by the kernel launched just before the call."""
+    for M in (1, 2, 40):
+        native, _, alpha, _ = weight(256, 288, True)
+        x = rand(M, 288, seed=M, dtype=torch.bfloat16)
+        a, b = torch.zeros_like(alpha), torch.zeros_like(alpha)
+        want = sbm.gated(x, native, alpha * 3, 128, bias=alpha)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            a.copy_(alpha).mul_(3)
+            b.copy_(alpha)
+            y = sbm.gated(x, native, a, 128, bias=b)
+            a.zero_()
+            assert torch.equal(y, want)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 outputs, sums and digits: the last tokens and rows are right."""
+    M, K, N = 65537, 32, 33000
+    native, w_t, alpha, T = weight(N, K, False)
+    x = rand(M, K, seed=1, dtype=torch.bfloat16)
+    s = torch.empty(M, device="cuda")
+    acc = torch.empty(M, N, dtype=torch.int32, device="cuda")
+    y = sbm.linear_epilogue(x, native, alpha, N, act="relu", acc=acc, out_s=s)
+    assert y.numel() > 2 ** 31
+    for at in (slice(0, 3), slice(M // 2, M // 2 + 3), slice(M - 3, M)):
+        acc_o, s_o, _ = exact_sums(x[at], T)
+        assert torch.equal(acc[at].double(), acc_o) and torch.equal(s[at], s_o)
+        want, bound = F.forward(acc_o, alpha.double(), s_o.double(), None, "relu", False, None, torch.bfloat16)
+        F.assert_within(y[at], want, bound, "y")
+    y.normal_(std=0.1, generator=torch.Generator(device="cuda").manual_seed(3))
+    dx, da, db = sbm.linear_backward(y, w_t, alpha, K, acc, s, act="relu")
+    for at in (slice(0, 3), slice(M - 3, M)):
+        want, bound = F.gradients(T, acc[at].double(), alpha.double(), s[at].double(), None, "relu", False, y[at].double(),
+                                  torch.bfloat16)
+        F.assert_within(dx[at], want[0], bound[0], "dx")
+    cols = torch.tensor([0, 1, N - 2, N - 1], device="cuda")
+    want, bound = F.gradients(T[cols], acc[:, cols].double(), alpha[cols].double(), s.double(), None, "relu", False,
+                              y[:, cols].double(), torch.bfloat16)
+    F.assert_within(da[cols], want[1], bound[1], "dalpha")
+    F.assert_within(db[cols], want[2], bound[2], "dbias")
+
+
+def test_calls_allocate_nothing():
+    """After the workspace is set aside, first calls of the C entry points leave the device's free memory
+    as it was (buffers are the caller's)."""
+    sbm.reserve_split()
+    L = sbm.load()
+    st = torch.cuda.current_stream().cuda_stream
+    native, w_t, alpha, _ = weight(512, 1056, True)
+    M, K, N = 90, 1056, 256
+    x = rand(M, K, dtype=torch.bfloat16)
+    h, dx = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x)
+    acc, q = torch.empty(M, 512, dtype=torch.int32, device="cuda"), torch.empty(M, K, dtype=torch.int8, device="cuda")
+    s, da, db = torch.empty(M, device="cuda"), torch.empty(512, device="cuda"), torch.empty(512, device="cuda")
+    work = torch.empty(L.sherry_grad_work_bytes(1, M, 512), dtype=torch.uint8, device="cuda")
+
+    def both():
+        assert L.sherry_gated(x.data_ptr(), 1, native.data_ptr(), alpha.data_ptr(), None, 3, h.data_ptr(), acc.data_ptr(),
+                              q.data_ptr(), s.data_ptr(), M, N, K, st) == sbm.OK
+        assert L.sherry_gated_grad(h.data_ptr(), 1, acc.data_ptr(), s.data_ptr(), w_t.data_ptr(), alpha.data_ptr(), None, 3,
+                                   dx.data_ptr(), da.data_ptr(), db.data_ptr(), work.data_ptr(), M, N, K, st) == sbm.OK
+        torch.cuda.synchronize()
+
+    both()                                     # loads the kernels
+    free = torch.cuda.mem_get_info()[0]
+    for _ in range(3):
+        both()
+    assert torch.cuda.mem_get_info()[0] == free
+
+
 # ------------------------------------------------------------------ layouts
 @pytest.mark.parametrize("N,K", [(1, 32), (5, 96), (64, 128), (130, 160), (257, 1056)])
 def test_layouts(N, K):
