@@ -107,15 +107,19 @@ __device__ __forceinline__ void act_slope(float z, int act, float& f, float& d)
     if (act == SHERRY_ACT_NONE) {
         f = z;
         d = 1.0f;
-    } else if (act == SHERRY_ACT_SILU || act == SHERRY_ACT_GELU_TANH) {
-        // d/dz [z S(t)] = S + z S (1 - S) t',  t' = 1 or c1 + 3 c3 z^2
-        const bool silu = act == SHERRY_ACT_SILU;
-        const float s = logistic(sigmoid_arg(z, silu));
-        const float t1 = silu ? 1.0f : __fmaf_rn(__fmul_rn(z, z), 3.0f * kGeluC3, kGeluC1);
+    } else if (act == SHERRY_ACT_SILU) {
+        // d/dz [z S(z)] = S + z S (1 - S)
+        const float s = logistic(z);
         f = __fmul_rn(z, s);
-        // a far z: z^2 may overflow where S (1 - S) is 0
-        const float w = __fmul_rn(s, __fsub_rn(1.0f, s));
-        d = w == 0.0f ? s : __fmaf_rn(__fmul_rn(z, w), t1, s);
+        d = __fmaf_rn(f, __fsub_rn(1.0f, s), s);
+    } else if (act == SHERRY_ACT_GELU_TANH) {
+        // d/dz [z S(t)] = S + z S (1 - S) t',  t' = c1 + 3 c3 z^2; a far z:
+        // z^2 may overflow where S (1 - S) is 0
+        const float s = logistic(sigmoid_arg(z, false));
+        const float t1 = __fmaf_rn(__fmul_rn(z, z), 3.0f * kGeluC3, kGeluC1);
+        f = __fmul_rn(z, s);
+        const float w = __fmul_rn(f, __fsub_rn(1.0f, s));
+        d = w == 0.0f ? s : __fmaf_rn(w, t1, s);
     } else if (act == SHERRY_ACT_GELU) {
         // d/dz [z Phi(z)] = Phi + z phi
         const float phi_cdf = __fmul_rn(0.5f, __fadd_rn(1.0f, erff(__fmul_rn(z, kSqrtHalf))));
