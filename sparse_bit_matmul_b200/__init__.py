@@ -321,9 +321,7 @@ def _refuse(name: str, t, want: str):
 
 
 def _ptr(t, name: str, dtype, shape, idx: int):
-    """Data pointer of a tensor argument of the given type and shape on device idx (None: NULL)."""
-    if t is None:
-        return None
+    """Data pointer of a tensor argument of the given type and shape on device idx."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
         _refuse(name, t, f"{dtype} {shape} on cuda:{idx}")
     return t.data_ptr()
@@ -429,19 +427,21 @@ def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q,
     if N <= 0 or K <= 0 or K % 32:
         raise ValueError(f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
     R = 2 * N if gated else N
-    wp = _ptr(w_native, "w_native", _torch.uint8, (-(-R // 128) * -(-K // 128) * 2560,), idx)
-    ap = _ptr(alpha, "alpha", _torch.float32, (R,), idx)
-    if wp is None or ap is None:
+    if w_native is None or alpha is None:
         raise ValueError("w_native and alpha are needed")
-    bp = _ptr(bias, "bias", _torch.float32, (R,), idx)
-    rp = _ptr(residual, "residual", x.dtype, (M, N), idx)
-    cp = _ptr(acc, "acc", _torch.int32, (M, R), idx)
-    qp = _ptr(out_q, "out_q", _torch.int8, (M, K), idx)
-    sp = _ptr(out_s, "out_s", _torch.float32, (M,), idx)
-    op = _ptr(out, "out", x.dtype, (M, N), idx)
+    f32 = _torch.float32
+    wp = _ptr(w_native, "w_native", _torch.uint8, (-(-R // 128) * -(-K // 128) * 2560,), idx)
+    ap = _ptr(alpha, "alpha", f32, (R,), idx)
+    bp = None if bias is None else _ptr(bias, "bias", f32, (R,), idx)
+    rp = None if residual is None else _ptr(residual, "residual", x.dtype, (M, N), idx)
+    cp = None if acc is None else _ptr(acc, "acc", _torch.int32, (M, R), idx)
+    qp = None if out_q is None else _ptr(out_q, "out_q", _torch.int8, (M, K), idx)
+    sp = None if out_s is None else _ptr(out_s, "out_s", f32, (M,), idx)
     if out is None:
         out = x.new_empty((M, N))
         op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", x.dtype, (M, N), idx)
     if M == 0:
         return out
     if qp is None and (M > 1 or K > 65536) or qp is not None and sp is None:
@@ -495,18 +495,16 @@ def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, w
     _need(acc is None or x_scale is not None, "x_scale: needed with acc")
     R = 2 * N if gated else N
     _need(alpha is not None and (w_t is not None or not want_dx), "alpha, and for dx w_t, are needed")
-    ap = _ptr(alpha, "alpha", _torch.float32, (R,), idx)
-    bp = _ptr(bias, "bias", _torch.float32, (R,), idx)
-    cp = _ptr(acc, "acc", _torch.int32, (M, R), idx)
-    sp = _ptr(x_scale, "x_scale", _torch.float32, (M,), idx)
+    f32 = _torch.float32
+    ap = _ptr(alpha, "alpha", f32, (R,), idx)
+    bp = None if bias is None else _ptr(bias, "bias", f32, (R,), idx)
+    cp = None if acc is None else _ptr(acc, "acc", _torch.int32, (M, R), idx)
+    sp = None if x_scale is None else _ptr(x_scale, "x_scale", f32, (M,), idx)
     dx = dalpha = dbias = wp = xp = kp = dap = dbp = None
     if want_dx:
         wp = _ptr(w_t, "w_t", _torch.uint8, (-(-R // 128) * -(-K // 128) * 4096,), idx)
-        xp = _ptr(out, "out", dy.dtype, (M, K), idx)
-        dx = out
-        if dx is None:
-            dx = dy.new_empty((M, K))
-            xp = dx.data_ptr()
+        dx = dy.new_empty((M, K)) if out is None else out
+        xp = dx.data_ptr() if out is None else _ptr(out, "out", dy.dtype, (M, K), idx)
     if want_scales:
         make = _torch.empty_like if M else _torch.zeros_like
         dalpha, dbias = make(alpha), make(alpha)
