@@ -213,9 +213,10 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
     p.U = p.TM * p.TN * p.Kc;
     const int64_t grid = plan.grid;
     p.whole = plan.whole;
+    p.cluster = plan.cluster;
     p.ws = nullptr;
     p.counters = nullptr;
-    if (!p.whole) {
+    if (!p.whole && !p.cluster) {
         void* ws = nullptr;
         const size_t ws_acc = (size_t)grid * BN * SHERRY_TILE_ROWS * sizeof(int32_t);
         st = get_workspace(ws_acc + (size_t)grid * sizeof(uint32_t), &ws);
@@ -248,7 +249,8 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (st != SHERRY_OK) return st;
-    return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream, map, maps, p));
+    return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream,
+                                  dim3((unsigned)std::max(1, plan.cluster)), map, maps, p));
 }
 
 // Weight of an epilogue for plan_tiles, beside a bare linear layer's: the

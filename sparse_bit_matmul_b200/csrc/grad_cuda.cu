@@ -17,27 +17,6 @@ constexpr int kSegMin = 1024;               // weight rows worth a block of thei
 constexpr int kSegMax = 8192;               // above, a block's 32 KB keep its neighbours off the SM
 constexpr int kClusterMax = 8;
 
-template <class... A, class... B>
-cudaError_t launch_cluster(void (*kernel)(A...), dim3 grid, dim3 cluster, int threads, size_t smem, cudaStream_t stream,
-                           B... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster.x;
-    attr[1].val.clusterDim.y = cluster.y;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Blocks that share the columns: of the cluster sizes that leave every warp
 // four tokens, the one whose last round of resident blocks is fullest; the
 // smallest such.
@@ -106,8 +85,8 @@ int digits(Params p, int sms, cudaStream_t stream)
         q.x_scale = p.x_scale ? p.x_scale + m0 : nullptr;
         q.dig = p.dig + m0 * kDigits<DT> * p.ld;
         q.dscale = p.dscale + m0;
-        const cudaError_t e = launch_cluster(kernel, dim3((unsigned)cx, (unsigned)n), dim3((unsigned)cx, 1), kDigitThreads,
-                                             (size_t)smem, stream, q);
+        const cudaError_t e = launch_pdl(kernel, dim3((unsigned)cx, (unsigned)n), dim3(kDigitThreads), (size_t)smem, stream,
+                                         dim3((unsigned)cx), q);
         if (e != cudaSuccess) return cuda_status(e);
     }
     return SHERRY_OK;
@@ -123,8 +102,8 @@ int both(Params p, bool dx, int sms, cudaStream_t stream)
     if (st != SHERRY_OK) return st;
     int c = 1;
     const int64_t smem = split_rows(p, sms, &c), tokens = dx ? p.M : 0;
-    return cuda_status(launch_cluster(kernel, dim3((unsigned)(c * (tokens + row_blocks(p.R)))), dim3((unsigned)c, 1),
-                                      kDigitThreads, (size_t)smem, stream, p, (uint32_t)tokens, (uint32_t)c));
+    return cuda_status(launch_pdl(kernel, dim3((unsigned)(c * (tokens + row_blocks(p.R)))), dim3(kDigitThreads),
+                                  (size_t)smem, stream, dim3((unsigned)c), p, (uint32_t)tokens, (uint32_t)c));
 }
 
 template <bool GATED, int ACT, int DT>
@@ -134,12 +113,12 @@ int columns(const Params& p, int sms, cudaStream_t stream)
     const unsigned bx = (unsigned)row_blocks(p.R);
     if (columns_wide(p.R, p.M, sms)) {
         const unsigned cy = (unsigned)std::min<int64_t>(kClusterMax, p.M / (4 * kColWarpsWide));
-        return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarpsWide>, dim3(bx, cy), dim3(1, cy),
-                                          32 * kColWarpsWide, 0, stream, p));
+        return cuda_status(launch_pdl(grad_columns_kernel<GATED, ACT, DT, kColWarpsWide>, dim3(bx, cy),
+                                      dim3(32 * kColWarpsWide), 0, stream, dim3(1, cy), p));
     }
     const unsigned cy = (unsigned)columns_cluster(p.R, p.M, sms);
-    return cuda_status(launch_cluster(grad_columns_kernel<GATED, ACT, DT, kColWarps>, dim3(bx, cy), dim3(1, cy),
-                                      32 * kColWarps, 0, stream, p));
+    return cuda_status(launch_pdl(grad_columns_kernel<GATED, ACT, DT, kColWarps>, dim3(bx, cy), dim3(32 * kColWarps), 0,
+                                  stream, dim3(1, cy), p));
 }
 
 template <bool GATED, int ACT, int DT>

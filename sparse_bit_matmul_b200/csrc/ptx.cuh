@@ -372,6 +372,11 @@ __device__ __forceinline__ void red_cluster_add_s32(uint32_t local_addr, uint32_
 {
     asm volatile("red.shared::cluster.add.s32 [%0], %1;" ::"r"(mapa(local_addr, cta)), "r"(v) : "memory");
 }
+// Adds v to the int32 at a cluster address (mapa).
+__device__ __forceinline__ void red_shared_cluster_add_s32(uint32_t addr, int32_t v)
+{
+    asm volatile("red.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // The float at `local_addr`'s offset in the shared memory of CTA `cta`.
 __device__ __forceinline__ float ld_cluster_f32(uint32_t local_addr, uint32_t cta)
 {

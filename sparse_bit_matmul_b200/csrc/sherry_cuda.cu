@@ -368,6 +368,7 @@ int launch_tc(const int8_t* x, const float* xs, const void* wn, const float* alp
     p.Kc = sherry_k_chunks(K);
     p.U = p.TM * p.TN * p.Kc;
     p.whole = 0;
+    p.cluster = 0;
     const int64_t grid = tc_grid(p.TM * p.TN, p.U, di.sms, p.Kc, BN);
     // the workspace is touched only by tiles whose K range is split across
     // CTAs: the last T mod G tiles (none when every CTA takes whole tiles)
@@ -652,6 +653,7 @@ int launch_tc_noalloc(const int8_t* x, const float* xs, const void* wn, const fl
     p.Kc = sherry_k_chunks(K);
     p.U = p.TM * p.TN * p.Kc;
     p.whole = 0;
+    p.cluster = 0;
     const int64_t grid = std::min<int64_t>(tc_grid(p.TM * p.TN, p.U, di.sms, p.Kc, BN), kNoAllocMaxCtas);
     p.ws = scratch;
     p.counters = reinterpret_cast<uint32_t*>(scratch + kNoAllocAccWords);

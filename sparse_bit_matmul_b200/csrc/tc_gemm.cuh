@@ -192,6 +192,7 @@ struct Params {
     int64_t U;                  // total units TM*TN*Kc
     int y_tma;                  // y rows 16-byte multiples: complete tiles leave through TMA stores
     int whole;                  // leftover tiles are not split: one each to the first CTAs
+    int cluster;                // CTAs per tile, a thread-block cluster (0: none); see kClusterSplit
 };
 
 // Parameters of the epilogues other than kEpPlain.  kEpGrad: M counts digit
@@ -400,7 +401,8 @@ __device__ __forceinline__ void ep_stage(const EpParams& p, const uint32_t (&v)[
 // tiles summed across CTAs come first (their reductions overlap the later
 // tiles), and every CTA ends on whole tiles.  With `whole` the last R tiles
 // are not cut: each of the first R CTAs walks one of them first, and no tile is
-// summed across CTAs.  All roles walk this sequence.
+// summed across CTAs.  With `cluster` every tile is one cluster's, a share of
+// its chunks each CTA's.  All roles walk this sequence.
 struct SegWalk {
     int64_t Kc, tile, cb, ce, end_u, r1_tile, r1_end_tile;
     int range;                                  // 0 split share, 1 own tiles, 2 done
@@ -413,7 +415,13 @@ struct SegWalk {
         r1_tile = b * F;
         r1_end_tile = (b + 1) * F;
         int64_t a0, a1;
-        if (p.whole) {
+        if (p.cluster) {
+            // one tile per cluster, its chunks cut evenly
+            const int64_t S = p.cluster, t = b / S, q = b - t * S;
+            a0 = t * Kc + Kc * q / S;
+            a1 = t * Kc + Kc * (q + 1) / S;
+            r1_tile = r1_end_tile = 0;
+        } else if (p.whole) {
             a0 = L0 + Kc * b;
             a1 = b < R ? a0 + Kc : a0;
         } else if (RU >= G) {
@@ -507,6 +515,13 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
     using C = Cfg<BN, SC, WF, EG>;
     static_assert(EK != kEpPlain || EG == 1, "EG");
     static_assert(EK == kEpGrad ? 16 % D == 0 : D == 1, "digits per token");
+    // Few tokens and fewer tiles than SMs: the CTAs of a cluster take a share of
+    // a tile's chunks each and add their sums into the first one's staging
+    // slots over distributed shared memory (M = 16 bf16: K = 4096, N = 4096
+    // 10.2 us whole, 11.1 split through the workspace, 9.2 so; K = 14336 24.6,
+    // 15.4, 13.3)
+    constexpr bool kClusterSplit = EK != kEpPlain && EG == 1 && BN <= 32;
+    const bool cluster = kClusterSplit && p.cluster > 0;
     // kEpLinear: a barrier per staging slot of each epilogue warp, for the
     // residual boxes loaded into it
     __shared__ __align__(8) uint64_t res_bars[EK == kEpLinear ? EG * 4 * C::kEpSlots : 1];
@@ -577,10 +592,20 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
         ptx::tmem_relinquish();
     }
     if (threadIdx.x == 0) ptx::prefetch_tensormap(&xmap);
+    if constexpr (kClusterSplit) {
+        // the sums start at zero; every CTA of the cluster has its slots ready
+        // once the barrier that starts here completes
+        if (cluster && warp >= C::kEpiWarp0) {
+            uint32_t* z = reinterpret_cast<uint32_t*>(smem + C::kOffStaging) + (warp & 3) * (C::kEpSlots * 16 * 32);
+            for (int i = lane; i < BN * 32; i += 32) z[i] = 0u;
+        }
+    }
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    if constexpr (kClusterSplit)
+        if (cluster) ptx::cluster_arrive_release();
     const uint32_t tmem = *tmem_holder;
     // Programmatic dependent launch: everything above (barriers, tensor
     // memory, table) overlaps the end of the previous kernel on the stream.
@@ -919,6 +944,9 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             reinterpret_cast<float*>(smem + C::kOffStaging) + (4 * grp + quad) * (C::kEpSlots * 16 * 32);
         SegWalk w(p, blockIdx.x, G);
         [[maybe_unused]] int turn = 0;             // segment index modulo EG
+        [[maybe_unused]] bool met = false;         // this thread passed the cluster's second barrier
+        if constexpr (kClusterSplit)
+            if (cluster) ptx::cluster_wait_acquire();
         for (; !w.done(); w.next()) {
             if constexpr (EG > 1) {
                 const bool mine = turn == grp;
@@ -991,7 +1019,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             }
             ptx::tc_fence_after();
             int64_t slot = 0, nparts = 1;
-            if (!complete) {
+            if (!complete && !cluster) {
                 int64_t bf = 0, bl = 0;
                 split_owners(p, tile, G, &bf, &bl);
                 slot = bf;
@@ -1111,6 +1139,15 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                 uint32_t v[16];
                 ptx::tmem_ld_32x32b_x16(lane_base + (uint32_t)(d * BN + j0), v);
                 ptx::tmem_wait_ld();
+                if constexpr (kClusterSplit) {
+                    if (cluster) {
+                        // [token][32 rows] of the first CTA's warp of this quadrant
+                        const uint32_t to = ptx::mapa(ptx::smem_u32(stg_w + j0 * 32 + lane), 0u);
+#pragma unroll
+                        for (int jj = 0; jj < 16; ++jj) ptx::red_shared_cluster_add_s32(to + 128u * (uint32_t)jj, (int32_t)v[jj]);
+                        continue;
+                    }
+                }
 #pragma unroll
                 for (int jj = 0; jj < 16; ++jj) {
                     const int64_t m = tm * BN + j0 + jj;
@@ -1139,16 +1176,29 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             }
             const int64_t cur_tm = tm;
             if (!complete) {
-                __threadfence();
-                ptx::named_bar_sync(ebar, 128);
-                if (etid == 0) {
-                    const uint32_t old = atomicAdd(p.counters + slot, 1u);
-                    last_flag[grp] = (old == (uint32_t)(nparts - 1)) ? 1 : 0;
-                }
-                __syncwarp();
-                ptx::named_bar_sync(ebar, 128);
-                if (last_flag[grp]) {
+                bool last;
+                if (cluster) {
+                    // every CTA's sums are in the first one's slots
+                    if constexpr (kClusterSplit) {
+                        __syncwarp();
+                        ptx::cluster_arrive_release();
+                        ptx::cluster_wait_acquire();
+                        met = true;
+                    }
+                    last = w.cb == 0;
+                } else {
                     __threadfence();
+                    ptx::named_bar_sync(ebar, 128);
+                    if (etid == 0) {
+                        const uint32_t old = atomicAdd(p.counters + slot, 1u);
+                        last_flag[grp] = (old == (uint32_t)(nparts - 1)) ? 1 : 0;
+                    }
+                    __syncwarp();
+                    ptx::named_bar_sync(ebar, 128);
+                    last = last_flag[grp];
+                    if (last) __threadfence();
+                }
+                if (last) {
                     // 16 independent L2 loads in flight per batch: one round
                     // trip per 16 tokens, not one per token
                     const int64_t mleft = p.M - cur_tm * BN;
@@ -1176,10 +1226,13 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                                 // 16-byte piece `lane` of every group of four
                                 // tokens; tokens past jn: zeros of the slot
                                 const uint32_t to = stg_a + (uint32_t)(q % kRing) * (kSlotFloats * 4);
-                                const int32_t* from = wsl + 16 * q * SHERRY_TILE_ROWS + piece0;
+                                if (!cluster) {
+                                    const int32_t* from = wsl + 16 * q * SHERRY_TILE_ROWS + piece0;
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    ptx::cp_async16(to + (uint32_t)(k * 4 * 32 * 4 + 16 * lane), from + k * (4 * SHERRY_TILE_ROWS));
+                                    for (int k = 0; k < 4; ++k)
+                                        ptx::cp_async16(to + (uint32_t)(k * 4 * 32 * 4 + 16 * lane),
+                                                        from + k * (4 * SHERRY_TILE_ROWS));
+                                }
                                 if constexpr (EK == kEpLinear) {
                                     if (res_in) {
                                         // rows of 32 es bytes: 2 es pieces each, whole inside the residual or outside
@@ -1226,10 +1279,12 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                                 if (p.y_tma) ep_stage<EK, D, S>(p, u, sc, al, bi, lane, stg, part, res_in);
                                 else ep_store<EK, D, S>(p, u, sc, al, bi, lane, (m0 + part) / D, col);
                             }
-                            // the slot's words are zero again for the next call
-                            int4* z = reinterpret_cast<int4*>(wsl + 16 * q * SHERRY_TILE_ROWS + piece0);
+                            if (!cluster) {
+                                // the slot's words are zero again for the next call
+                                int4* z = reinterpret_cast<int4*>(wsl + 16 * q * SHERRY_TILE_ROWS + piece0);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) z[k * SHERRY_TILE_ROWS] = make_int4(0, 0, 0, 0);
+                                for (int k = 0; k < 4; ++k) z[k * SHERRY_TILE_ROWS] = make_int4(0, 0, 0, 0);
+                            }
                             if (p.y_tma) ptx::fence_proxy_async_smem();
                             __syncwarp();
                             if (p.y_tma && lane == 0) {
@@ -1262,10 +1317,18 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                             }
                         }
                     }
-                    if (etid == 0) atomicExch(p.counters + slot, 0u);
+                    if (etid == 0 && !cluster) atomicExch(p.counters + slot, 0u);
                 }
                 __syncwarp();
                 ptx::named_bar_sync(ebar, 128);
+            }
+        }
+        if constexpr (kClusterSplit) {
+            // a warp that gave up still meets the others
+            __syncwarp();
+            if (cluster && !met) {
+                ptx::cluster_arrive_release();
+                ptx::cluster_wait_acquire();
             }
         }
         // shared memory stays valid until every TMA store has read it
@@ -1273,6 +1336,14 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
     }
 
     __syncwarp();
+    if constexpr (kClusterSplit) {
+        // the other warps' part in the cluster's two barriers
+        if (cluster && warp < C::kEpiWarp0) {
+            ptx::cluster_wait_acquire();
+            ptx::cluster_arrive_release();
+            ptx::cluster_wait_acquire();
+        }
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();

@@ -20,19 +20,25 @@ inline int tc_token_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 
 // chunks' issue that does not fit beside it.  A second epilogue group cuts the
 // epilogue's share to a third and, one decoder group fewer, slows the chunks.
 // Splitting the leftover tiles (or, with fewer tiles than SMs, every tile S
-// ways) evens out the chunks but costs the sums through the workspace.
+// ways) evens out the chunks but costs the sums through the workspace; small
+// tiles are split within a cluster instead.
 // Constants fitted on one B200 to about 1200 forced launches of 220 shapes
 // (forward and gradients, M 5 to 2048, 1 to 112 chunks): the choice is on
 // average 1.3 % and at most 16 % above the best of them; the rule of
 // sherry_gemm_tc was 26 % above it (K = 1056, N = 2000, M = 1400: 21 us instead
 // of 45; K = 4096, N = 4096, M = 700: 25.5 instead of 42.5), and one epilogue
 // group 20 to 40 % on long batches of few chunks (M = 2048, N = 4096, gelu with
-// residual, fp32: K = 768 68 -> 46 us, K = 4096 89 -> 72 us).
+// residual, fp32: K = 768 68 -> 46 us, K = 4096 89 -> 72 us).  The clusters'
+// constants come from 54 shapes of few rows (M 4 to 64): there the choice is
+// 0.9 % above the best and at most 8 %, without clusters 7 % and up to 42 % (K = 14336,
+// N = 4096, M = 16: 15.4 -> 13.3 us).  Clusters of eight never won and, at 128
+// CTAs, lost 5 to 10 us: not all of them are resident.
 struct TilePlan {
     int bn = 16;
     int eg = 1;
     int64_t grid = 1;
     int whole = 1;
+    int cluster = 0;            // CTAs per tile
 };
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -54,10 +60,22 @@ inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, doubl
         const int64_t T = ceil_div(M, t.bn) * TN;
         const double e = (0.1 + 0.026 * t.bn) * w, chunks = t.chunk_us * (double)Kc;
         const double steady = std::max(chunks, (t.eg == 2 ? 0.34 * e : e) + 0.65 * chunks);
-        const double whole = (double)(ceil_div(T, sms) - 1) * steady + chunks + e;
+        // more than two thirds of the SMs at once slow the small tiles
+        const bool crowded = t.bn <= 32 && T <= sms && 3 * T > 2 * sms;
+        const double whole = (double)(ceil_div(T, sms) - 1) * steady + chunks + e + (crowded ? 0.5 : 0.0);
         if (whole < best_us) {
             best_us = whole;
             best = {t.bn, t.eg, std::min(T, sms), 1};
+        }
+        // a cluster of S CTAs per tile, while all clusters are resident (an SM
+        // each CTA; a cluster of four may leave SMs of a GPC out)
+        for (int S = 2; t.bn <= 32 && S <= 4 && S <= Kc && T * S <= sms * 7 / 8; S *= 2) {
+            const double adds = (S == 2 ? 1.4 : 2.0) * (t.bn == 32 ? 1.6 : 1.0) + (3 * T * S > 2 * sms ? 1.5 : 0.0);
+            const double us = t.chunk_us * (double)ceil_div(Kc, S) + e + adds;
+            if (us < best_us) {
+                best_us = us;
+                best = {t.bn, 1, T * S, 0, S};
+            }
         }
         // split launches stay within the workspace of sherry_reserve(M, ..)
         if (t.eg == 2 || t.bn > tc_token_tile(M)) continue;
