@@ -37,6 +37,22 @@ __device__ __forceinline__ uint16_t to16(float v, int dtype)
     return dtype == SHERRY_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
+// Rows of digits, D per token.  16 of them (a slice of the tensor-core
+// kernel's epilogue) hold 16 / D tokens whole: with D = 3 five tokens and a row
+// that nobody writes and whose sums nobody reads.
+template <int D>
+__host__ __device__ constexpr int64_t first_row(int64_t token)
+{
+    return D == 3 ? token / 5 * 16 + token % 5 * 3 : token * D;
+}
+
+// of the rows from `row` on, for D = 3 a multiple of 16
+template <int D>
+__host__ __device__ constexpr int64_t first_token(int64_t row)
+{
+    return D == 3 ? row / 16 * 5 : row / D;
+}
+
 // element `i` of a tensor of `dtype`
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype)
 {

@@ -235,7 +235,7 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
     p.y_tma = (p.No * ep::elem_size(p.dtype)) % 16 == 0 && aligned16(p.out);
     if (p.res) p.y_tma = p.y_tma && aligned16(p.res);
     if (p.y_tma) {
-        st = make_out_map(&maps.out, p.out, p.dtype, p.Mo, p.No, EK == tc::kEpGated ? 16 : 32, 16 / D);
+        st = make_out_map(&maps.out, p.out, p.dtype, p.Mo, p.No, EK == tc::kEpGated ? 16 : 32, (int)ep::first_token<D>(16));
         if (st == SHERRY_OK && p.res)
             st = make_out_map(&maps.res, const_cast<void*>(p.res), p.dtype, p.Mo, p.No, 32, 16);
         if (st != SHERRY_OK) return st;
@@ -415,9 +415,14 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
 // Row stride of the digit rows: whole 16-byte units (TMA).
 int64_t digit_ld(int64_t R) { return (R + 15) & ~int64_t(15); }
 
+int64_t digit_rows(int dtype, int64_t M)
+{
+    return dtype == SHERRY_BF16 ? 2 * M : dtype == SHERRY_F16 ? (M + 4) / 5 * 16 : 4 * M;
+}
+
 int64_t digit_bytes(int dtype, int64_t M, int64_t R)
 {
-    return ((int64_t)sherry_grad_digits(dtype) * M * digit_ld(R) + 255) & ~int64_t(255);
+    return (digit_rows(dtype, M) * digit_ld(R) + 255) & ~int64_t(255);
 }
 
 constexpr int64_t kGradMaxRows = (int64_t(1) << 24) - 1;
@@ -444,7 +449,6 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     int st = device_info(&di);
     if (st != SHERRY_OK) return st;
 
-    const int D = sherry_grad_digits(dtype);
     grad::Params g = {};
     g.dy = dy;
     g.acc = acc;
@@ -461,20 +465,22 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.dalpha = dalpha;
     g.dbias = dbias;
     if (!dx) return grad::launch_columns(g, gated, act, dtype, di.sms, s);
-    const TilePlan plan = plan_tiles(M * D, sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true);
+    const TilePlan plan = plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true);
     st = grad::launch_ahead(g, gated, act, dtype, di.sms, s);
     if (st != SHERRY_OK) return st;
     tc::EpParams p = {};
     p.wnative = static_cast<const uint8_t*>(wt);
     p.x_scale = g.dscale;
-    p.M = M * D;
+    p.M = digit_rows(dtype, M);
     p.N = K;
     p.K = R;
     p.out = dx;
     p.Mo = M;
     p.No = K;
     p.dtype = dtype;
-    return D == 2 ? launch_grad_tc<2>(g.dig, g.ld, p, plan, s) : launch_grad_tc<4>(g.dig, g.ld, p, plan, s);
+    if (dtype == SHERRY_BF16) return launch_grad_tc<grad::kDigits<SHERRY_BF16>>(g.dig, g.ld, p, plan, s);
+    if (dtype == SHERRY_F16) return launch_grad_tc<grad::kDigits<SHERRY_F16>>(g.dig, g.ld, p, plan, s);
+    return launch_grad_tc<grad::kDigits<SHERRY_F32>>(g.dig, g.ld, p, plan, s);
 }
 
 int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)

@@ -11,8 +11,11 @@
 // Fixed point.  e of a token is scaled to integers v below its largest |e|:
 // D = 2 digits (bf16 tensors) |v| <= 32639 = 127 (256 + 1), so e is off by at
 // most 2^-16 of the token's largest (a bf16 output rounds by 2^-9 of itself);
-// D = 4 (fp32, fp16) a power of two with |v| < 2^30, exact for every e within
-// a factor 64 of the largest and off by at most 2^-30 of it below.
+// D = 3 (fp16) a power of two with |v| < 2^22, off by at most 2^-22 (an output
+// rounds by 2^-12; four digits: M=1386 K=1504, gated to 14319 367 us, three 339);
+// D = 4 (fp32) a power of two with |v| < 2^30, exact for
+// every e within a factor 64 of the largest and off by at most 2^-30 of it
+// below.
 // v = sum_d 256^d digit_d with digits in [-128, 127]: the integer sums over n
 // below 2^24 rows stay inside int32.
 #pragma once
@@ -36,7 +39,7 @@ struct Params {
     const float* alpha;         // [R]
     const float* bias;          // [R] or null
     int64_t M, R, No;           // R = No, or 2 No when gated
-    int8_t* dig;                // [M * D][ld] digit rows
+    int8_t* dig;                // [digit rows][ld]: a token's from ep::first_row<D>(m) on
     float* dscale;              // [M]
     int64_t ld;                 // a multiple of 16, >= R
     int seg;                    // rows of the weight per block of a cluster, a multiple of 4
@@ -62,7 +65,7 @@ __device__ __forceinline__ float widen(typename Elem<DT>::type v)
 }
 
 template <int DT>
-constexpr int kDigits = DT == SHERRY_BF16 ? 2 : 4;
+constexpr int kDigits = DT == SHERRY_BF16 ? 2 : DT == SHERRY_F16 ? 3 : 4;
 
 __device__ __forceinline__ float pre_act(int32_t acc, float al, float s, bool has_bias, float b)
 {
@@ -234,8 +237,8 @@ struct Segment {
 // cluster, then the digit rows.
 // Bound by instruction issue and DRAM in about equal parts: magnitudes are
 // compared as integers (one mask and one maximum a value; Inf and NaN order
-// above every number), and 16-bit digits come out of the low bits of e * inv +
-// 1.5 * 2^23 without a conversion instruction.
+// above every number), and two or three digits come out of the low bits of
+// e * inv + 1.5 * 2^23 without a conversion instruction.
 constexpr int kDigitThreads = 256;
 constexpr uint32_t kInfBits = 0x7F800000u;
 
@@ -301,7 +304,7 @@ __device__ __forceinline__ void grad_digits(const Params& p, int64_t m, uint32_t
             }
         } else {
             const int ex = (int)(mx >> 23) - 127;            // big < 2^(ex + 1)
-            const int k = min(29 - ex, 126);
+            const int k = min((D == 3 ? 21 : 29) - ex, 126);
             inv = __uint_as_float((uint32_t)(127 + k) << 23);
             sc = __uint_as_float((uint32_t)(127 - k) << 23);
         }
@@ -310,7 +313,7 @@ __device__ __forceinline__ void grad_digits(const Params& p, int64_t m, uint32_t
     if (tid == 0 && rank == 0) p.dscale[m] = sc;
     // the block of the last rows also writes the padding up to ld
     const int W = (int)((min(r0 + p.seg, p.ld) - r0) >> 2);
-    int8_t* dig = p.dig + m * D * p.ld + r0;
+    int8_t* dig = p.dig + ep::first_row<D>(m) * p.ld + r0;
 #pragma unroll 2
     for (int u = tid; u < W; u += kDigitThreads) {
         float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -323,11 +326,14 @@ __device__ __forceinline__ void grad_digits(const Params& p, int64_t m, uint32_t
             }
         }
         uint32_t v[4];
-        // |v| <= 32639: rint(e inv) in the low bits of the sum
+        // |v| < 2^22: rint(e inv) in the low bits of the sum, above its bits
+        // for 0 (which reach the third byte)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            v[k] = D == 2 ? __float_as_uint(__fmaf_rn(e[k], inv, quant::kRoundMagic))
-                          : (uint32_t)__float2int_rn(__fmul_rn(e[k], inv));
+        for (int k = 0; k < 4; ++k) {
+            v[k] = D < 4 ? __float_as_uint(__fmaf_rn(e[k], inv, quant::kRoundMagic))
+                         : (uint32_t)__float2int_rn(__fmul_rn(e[k], inv));
+            if (D == 3) v[k] -= __float_as_uint(quant::kRoundMagic);
+        }
         // digit d is byte d of v once 128 was added to every byte below it:
         // (v - digit) / 256 is (v + 128) >> 8 for a digit in [-128, 127]
 #pragma unroll

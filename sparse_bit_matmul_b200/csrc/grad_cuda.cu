@@ -76,14 +76,14 @@ int digits(Params p, int sms, cudaStream_t stream)
     if (st != SHERRY_OK) return st;
     int cx = 1;
     const int64_t smem = split_rows(p, sms, &cx);
-    // tokens in grid.y: at most 65535 a launch
+    // tokens in grid.y: at most 65535 a launch (whole groups of 16 digit rows)
     Params q = p;
     for (int64_t m0 = 0; m0 < p.M; m0 += 65535) {
         const int64_t left = p.M - m0, n = left < 65535 ? left : 65535;
         q.dy = static_cast<const uint8_t*>(p.dy) + m0 * p.No * (DT == SHERRY_F32 ? 4 : 2);
         q.acc = p.acc ? p.acc + m0 * p.R : nullptr;
         q.x_scale = p.x_scale ? p.x_scale + m0 : nullptr;
-        q.dig = p.dig + m0 * kDigits<DT> * p.ld;
+        q.dig = p.dig + ep::first_row<kDigits<DT>>(m0) * p.ld;
         q.dscale = p.dscale + m0;
         const cudaError_t e = launch_pdl(kernel, dim3((unsigned)cx, (unsigned)n), dim3(kDigitThreads), (size_t)smem, stream,
                                          dim3((unsigned)cx), q);

@@ -66,8 +66,8 @@
 // so no lane idles) and writes act(gate) * up; kEpGrad is the input gradient:
 // the weights are T^T at two bits each (kWeightT2, four byte selectors per
 // shift and mask, one byte permute per TMEM cell, no table), the "tokens" are
-// the int8 base-256 digits of a fixed-point gradient, D per token, and the
-// epilogue joins a token's D sums.  Its sums are as exact as the forward's,
+// the int8 base-256 digits of a fixed-point gradient, D per token (three: five
+// tokens to 16 rows), and the epilogue joins a token's D sums.  Its sums are as exact as the forward's,
 // so the split-K reductions stay free of order.
 #pragma once
 
@@ -196,7 +196,7 @@ struct Params {
 };
 
 // Parameters of the epilogues other than kEpPlain.  kEpGrad: M counts digit
-// rows (D per token), N is the output's row length, x_scale one per token.
+// rows, N is the output's row length, x_scale one per token.
 struct EpParams : Params {
     const float* bias;          // [N] or null
     const void* res;            // [Mo][No] or null (kEpLinear)
@@ -227,14 +227,14 @@ struct ParamsOf<kEpPlain> {
 // S sums of one weight row (32 lanes: 32 rows), of S consecutive tokens or
 // digit rows with the scales sc, into output values: kEpLinear o[i] of token
 // i, kEpGated o[i] of token 2 i + (lane & 1) and the lane's row pair, kEpGrad
-// o[i] of token i (digit rows D i .. D i + D - 1, lowest digit first).
+// o[i] of token i (digit rows D i .. D i + D - 1, lowest first).
 // All 32 lanes call it.
 template <int EK, int D, int S, int O>
 __device__ __forceinline__ void ep_values(const EpParams& p, const uint32_t (&v)[S], const float* sc, float al,
                                           float bi, int lane, float (&o)[O])
 {
     if constexpr (EK == kEpGrad) {
-        static_assert(O * D == S, "digits");
+        static_assert(O == S / D, "digits");
 #pragma unroll
         for (int i = 0; i < O; ++i) {
             // every step rounds relative to the joined value
@@ -369,7 +369,7 @@ __device__ __forceinline__ void ep_stage(const EpParams& p, const uint32_t (&v)[
     constexpr int kStep = EK == kEpGated ? 2 * OW : OW;
     float o[O];
     ep_values<EK, D, S, O>(p, v, sc, al, bi, lane, o);
-    const int at0 = part / D * OW + (EK == kEpGated ? (lane & 1) * OW + (lane >> 1) : lane);
+    const int at0 = (int)ep::first_token<D>(part) * OW + (EK == kEpGated ? (lane & 1) * OW + (lane >> 1) : lane);
     if (p.dtype == SHERRY_F32) {
         if (has_res) {
 #pragma unroll
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
 {
     using C = Cfg<BN, SC, WF, EG>;
     static_assert(EK != kEpPlain || EG == 1, "EG");
-    static_assert(EK == kEpGrad ? 16 % D == 0 : D == 1, "digits per token");
+    static_assert(EK == kEpGrad ? D >= 2 && D <= 4 : D == 1, "digits per token");
     // Few tokens and fewer tiles than SMs: the CTAs of a cluster take a share of
     // a tile's chunks each and add their sums into the first one's staging
     // slots over distributed shared memory (M = 16 bf16: K = 4096, N = 4096
@@ -963,8 +963,9 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             float* sc_s = reinterpret_cast<float*>(smem + C::kOffMisc + 64) + (2 * grp + (int)(seg & 1)) * BN;
             int64_t Mo = p.M;                          // scales: one per token
             if constexpr (EK != kEpPlain) Mo = p.Mo;
-            for (int i = etid; i < BN / D; i += 128) {
-                const int64_t m = tm * (BN / D) + i;
+            constexpr int kTileTokens = (int)ep::first_token<D>(BN);
+            for (int i = etid; i < kTileTokens; i += 128) {
+                const int64_t m = tm * kTileTokens + i;
                 sc_s[i] = (m < Mo) ? __ldg(p.x_scale + m) : 0.0f;
             }
             float al = 0.0f, bi = 0.0f;
@@ -1037,7 +1038,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
 #pragma unroll 1
                     for (int q = 0; q < nslices; ++q) {
                         const int j0 = 16 * q;
-                        const int64_t m0 = (tm * BN + j0) / D;
+                        const int64_t m0 = ep::first_token<D>(tm * BN + j0);
                         const uint32_t slot = stage_slice % C::kEpSlots;
                         float* stg = stg_w + slot * (16 * 32);
                         if (has_res) {
@@ -1066,7 +1067,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                             else ptx::tmem_ld_32x32b_x8(lane_base + (uint32_t)(d * BN + j0 + part), v);
                             ptx::tmem_wait_ld_of(v);
                             if constexpr (EK != kEpGrad) ep_keep<S>(p, v, m0 + part, n);
-                            ep_stage<EK, D, S>(p, v, sc_s + (j0 + part) / D, al, bi, lane, stg, part, has_res);
+                            ep_stage<EK, D, S>(p, v, sc_s + ep::first_token<D>(j0 + part), al, bi, lane, stg, part, has_res);
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
@@ -1122,7 +1123,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
             for (int j0 = 0; j0 < (via_tma ? 0 : BN); j0 += 16) {
                 if constexpr (EK != kEpPlain) {
                     if (complete) {
-                        if ((tm * BN + j0) / D >= p.Mo) break;
+                        if (ep::first_token<D>(tm * BN + j0) >= p.Mo) break;
                         constexpr int S = kEpSums<EK>;
 #pragma unroll 1
                         for (int j = j0; j < j0 + 16; j += S) {
@@ -1131,7 +1132,8 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                             else ptx::tmem_ld_32x32b_x8(lane_base + (uint32_t)(d * BN + j), u);
                             ptx::tmem_wait_ld_of(u);
                             if constexpr (EK != kEpGrad) ep_keep<S>(p, u, tm * BN + j, n);
-                            ep_store<EK, D, S>(p, u, sc_s + j / D, al, bi, lane, (tm * BN + j) / D, col);
+                            ep_store<EK, D, S>(p, u, sc_s + ep::first_token<D>(j), al, bi, lane, ep::first_token<D>(tm * BN + j),
+                                               col);
                         }
                         continue;
                     }
@@ -1275,9 +1277,9 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < S; ++i) u[i] = __float_as_uint(in[(part + i) * 32 + lane]);
                                 if constexpr (EK != kEpGrad) ep_keep<S>(p, u, m0 + part, n);
-                                const float* sc = sc_s + (16 * q + part) / D;
+                                const float* sc = sc_s + ep::first_token<D>(16 * q + part);
                                 if (p.y_tma) ep_stage<EK, D, S>(p, u, sc, al, bi, lane, stg, part, res_in);
-                                else ep_store<EK, D, S>(p, u, sc, al, bi, lane, (m0 + part) / D, col);
+                                else ep_store<EK, D, S>(p, u, sc, al, bi, lane, ep::first_token<D>(m0 + part), col);
                             }
                             if (!cluster) {
                                 // the slot's words are zero again for the next call
@@ -1288,7 +1290,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                             if (p.y_tma) ptx::fence_proxy_async_smem();
                             __syncwarp();
                             if (p.y_tma && lane == 0) {
-                                ptx::tma_store_2d(&ymap.out, out_x, (int32_t)(m0 / D), ptx::smem_u32(stg));
+                                ptx::tma_store_2d(&ymap.out, out_x, (int32_t)ep::first_token<D>(m0), ptx::smem_u32(stg));
                                 ptx::bulk_commit_group();
                             }
                             if constexpr (kRing == 1) fetch(q + 1);

@@ -117,14 +117,15 @@ def gradients(T, acc, alpha, s, bias, name, gated, dy, dtype):
     """(dx, dalpha, dbias) in 64 bits and their bounds.
 
     dx: e = dz alpha (one more rounding), off by half a step of the fixed point: the token's largest
-    |e| / 32639 (bf16), at most 2^-29 of it (others); the integer sums are exact, joining and scaling
-    the digits takes at most 9 roundings, and the result is rounded once.  Column sums: M terms in
-    chains of at most M / 16 + 17 additions, each term off by its own bound and 3 roundings."""
+    |e| / 32639 (bf16), at most 2^-21 of it (fp16: it is 2^21 steps or more) or 2^-29 (fp32); the
+    integer sums are exact, joining and scaling the digits takes at most 9 roundings, and the result is
+    rounded once.  Column sums: M terms in chains of at most M / 16 + 17 additions, each term off by its
+    own bound and 3 roundings."""
     dz, edz = dz_bound(acc, alpha, s, bias, name, gated, dy)
     e, ee = dz * alpha, edz * alpha.abs()
     ee = ee + U * (e.abs() + ee)
     big = (e.abs() + ee).amax(1, keepdim=True)
-    step = big / 32639 if dtype is torch.bfloat16 else big * 2.0 ** -29
+    step = big / 32639 if dtype is torch.bfloat16 else big * 2.0 ** (-21 if dtype is torch.float16 else -29)
     ee = ee + 0.51 * step + 2 * U * e.abs() * (dtype is torch.bfloat16) + 2.0 ** -114
     A = T.abs()
     dx = e @ T

@@ -355,6 +355,25 @@ def test_more_tokens_than_one_grid_dimension():
     run_backward(True, 70001, 32, 3, "bf16", "silu", False)
 
 
+@pytest.mark.parametrize("M", [4, 5, 6, 10, 11, 79, 81, 400, 401])
+def test_fp16_tokens_around_groups_of_five(M):
+    """fp16 digit rows hold five tokens to 16; the output may end inside a group, at element alignment."""
+    for K, R in ((160, 136), (256, 5000), (32, 20000)):
+        dy = rand(M, R, seed=M, dtype=torch.float16)
+        dx = run_backward(False, M, K, R, "f16", "none", False, dy=dy)[0]
+        _, w_t, alpha, _ = weight(R, K, False)
+        buf = torch.full((M * K + 3,), 9.0, dtype=torch.float16, device="cuda")
+        out = buf[1:1 + M * K].view(M, K)
+        sbm.linear_backward(dy, w_t, alpha, K, want_scales=False, out=out)
+        assert torch.equal(out, dx) and buf[0] == 9 and (buf[1 + M * K:] == 9).all()
+        # whatever the buffer of the digits held before
+        work = torch.full((sbm.load().sherry_grad_work_bytes(2, M, R),), 0x7f, dtype=torch.uint8, device="cuda")
+        rc = sbm.load().sherry_linear_grad(dy.data_ptr(), 2, None, None, w_t.data_ptr(), alpha.data_ptr(), None, 0,
+                                           out.data_ptr(), None, None, work.data_ptr(), M, R, K,
+                                           torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and torch.equal(out, dx)
+
+
 def test_linear_gradient_without_sums():
     """act none and no dalpha: dx needs neither sums nor scales."""
     _, w_t, alpha, T = weight(130, 160, False)
