@@ -13,9 +13,8 @@
 // most 2^-16 of the token's largest (a bf16 output rounds by 2^-9 of itself);
 // D = 3 (fp16) a power of two with |v| < 2^22, off by at most 2^-22 (an output
 // rounds by 2^-12; four digits: M=1386 K=1504, gated to 14319 367 us, three 339);
-// D = 4 (fp32) a power of two with |v| < 2^30, exact for
-// every e within a factor 64 of the largest and off by at most 2^-30 of it
-// below.
+// D = 4 (fp32) a power of two with |v| < 2^30, exact for every e within a
+// factor 64 of the largest and off by at most 2^-30 of it below.
 // v = sum_d 256^d digit_d with digits in [-128, 127]: the integer sums over n
 // below 2^24 rows stay inside int32.
 #pragma once
@@ -427,7 +426,7 @@ struct Column {
     }
 };
 
-template <bool GATED, int ACT, int DT, bool VEC, bool ACC>
+template <bool GATED, int ACT, int DT, bool VEC, bool ACC, int BATCH>
 __device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t m0, int64_t step, float (&sa)[4],
                                             float (&sb)[4])
 {
@@ -444,12 +443,11 @@ __device__ __forceinline__ void column_sums(const Params& p, int64_t r, int64_t 
     c.cols = (int)min(p.No - col, int64_t(kColRows));
     c.hb = p.bias != nullptr;
     c.w = load_rows<GATED, VEC>(p.alpha + r, c.hb ? p.bias + r : nullptr, c.rows, c.kLanes);
-    constexpr int kBatch = GATED ? 4 : 3;                    // what 80 registers hold
-    c.template run<kBatch>(p.M, sa, sb);
+    c.template run<BATCH>(p.M, sa, sb);
     c.template run<1>(p.M, sa, sb);
 }
 
-template <bool GATED, int ACT, int DT, int WARPS>
+template <bool GATED, int ACT, int DT, int WARPS, int BATCH>
 __device__ __forceinline__ void columns_block(const Params& p, int64_t bx, uint32_t rank, uint32_t CY)
 {
     __shared__ float part[WARPS][2][kColRows];
@@ -462,13 +460,13 @@ __device__ __forceinline__ void columns_block(const Params& p, int64_t bx, uint3
         const int64_t m0 = (int64_t)rank * WARPS + warp, step = (int64_t)CY * WARPS;
         if constexpr (!GATED && ACT == SHERRY_ACT_NONE) {
             if (!p.acc) {                                    // dbias alone
-                if (p.vec) column_sums<GATED, ACT, DT, true, false>(p, r, m0, step, sa, sb);
-                else column_sums<GATED, ACT, DT, false, false>(p, r, m0, step, sa, sb);
+                if (p.vec) column_sums<GATED, ACT, DT, true, false, BATCH>(p, r, m0, step, sa, sb);
+                else column_sums<GATED, ACT, DT, false, false, BATCH>(p, r, m0, step, sa, sb);
             }
         }
         if (p.acc) {
-            if (p.vec) column_sums<GATED, ACT, DT, true, true>(p, r, m0, step, sa, sb);
-            else column_sums<GATED, ACT, DT, false, true>(p, r, m0, step, sa, sb);
+            if (p.vec) column_sums<GATED, ACT, DT, true, true, BATCH>(p, r, m0, step, sa, sb);
+            else column_sums<GATED, ACT, DT, false, true, BATCH>(p, r, m0, step, sa, sb);
         }
     }
     if (p.vec) {
@@ -522,25 +520,35 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 
 {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    columns_block<GATED, ACT, DT, WARPS>(p, blockIdx.x, blockIdx.y, gridDim.y);
+    constexpr int kBatch = GATED ? 4 : 3;                    // what 80 registers hold
+    columns_block<GATED, ACT, DT, WARPS, kBatch>(p, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
 // Both in one launch, for few tokens, where a launch costs more than the work
 // (M=5 K=1024, gated to 2816, bf16: 13.6 -> 11.3 us for the call, 21.9 -> 19.2 us with the host): clusters of
-// `cluster` blocks, the first `tokens` of them (all M, or none) the tokens'
-// digits, the others column sums, whose order does not depend on whether the
-// digits are wanted.  (M=300 K=2080, gated to 5001, f16: 52.4 us in two
-// launches, 46.9 in one; M=500 K=14336 N=1000 bf16: 28.7 and 35.2.)
-constexpr int64_t kBothMaxTokens = 384;
+// `cluster` blocks, the first `ahead` of them the tokens' digits (a cluster per
+// token, or with `whole` a block), the others column sums, whose order does not
+// depend on whether the digits are wanted.  In two launches and in one: M=750
+// K=640, gated to 1197, bf16 29.0 and 22.0 us, M=1000, 4096 x 4096, bf16 47.5 and
+// 44.2; M=2048 K=4096, gated to 14336, 511 and 536.  Four blocks an SM, so that
+// the digits of other tokens hide a token's two passes; the column sums load
+// fewer tokens at once for it (M=300 K=2080, gated to 5001, f16: 48.1 -> 44.0 us;
+// M=380 K=1056 N=10001 f32 gelu 64 -> 56).
+constexpr int64_t kBothMaxTokens = 1024;
+constexpr int kBothBlocks = 4;
 
 template <bool GATED, int ACT, int DT>
-__global__ void __launch_bounds__(kDigitThreads) grad_both_kernel(const Params p, uint32_t tokens, uint32_t cluster)
+__global__ void __launch_bounds__(kDigitThreads, kBothBlocks)
+    grad_both_kernel(const Params p, uint32_t ahead, uint32_t cluster, int whole)
 {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const uint32_t id = blockIdx.x / cluster, rank = blockIdx.x - id * cluster;
-    if (id < tokens) digits_block<GATED, ACT, DT>(p, id, rank, cluster);
-    else columns_block<GATED, ACT, DT, kDigitThreads / 32>(p, id - tokens, rank, cluster);
+    // what 64 registers hold
+    constexpr int kBatch = ACT == SHERRY_ACT_GELU ? 1 : 2;
+    const uint32_t token = whole ? blockIdx.x : id;
+    if (id >= ahead) columns_block<GATED, ACT, DT, kDigitThreads / 32, kBatch>(p, id - ahead, rank, cluster);
+    else if (token < p.M) digits_block<GATED, ACT, DT>(p, token, whole ? 0 : rank, whole ? 1 : cluster);
 }
 
 // Host (grad_cuda.cu): what a gradient call launches ahead of its product, and
