@@ -367,7 +367,8 @@ def _on_device(fn):
 def reserve_split(device=None):
     """Sets aside, host-synchronously, the split-K workspace (about 15 MB) of every linear_epilogue, gated
     and gradient call on `device` (default: the current one).  The first such call does it too; do it
-    before capturing a graph."""
+    before capturing a graph.  All calls on the device share it (sherry.h): two that may run at the same
+    time, replays of captured graphs included, need one stream or events between them."""
     _types()
     dev = _torch.device("cuda" if device is None else device) if not isinstance(device, int) else \
         _torch.device("cuda", device)

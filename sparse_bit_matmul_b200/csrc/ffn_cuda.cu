@@ -172,11 +172,28 @@ bool aligned_elem(const void* p, int dtype)
     return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(ep::elem_size(dtype) - 1)) == 0;
 }
 
-// Whether two buffers share a byte (null: no).
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
+struct Span {
+    const void* p;              // or null: empty
+    int64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b)
 {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
+// Whether an output shares a byte with an input or with another output.
+template <int O, int I>
+bool overlaps(const Span (&out)[O], const Span (&in)[I])
+{
+    for (int o = 0; o < O; ++o) {
+        for (int i = 0; i < I; ++i)
+            if (overlap(out[o], in[i])) return true;
+        for (int q = 0; q < o; ++q)
+            if (overlap(out[o], out[q])) return true;
+    }
+    return false;
 }
 
 // out [Mo][No]: boxes of box_n columns x box_m rows, for complete tiles
@@ -343,10 +360,11 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     if (!sherry_shape_ok(M, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x) || !aligned16(wn) || (x_i8 && !aligned16(x_i8))) return SHERRY_ERR_INVALID_ARG;
     if (!aligned_elem(out, dtype) || (res && !aligned_elem(res, dtype))) return SHERRY_ERR_INVALID_ARG;
-    const int64_t es = ep::elem_size(dtype), xb = M * K * es, ob = M * No * es, ab = 4 * M * R;
-    if (overlap(out, ob, x, xb) || (out != res && overlap(out, ob, res, ob)) || overlap(acc, ab, x, xb) ||
-        overlap(acc, ab, out, ob) || overlap(acc, ab, res, ob) || overlap(x_i8, M * K, x, xb) || overlap(x_i8, M * K, out, ob))
-        return SHERRY_ERR_INVALID_ARG;
+    const int64_t es = ep::elem_size(dtype), rb = 4 * R;
+    const Span outs[] = {{out, M * No * es}, {acc, M * rb}, {x_i8, M * K}, {x_scale, 4 * M}};
+    const Span ins[] = {{x, M * K * es}, {wn, (int64_t)sherry_native_bytes(R, K)}, {alpha, rb}, {bias, rb},
+                        {res == out ? nullptr : res, M * No * es}};
+    if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
     DeviceInfo di;
     int st = device_info(&di);
     if (st != SHERRY_OK) return st;
@@ -440,11 +458,11 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     if (!sherry_shape_ok(M, R, K) || R > kGradMaxRows || M > SHERRY_MAX_DIM / 4) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned_elem(dy, dtype) || (reinterpret_cast<uintptr_t>(acc) & 7u)) return SHERRY_ERR_INVALID_ARG;
     if (dx && (!aligned16(wt) || !aligned16(work) || !aligned_elem(dx, dtype))) return SHERRY_ERR_INVALID_ARG;
-    const int64_t es = ep::elem_size(dtype), yb = M * No * es, xb = M * K * es, rb = 4 * R;
-    if (overlap(dx, xb, dy, yb) || overlap(dx, xb, acc, M * rb) || overlap(dalpha, rb, alpha, rb) ||
-        overlap(dalpha, rb, bias, rb) || overlap(dbias, rb, alpha, rb) || overlap(dbias, rb, bias, rb) ||
-        overlap(dalpha, rb, dbias, rb))
-        return SHERRY_ERR_INVALID_ARG;
+    const int64_t es = ep::elem_size(dtype), rb = 4 * R;
+    const Span outs[] = {{dx, M * K * es}, {dalpha, rb}, {dbias, rb}, {dx ? work : nullptr, digit_bytes(dtype, M, R) + 4 * M}};
+    const Span ins[] = {{dy, M * No * es}, {acc, M * rb}, {x_scale, 4 * M}, {alpha, rb}, {bias, rb},
+                        {dx ? wt : nullptr, (int64_t)sherry_transposed_bytes(R, K)}};
+    if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
     DeviceInfo di;
     int st = device_info(&di);
     if (st != SHERRY_OK) return st;
@@ -490,6 +508,8 @@ int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64
     if (!sherry_shape_ok(1, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(out)) return SHERRY_ERR_INVALID_ARG;
     const int64_t words = (int64_t)((transposed ? sherry_transposed_bytes(R, K) : sherry_native_bytes(R, K)) / 4);
+    const Span outs[] = {{out, 4 * words}}, ins[] = {{a, N * (K / 32 * 5)}, {b, N * (K / 32 * 5)}};
+    if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
     const int threads = 256;
     const unsigned blocks = (unsigned)std::min<int64_t>((words + threads - 1) / threads, 148 * 32);
     const Codes codes = {a, b, K / 32 * 5};
@@ -509,12 +529,14 @@ extern "C" {
 int sherry_quant_act_dt(const void* x, int x_dtype, int64_t M, int64_t K, int8_t* x_i8, float* x_scale, void* stream)
 {
     if (!dtype_ok(x_dtype)) return SHERRY_ERR_INVALID_ARG;
-    if (x_dtype == SHERRY_F32)
-        return sherry_quant_act(static_cast<const float*>(x), M, K, x_i8, x_scale, stream);
     if (!x || !x_i8 || !x_scale) return SHERRY_ERR_INVALID_ARG;
     if (M <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
     if (!sherry_shape_ok(M, 1, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x) || !aligned16(x_i8)) return SHERRY_ERR_INVALID_ARG;
+    const Span outs[] = {{x_i8, M * K}, {x_scale, 4 * M}}, ins[] = {{x, M * K * ep::elem_size(x_dtype)}};
+    if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
+    if (x_dtype == SHERRY_F32)
+        return sherry_quant_act(static_cast<const float*>(x), M, K, x_i8, x_scale, stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid((unsigned)M), block(kQuantThreads);
     if (x_dtype == SHERRY_BF16)

@@ -159,13 +159,22 @@ def test_overlapping_buffers_are_refused(lib):
     far = at(1 << 16)
     kw = dict(M=2, N=4, K=32, x=at(0), y=far)
     for bad in (dict(kw, y=at(0)), dict(kw, y=at(126)), dict(kw, acc=at(64)), dict(kw, acc=far),
-                dict(kw, res=at((1 << 16) + 2)), dict(kw, q=at(16), s=at(1 << 17)), dict(kw, res=at(1 << 18), acc=at(1 << 18))):
+                dict(kw, res=at((1 << 16) + 2)), dict(kw, q=at(16), s=at(1 << 17)), dict(kw, res=at(1 << 18), acc=at(1 << 18)),
+                dict(kw, w=far), dict(kw, w=at((1 << 16) - 2544)), dict(kw, bias=far), dict(kw, alpha=at((1 << 16) + 8)),
+                dict(kw, s=far), dict(kw, q=at(1 << 17), s=at((1 << 17) + 60)), dict(kw, q=at(1 << 17), s=at(124))):
         assert _linear(L, **bad) == INVALID, bad
     kw = dict(M=2, N=4, K=32, dy=at(0), dx=far, acc=at(1 << 17), da=at(1 << 18), db=at(1 << 19), alpha=at(1 << 21),
               work=at(1 << 22), wt=at(1 << 23), s=at(1 << 24))
     for bad in (dict(kw, dx=at(0)), dict(kw, dx=at((1 << 17) + 16)), dict(kw, da=at(1 << 21)), dict(kw, db=at((1 << 18) + 8)),
-                dict(kw, bias=at(1 << 18)), dict(kw, bias=at((1 << 19) - 4))):
+                dict(kw, bias=at(1 << 18)), dict(kw, bias=at((1 << 19) - 4)), dict(kw, work=at(0)), dict(kw, work=far),
+                dict(kw, wt=at((1 << 16) - 16)), dict(kw, da=at((1 << 24) + 4)), dict(kw, db=at(12)), dict(kw, da=at(1 << 22)),
+                dict(kw, dx=at((1 << 21) - 120))):
         assert _grad(L, "sherry_linear_grad", **bad) == INVALID, bad
+    assert L.sherry_quant_act_dt(at(0), 1, 2, 32, at(64), far, None) == INVALID
+    assert L.sherry_quant_act_dt(at(0), 0, 2, 32, at(192), far, None) == INVALID
+    assert L.sherry_quant_act_dt(at(0), 1, 2, 32, far, at((1 << 16) + 60), None) == INVALID
+    assert L.sherry_repack_t(at(4090), 4, 32, at(0), None) == INVALID
+    assert L.sherry_repack_gated(far, at(2544), 4, 32, at(0), None) == INVALID
 
 
 def test_feed_forward_sources_never_allocate_or_synchronise():
