@@ -430,8 +430,9 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
                  : launch_forward_tc<tc::kEpLinear>(x_i8, p, di.sms, s);
 }
 
-// Row stride of the digit rows: whole 16-byte units (TMA).
-int64_t digit_ld(int64_t R) { return (R + 15) & ~int64_t(15); }
+// Row stride of the digit rows: whole 128-byte lines, so that a TMA box row is
+// one of them and not parts of two.
+int64_t digit_ld(int64_t R) { return (R + 127) & ~int64_t(127); }
 
 int64_t digit_rows(int dtype, int64_t M)
 {

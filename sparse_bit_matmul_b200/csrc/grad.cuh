@@ -40,7 +40,7 @@ struct Params {
     int64_t M, R, No;           // R = No, or 2 No when gated
     int8_t* dig;                // [digit rows][ld]: a token's from ep::first_row<D>(m) on
     float* dscale;              // [M]
-    int64_t ld;                 // a multiple of 16, >= R
+    int64_t ld;                 // a multiple of 16, >= R; what is past R is not read
     int seg;                    // rows of the weight per block of a cluster, a multiple of 4
     int cached;                 // a block's e fits in its shared memory
     int vec;                    // rows and bases allow 16-byte loads of four rows' values
@@ -310,13 +310,11 @@ __device__ __forceinline__ void grad_digits(const Params& p, int64_t m, uint32_t
     }
     if (bad) sc = __uint_as_float(0x7FC00000u);              // the whole dx row becomes NaN
     if (tid == 0 && rank == 0) p.dscale[m] = sc;
-    // the block of the last rows also writes the padding up to ld
-    const int W = (int)((min(r0 + p.seg, p.ld) - r0) >> 2);
     int8_t* dig = p.dig + ep::first_row<D>(m) * p.ld + r0;
 #pragma unroll 2
-    for (int u = tid; u < W; u += kDigitThreads) {
+    for (int u = tid; u < U; u += kDigitThreads) {
         float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (u < U && inv != 0.0f) {
+        if (inv != 0.0f) {
             if (p.cached) {
                 const float4 t = *reinterpret_cast<const float4*>(cache + 4 * u);
                 e[0] = t.x; e[1] = t.y; e[2] = t.z; e[3] = t.w;

@@ -50,9 +50,9 @@ int64_t split_rows(Params& p, int sms, int per, int* blocks)
 {
     int cx = 1;
     while (cx < kClusterMax &&
-           (p.ld > (int64_t)cx * kSegMax || (p.M * cx < per * (int64_t)sms && p.ld >= (int64_t)cx * 2 * kSegMin)))
+           (p.R > (int64_t)cx * kSegMax || (p.M * cx < per * (int64_t)sms && p.R >= (int64_t)cx * 2 * kSegMin)))
         cx *= 2;
-    p.seg = (int)(((p.ld + cx - 1) / cx + 15) & ~int64_t(15));
+    p.seg = (int)(((p.R + cx - 1) / cx + 15) & ~int64_t(15));
     const int64_t need = 4 * std::min<int64_t>(p.seg, (p.R + 3) & ~int64_t(3));
     p.cached = need <= kCacheMax;
     *blocks = cx;
