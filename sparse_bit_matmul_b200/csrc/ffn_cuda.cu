@@ -10,6 +10,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "sherry.h"
 #include "sherry_internal.h"
@@ -24,79 +25,107 @@ namespace sherry {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Activation quantiser for 16-bit activations: the rule and the shape of
-// quant_act_kernel (one block per token, the row held in registers between
-// the absmax and the quantisation when it fits), eight values per load.
+// Activation quantiser for any element type: the rule of quant_act_kernel, one
+// block per token.  Rows of up to kQuantXV 16-byte loads a thread stay in
+// registers between the absmax and the quantisation; longer ones are read
+// twice.  Blocks are as narrow as that allows when the tokens fill the SMs
+// (every load of a row in flight at once, little to synchronise: M=2048 bf16,
+// K=4096 QA us with 512 threads, QB so; K=14336 QC and QD), and a load a thread
+// when they do not (M=16 K=4096 QE and QF).
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 512;
-constexpr int kQuantXV = 4;                 // rows up to 16384 in registers
+constexpr int kQuantXV = 8;
 
-template <class XT>
-__device__ __forceinline__ void widen8(const uint4& w, float4& a, float4& b)
+int quant_threads(int64_t M, int64_t units, int sms)
 {
-    const uint2 lo = make_uint2(w.x, w.y), hi = make_uint2(w.z, w.w);
-    a = decode::load_x4<XT>(reinterpret_cast<const XT*>(&lo), 0);
-    b = decode::load_x4<XT>(reinterpret_cast<const XT*>(&hi), 0);
+    const int64_t t = M >= 4 * (int64_t)sms ? (units + kQuantXV - 1) / kQuantXV : units;
+    return (int)std::min<int64_t>(kQuantThreads, (t + 31) & ~int64_t(31));
 }
 
+// 16 bytes of activations: their largest magnitude, their int8 codes.
 template <class XT>
-__global__ void __launch_bounds__(kQuantThreads)
-    quant_act16_kernel(const XT* __restrict__ x, int64_t K, int8_t* __restrict__ q, float* __restrict__ scale)
+struct Quant16 {
+    static constexpr int kWords = std::is_same_v<XT, float> ? 1 : 2;
+    float4 f[kWords];
+
+    __device__ __forceinline__ explicit Quant16(const uint4& w)
+    {
+        if constexpr (kWords == 1) {
+            f[0] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+        } else {
+            const uint2 lo = make_uint2(w.x, w.y), hi = make_uint2(w.z, w.w);
+            f[0] = decode::load_x4<XT>(reinterpret_cast<const XT*>(&lo), 0);
+            f[1] = decode::load_x4<XT>(reinterpret_cast<const XT*>(&hi), 0);
+        }
+    }
+    __device__ __forceinline__ float absmax() const
+    {
+        float a = quant::absmax4(f[0]);
+        if constexpr (kWords == 2) a = fmaxf(a, quant::absmax4(f[1]));
+        return a;
+    }
+    __device__ __forceinline__ void store(int8_t* row, int unit, const quant::Scale& sc) const
+    {
+        if constexpr (kWords == 1)
+            reinterpret_cast<uint32_t*>(row)[unit] = quant::quantise4(f[0], sc);
+        else
+            reinterpret_cast<uint2*>(row)[unit] = make_uint2(quant::quantise4(f[0], sc), quant::quantise4(f[1], sc));
+    }
+};
+
+template <class XT>
+__global__ void __launch_bounds__(kQuantThreads, 2)
+    quant_rows_kernel(const XT* __restrict__ x, int64_t K, int8_t* __restrict__ q, float* __restrict__ scale)
 {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const int64_t m = blockIdx.x;
     const uint4* xr = reinterpret_cast<const uint4*>(x + m * K);
-    uint2* qw = reinterpret_cast<uint2*>(q + m * K);
-    const int K8 = (int)(K / 8);
+    int8_t* qr = q + m * K;
+    const int U = (int)(K * sizeof(XT) / 16), nthr = blockDim.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool in_regs = K8 <= kQuantXV * kQuantThreads;
+    const bool in_regs = U <= kQuantXV * nthr;
 
     uint4 v[kQuantXV];
     float a = 0.0f;
-    auto absmax8 = [](const uint4& w) {
-        float4 f, g;
-        widen8<XT>(w, f, g);
-        return fmaxf(quant::absmax4(f), quant::absmax4(g));
-    };
     if (in_regs) {
 #pragma unroll
-        for (int u = 0; u < kQuantXV; ++u) {
-            const int idx = tid + u * kQuantThreads;
-            v[u] = idx < K8 ? xr[idx] : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int u = 0; u < kQuantXV; ++u)
+            v[u] = tid + u * nthr < U ? xr[tid + u * nthr] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int u = 0; u < kQuantXV; ++u) a = fmaxf(a, absmax8(v[u]));
+        for (int u = 0; u < kQuantXV; ++u)
+            if (u * nthr < U) a = fmaxf(a, Quant16<XT>(v[u]).absmax());
     } else {
 #pragma unroll 4
-        for (int i = tid; i < K8; i += kQuantThreads) a = fmaxf(a, absmax8(xr[i]));
+        for (int i = tid; i < U; i += nthr) a = fmaxf(a, Quant16<XT>(xr[i]).absmax());
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     __shared__ float warp_max[kQuantThreads / 32];
     if (lane == 0) warp_max[warp] = a;
     __syncthreads();
-    a = lane < kQuantThreads / 32 ? warp_max[lane] : 0.0f;
+    a = lane < nthr / 32 ? warp_max[lane] : 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
 
     const quant::Scale sc = quant::make_scale(a);
     if (tid == 0) scale[m] = sc.s;
-    auto quantise8 = [&sc](const uint4& w) {
-        float4 f, g;
-        widen8<XT>(w, f, g);
-        return make_uint2(quant::quantise4(f, sc), quant::quantise4(g, sc));
-    };
     if (in_regs) {
 #pragma unroll
-        for (int u = 0; u < kQuantXV; ++u) {
-            const int idx = tid + u * kQuantThreads;
-            if (idx < K8) qw[idx] = quantise8(v[u]);
-        }
+        for (int u = 0; u < kQuantXV; ++u)
+            if (tid + u * nthr < U) Quant16<XT>(v[u]).store(qr, tid + u * nthr, sc);
     } else {
 #pragma unroll 4
-        for (int i = tid; i < K8; i += kQuantThreads) qw[i] = quantise8(xr[i]);
+        for (int i = tid; i < U; i += nthr) Quant16<XT>(xr[i]).store(qr, i, sc);
     }
+}
+
+template <class XT>
+int launch_quant(const void* x, int64_t M, int64_t K, int8_t* q, float* scale, int sms, cudaStream_t s)
+{
+    return cuda_status(launch_pdl(quant_rows_kernel<XT>, dim3((unsigned)M),
+                                  dim3((unsigned)quant_threads(M, K * (int64_t)sizeof(XT) / 16, sms)), 0, s,
+                                  static_cast<const XT*>(x), K, q, scale));
 }
 
 // ---------------------------------------------------------------------------
@@ -536,15 +565,13 @@ int sherry_quant_act_dt(const void* x, int x_dtype, int64_t M, int64_t K, int8_t
     if (!aligned16(x) || !aligned16(x_i8)) return SHERRY_ERR_INVALID_ARG;
     const Span outs[] = {{x_i8, M * K}, {x_scale, 4 * M}}, ins[] = {{x, M * K * ep::elem_size(x_dtype)}};
     if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
-    if (x_dtype == SHERRY_F32)
-        return sherry_quant_act(static_cast<const float*>(x), M, K, x_i8, x_scale, stream);
+    DeviceInfo di;
+    const int st = device_info(&di);
+    if (st != SHERRY_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)M), block(kQuantThreads);
-    if (x_dtype == SHERRY_BF16)
-        return cuda_status(launch_pdl(quant_act16_kernel<__nv_bfloat16>, grid, block, 0, s,
-                                      static_cast<const __nv_bfloat16*>(x), K, x_i8, x_scale));
-    return cuda_status(launch_pdl(quant_act16_kernel<__half>, grid, block, 0, s, static_cast<const __half*>(x), K, x_i8,
-                                  x_scale));
+    if (x_dtype == SHERRY_F32) return launch_quant<float>(x, M, K, x_i8, x_scale, di.sms, s);
+    if (x_dtype == SHERRY_BF16) return launch_quant<__nv_bfloat16>(x, M, K, x_i8, x_scale, di.sms, s);
+    return launch_quant<__half>(x, M, K, x_i8, x_scale, di.sms, s);
 }
 
 int sherry_repack_gated(const uint8_t* gate_dev, const uint8_t* up_dev, int64_t N, int64_t K, void* native_dev,

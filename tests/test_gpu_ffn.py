@@ -279,14 +279,17 @@ def test_layouts(N, K):
     assert np.array_equal(sbm.repack_gated_t(dg, du, N, K).cpu().numpy().view(np.uint32), want)
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f16"])
-@pytest.mark.parametrize("M,K", [(1, 32), (3, 4096), (5, 16384), (2, 20000 // 32 * 32)])
-def test_quantiser_of_16_bit_activations(M, K, dt):
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 4096), (5, 16384), (2, 20000 // 32 * 32), (2, 32768 + 32), (1, 65568),
+                                 # narrow blocks: many tokens
+                                 (600, 32), (700, 1056), (601, 4128), (593, 14336), (600, 32800)])
+def test_quantiser_of_any_type(M, K, dt):
     x = rand(M, K, seed=K, dtype=F.DTYPES[dt])
+    x[M // 2] = 0
     q = torch.empty(M, K, dtype=torch.int8, device="cuda")
     s = torch.empty(M, device="cuda")
     L = sbm.load()
-    rc = L.sherry_quant_act_dt(x.data_ptr(), {"bf16": 1, "f16": 2}[dt], M, K, q.data_ptr(), s.data_ptr(),
+    rc = L.sherry_quant_act_dt(x.data_ptr(), {"f32": 0, "bf16": 1, "f16": 2}[dt], M, K, q.data_ptr(), s.data_ptr(),
                                torch.cuda.current_stream().cuda_stream)
     assert rc == sbm.OK
     q_o, s_o = oracle.quant_act(np.ascontiguousarray(x.float().cpu().numpy()))
