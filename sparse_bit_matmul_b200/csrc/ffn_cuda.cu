@@ -26,55 +26,76 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Activation quantiser for any element type: the rule of quant_act_kernel, one
-// block per token.  Rows of up to kQuantXV 16-byte loads a thread stay in
-// registers between the absmax and the quantisation; longer ones are read
-// twice.  Blocks are as narrow as that allows when the tokens fill the SMs
-// (every load of a row in flight at once, little to synchronise: M=2048 bf16,
-// K=4096 QA us with 512 threads, QB so; K=14336 QC and QD), and a load a thread
-// when they do not (M=16 K=4096 QE and QF).
+// block per token.  Rows of up to XV 16-byte loads a thread stay in registers
+// between the absmax and the quantisation; longer ones are read twice.  When
+// the tokens fill the SMs, blocks are as narrow as four loads a thread allow
+// (little to synchronise, and other tokens hide a token's two passes: M=2048
+// bf16, K=4096 11.9 us with 512 threads, 7.8 so, 9.2 with eight loads; K=1024
+// 9.6, 4.4 and 4.4); when they do not, a thread has one load (M=333 K=1056 3.4
+// and 2.7).  Bound by issue: 16-bit values tie at half integers often, and
+// those take the exact division.
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 512;
-constexpr int kQuantXV = 8;
+constexpr int kQuantLoads = 4;
+constexpr int kQuantLoadsMax = 8;           // rows beyond kQuantLoads * kQuantThreads loads
 
 int quant_threads(int64_t M, int64_t units, int sms)
 {
-    const int64_t t = M >= 4 * (int64_t)sms ? (units + kQuantXV - 1) / kQuantXV : units;
+    const int64_t t = M >= 4 * (int64_t)sms ? (units + kQuantLoads - 1) / kQuantLoads : units;
     return (int)std::min<int64_t>(kQuantThreads, (t + 31) & ~int64_t(31));
 }
 
-// 16 bytes of activations: their largest magnitude, their int8 codes.
+// The largest magnitude of 16-byte pieces of a row (NaN: ignored), two values
+// at a time where they are 16-bit.
 template <class XT>
-struct Quant16 {
-    static constexpr int kWords = std::is_same_v<XT, float> ? 1 : 2;
-    float4 f[kWords];
+struct AbsMax {
+    using Pair = std::conditional_t<std::is_same_v<XT, __half>, __half2, __nv_bfloat162>;
+    static constexpr bool kWide = std::is_same_v<XT, float>;
+    std::conditional_t<kWide, float, Pair> a;
 
-    __device__ __forceinline__ explicit Quant16(const uint4& w)
+    __device__ __forceinline__ AbsMax()
     {
-        if constexpr (kWords == 1) {
-            f[0] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-        } else {
-            const uint2 lo = make_uint2(w.x, w.y), hi = make_uint2(w.z, w.w);
-            f[0] = decode::load_x4<XT>(reinterpret_cast<const XT*>(&lo), 0);
-            f[1] = decode::load_x4<XT>(reinterpret_cast<const XT*>(&hi), 0);
+        const uint32_t zero = 0u;
+        memcpy(&a, &zero, 4);
+    }
+    __device__ __forceinline__ void add(const uint4& w)
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kWide) {
+                a = fmaxf(a, fabsf(__uint_as_float(u[i])));
+            } else {
+                Pair p;
+                memcpy(&p, &u[i], 4);
+                a = __hmax2(a, __habs2(p));
+            }
         }
     }
-    __device__ __forceinline__ float absmax() const
+    __device__ __forceinline__ float get() const
     {
-        float a = quant::absmax4(f[0]);
-        if constexpr (kWords == 2) a = fmaxf(a, quant::absmax4(f[1]));
-        return a;
-    }
-    __device__ __forceinline__ void store(int8_t* row, int unit, const quant::Scale& sc) const
-    {
-        if constexpr (kWords == 1)
-            reinterpret_cast<uint32_t*>(row)[unit] = quant::quantise4(f[0], sc);
-        else
-            reinterpret_cast<uint2*>(row)[unit] = make_uint2(quant::quantise4(f[0], sc), quant::quantise4(f[1], sc));
+        if constexpr (kWide) return a;
+        else if constexpr (std::is_same_v<XT, __half>) return fmaxf(__low2float(a), __high2float(a));
+        else return fmaxf(__bfloat162float(a.x), __bfloat162float(a.y));
     }
 };
 
+// The int8 codes of 16 bytes of activations.
 template <class XT>
-__global__ void __launch_bounds__(kQuantThreads, 2)
+__device__ __forceinline__ void quantise16(int8_t* row, int unit, const uint4& w, const quant::Scale& sc)
+{
+    if constexpr (std::is_same_v<XT, float>) {
+        reinterpret_cast<uint32_t*>(row)[unit] = quant::quantise4(decode::load_x4<XT>(reinterpret_cast<const XT*>(&w), 0), sc);
+    } else {
+        const uint2 lo = make_uint2(w.x, w.y), hi = make_uint2(w.z, w.w);
+        reinterpret_cast<uint2*>(row)[unit] =
+            make_uint2(quant::quantise4(decode::load_x4<XT>(reinterpret_cast<const XT*>(&lo), 0), sc),
+                       quant::quantise4(decode::load_x4<XT>(reinterpret_cast<const XT*>(&hi), 0), sc));
+    }
+}
+
+template <class XT, int XV>
+__global__ void __launch_bounds__(kQuantThreads, XV == kQuantLoads ? 3 : 2)
     quant_rows_kernel(const XT* __restrict__ x, int64_t K, int8_t* __restrict__ q, float* __restrict__ scale)
 {
     ptx::pdl_launch_dependents();
@@ -84,21 +105,22 @@ __global__ void __launch_bounds__(kQuantThreads, 2)
     int8_t* qr = q + m * K;
     const int U = (int)(K * sizeof(XT) / 16), nthr = blockDim.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool in_regs = U <= kQuantXV * nthr;
+    const bool in_regs = U <= XV * nthr;
 
-    uint4 v[kQuantXV];
-    float a = 0.0f;
+    uint4 v[XV];
+    AbsMax<XT> mx;
     if (in_regs) {
 #pragma unroll
-        for (int u = 0; u < kQuantXV; ++u)
+        for (int u = 0; u < XV; ++u)
             v[u] = tid + u * nthr < U ? xr[tid + u * nthr] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int u = 0; u < kQuantXV; ++u)
-            if (u * nthr < U) a = fmaxf(a, Quant16<XT>(v[u]).absmax());
+        for (int u = 0; u < XV; ++u)
+            if (u * nthr < U) mx.add(v[u]);
     } else {
 #pragma unroll 4
-        for (int i = tid; i < U; i += nthr) a = fmaxf(a, Quant16<XT>(xr[i]).absmax());
+        for (int i = tid; i < U; i += nthr) mx.add(xr[i]);
     }
+    float a = mx.get();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     __shared__ float warp_max[kQuantThreads / 32];
@@ -112,19 +134,21 @@ __global__ void __launch_bounds__(kQuantThreads, 2)
     if (tid == 0) scale[m] = sc.s;
     if (in_regs) {
 #pragma unroll
-        for (int u = 0; u < kQuantXV; ++u)
-            if (tid + u * nthr < U) Quant16<XT>(v[u]).store(qr, tid + u * nthr, sc);
+        for (int u = 0; u < XV; ++u)
+            if (tid + u * nthr < U) quantise16<XT>(qr, tid + u * nthr, v[u], sc);
     } else {
 #pragma unroll 4
-        for (int i = tid; i < U; i += nthr) Quant16<XT>(xr[i]).store(qr, i, sc);
+        for (int i = tid; i < U; i += nthr) quantise16<XT>(qr, i, xr[i], sc);
     }
 }
 
 template <class XT>
 int launch_quant(const void* x, int64_t M, int64_t K, int8_t* q, float* scale, int sms, cudaStream_t s)
 {
-    return cuda_status(launch_pdl(quant_rows_kernel<XT>, dim3((unsigned)M),
-                                  dim3((unsigned)quant_threads(M, K * (int64_t)sizeof(XT) / 16, sms)), 0, s,
+    const int64_t units = K * (int64_t)sizeof(XT) / 16;
+    auto kernel = units <= kQuantLoads * kQuantThreads ? quant_rows_kernel<XT, kQuantLoads>
+                                                       : quant_rows_kernel<XT, kQuantLoadsMax>;
+    return cuda_status(launch_pdl(kernel, dim3((unsigned)M), dim3((unsigned)quant_threads(M, units, sms)), 0, s,
                                   static_cast<const XT*>(x), K, q, scale));
 }
 
