@@ -331,9 +331,10 @@ def _matrix(t, name: str):
     """Shape, sherry_dtype and device index of the [M][.] tensor a feed-forward call starts from."""
     code = _types().get(t.dtype)
     shape = t.shape
-    if code is None or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
+    idx = t.get_device()                                # -1: not on a GPU
+    if code is None or len(shape) != 2 or idx < 0 or not t.is_contiguous():
         _refuse(name, t, "[M][.] of float32, bfloat16 or float16")
-    return shape[0], shape[1], code, t.get_device()
+    return shape[0], shape[1], code, idx
 
 
 def _activation(act) -> int:
@@ -421,7 +422,7 @@ def repack_gated_t(gate_dev, up_dev, N: int, K: int, out=None):
 
 def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s):
     M, K, dt, idx = _matrix(x, "x")
-    if idx != _torch.cuda.current_device():
+    if idx != _torch._C._cuda_getDevice():
         with _torch.cuda.device(idx):
             return _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s)
     a = _activation(act)
@@ -439,7 +440,7 @@ def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q,
     qp = None if out_q is None else _ptr(out_q, "out_q", _torch.int8, (M, K), idx)
     sp = None if out_s is None else _ptr(out_s, "out_s", f32, (M,), idx)
     if out is None:
-        out = x.new_empty((M, N))
+        out = x.new_empty(M, N)
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", x.dtype, (M, N), idx)
@@ -485,17 +486,21 @@ def gated(x, w_native, alpha, N: int, bias=None, act: str = "silu", out=None, ac
 
 def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales):
     M, N, dt, idx = _matrix(dy, "dy")
-    if idx != _torch.cuda.current_device():
+    if idx != _torch._C._cuda_getDevice():
         with _torch.cuda.device(idx):
             return _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales)
     a = _activation(act)
     if N <= 0 or K <= 0 or K % 32:
         raise ValueError(f"want N > 0 and K a positive multiple of 32, got N={N}, K={K}")
-    _need(want_dx or want_scales, "nothing to compute: want_dx and want_scales are both False")
-    _need(acc is not None or not (gated or a != 0 or want_scales), "acc: needed for this gradient")
-    _need(acc is None or x_scale is not None, "x_scale: needed with acc")
+    if not (want_dx or want_scales):
+        raise ValueError("nothing to compute: want_dx and want_scales are both False")
+    if acc is None and (gated or a != 0 or want_scales):
+        raise ValueError("acc: needed for this gradient")
+    if acc is not None and x_scale is None:
+        raise ValueError("x_scale: needed with acc")
+    if alpha is None or (w_t is None and want_dx):
+        raise ValueError("alpha, and for dx w_t, are needed")
     R = 2 * N if gated else N
-    _need(alpha is not None and (w_t is not None or not want_dx), "alpha, and for dx w_t, are needed")
     f32 = _torch.float32
     ap = _ptr(alpha, "alpha", f32, (R,), idx)
     bp = None if bias is None else _ptr(bias, "bias", f32, (R,), idx)
@@ -504,7 +509,7 @@ def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, w
     dx = dalpha = dbias = wp = xp = kp = dap = dbp = None
     if want_dx:
         wp = _ptr(w_t, "w_t", _torch.uint8, (-(-R // 128) * -(-K // 128) * 4096,), idx)
-        dx = dy.new_empty((M, K)) if out is None else out
+        dx = dy.new_empty(M, K) if out is None else out
         xp = dx.data_ptr() if out is None else _ptr(out, "out", dy.dtype, (M, K), idx)
     if want_scales:
         make = _torch.empty_like if M else _torch.zeros_like
