@@ -360,6 +360,7 @@ def test_gradient_of_more_rows_than_shared_memory_holds():
 def test_more_tokens_than_one_grid_dimension():
     run_forward(True, 70001, 32, 3, "bf16", "silu", False, False)
     run_backward(True, 70001, 32, 3, "bf16", "silu", False)
+    run_backward(False, 131073, 32, 7, "f16", "gelu", True)
 
 
 @pytest.mark.parametrize("M", [4, 5, 6, 10, 11, 79, 81, 400, 401])
