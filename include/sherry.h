@@ -436,9 +436,13 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  *   linear   dz = dy * act'(z)           (the gradient of residual is dy)
  *   gated    dz[2n] = dh * z[2n + 1] * act'(z[2n]),  dz[2n + 1] = dh * act(z[2n])
  * The sums over n of dx run in integers: dz * alpha of a token becomes fixed
- * point below the token's largest |dz * alpha| (16 bits for SHERRY_BF16, 23
- * for SHERRY_F16, 31 for SHERRY_F32), cut into signed base-256 digits that the
- * tensor cores multiply with T exactly.  A token whose dz * alpha holds an
+ * point below the token's largest |dz * alpha| (23 bits for SHERRY_BF16 and
+ * SHERRY_F16, 31 for SHERRY_F32), cut into signed base-256 digits that the
+ * tensor cores multiply with T exactly.  Beside one |dz * alpha| r times the
+ * token's others, the columns of dx whose weight in that row is 0 are off by
+ * about 7e-8 r (SHERRY_F32: 5e-10 r) of themselves, above the rounding of the
+ * type from r = 20000 (SHERRY_BF16), 3000 (SHERRY_F16) or 100 (SHERRY_F32)
+ * on.  A token whose dz * alpha holds an
  * Inf or NaN gives a dx row of NaN.  Results do not depend on the launch
  * shape or on the order of any sum across blocks: the same call gives the
  * same bits.
@@ -512,9 +516,9 @@ int sherry_repack_gated_t(const uint8_t* gate_dev, const uint8_t* up_dev, int64_
  * Returns 0 for invalid arguments. */
 size_t sherry_grad_work_bytes(int dtype, int64_t M, int64_t R);
 
-/* Rows of int8 digits a token takes at most in a gradient call: sherry_reserve(this
- * times M, ..) sets aside the split-K workspace of sherry_linear_grad and
- * sherry_gated_grad.  0 for an invalid dtype. */
+/* Reserve factor of the gradient calls: sherry_reserve(this times M, ..) sets
+ * aside the split-K workspace of sherry_linear_grad and sherry_gated_grad with
+ * M tokens.  0 for an invalid dtype. */
 int sherry_grad_digits(int dtype);
 
 /*

@@ -489,7 +489,7 @@ int64_t digit_ld(int64_t R) { return (R + 127) & ~int64_t(127); }
 
 int64_t digit_rows(int dtype, int64_t M)
 {
-    return dtype == SHERRY_BF16 ? 2 * M : dtype == SHERRY_F16 ? (M + 4) / 5 * 16 : 4 * M;
+    return dtype == SHERRY_F32 ? 4 * M : (M + 4) / 5 * 16;
 }
 
 int64_t digit_bytes(int dtype, int64_t M, int64_t R)
@@ -537,7 +537,9 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.dalpha = dalpha;
     g.dbias = dbias;
     if (!dx) return grad::launch_columns(g, gated, act, dtype, di.sms, s);
-    const TilePlan plan = plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true);
+    // split tiles stay within what sherry_reserve(sherry_grad_digits(dtype) M, ..) sets aside
+    const TilePlan plan = plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true,
+                                     tc_token_tile(sherry_grad_digits(dtype) * M));
     st = grad::launch_ahead(g, gated, act, dtype, di.sms, s);
     if (st != SHERRY_OK) return st;
     tc::EpParams p = {};
@@ -550,9 +552,9 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     p.Mo = M;
     p.No = K;
     p.dtype = dtype;
-    if (dtype == SHERRY_BF16) return launch_grad_tc<grad::kDigits<SHERRY_BF16>>(g.dig, g.ld, p, plan, s);
-    if (dtype == SHERRY_F16) return launch_grad_tc<grad::kDigits<SHERRY_F16>>(g.dig, g.ld, p, plan, s);
-    return launch_grad_tc<grad::kDigits<SHERRY_F32>>(g.dig, g.ld, p, plan, s);
+    if (dtype == SHERRY_F32) return launch_grad_tc<grad::kDigits<SHERRY_F32>>(g.dig, g.ld, p, plan, s);
+    static_assert(grad::kDigits<SHERRY_BF16> == grad::kDigits<SHERRY_F16>, "one kernel for the 16-bit types");
+    return launch_grad_tc<grad::kDigits<SHERRY_F16>>(g.dig, g.ld, p, plan, s);
 }
 
 int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)

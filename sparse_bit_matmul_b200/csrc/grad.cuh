@@ -9,12 +9,17 @@
 //   dalpha[n] = sum_m dz acc s,  dbias[n] = sum_m dz
 //
 // Fixed point.  e of a token is scaled to integers v below its largest |e|:
-// D = 2 digits (bf16 tensors) |v| <= 32639 = 127 (256 + 1), so e is off by at
-// most 2^-16 of the token's largest (a bf16 output rounds by 2^-9 of itself);
-// D = 3 (fp16) a power of two with |v| < 2^22, off by at most 2^-22 (an output
-// rounds by 2^-12; four digits: M=1386 K=1504, gated to 14319 367 us, three 339);
+// D = 3 digits (bf16 and fp16 tensors) |v| <= 2^22 - 1, so e is off by at most
+// 2^-23 of the token's largest;
 // D = 4 (fp32) a power of two with |v| < 2^30, exact for every e within a
 // factor 64 of the largest and off by at most 2^-30 of it below.
+// The error is the token's, not the term's: beside one |e| r times the others,
+// the columns of dx whose weight in that row is 0 (a quarter of them) hold the
+// others alone, and are off by about 7e-8 r of themselves (D = 3; D = 4 5e-10 r
+// to 3e-10 r).  A bf16 output rounds by 1.7e-3 in the same norm, an fp16 one by
+// 2.1e-4: r = 20000 and r = 3000 reach that.  Two digits would reach it at r =
+// 200 for bf16 (r = 1000: 0.9 %), and outliers of that size are ordinary behind
+// a gate.  Four digits for fp16: M=1386 K=1504, gated to 14319 367 us, three 339.
 // v = sum_d 256^d digit_d with digits in [-128, 127]: the integer sums over n
 // below 2^24 rows stay inside int32.
 #pragma once
@@ -64,7 +69,7 @@ __device__ __forceinline__ float widen(typename Elem<DT>::type v)
 }
 
 template <int DT>
-constexpr int kDigits = DT == SHERRY_BF16 ? 2 : DT == SHERRY_F16 ? 3 : 4;
+constexpr int kDigits = DT == SHERRY_F32 ? 4 : 3;
 
 __device__ __forceinline__ float pre_act(int32_t acc, float al, float s, bool has_bias, float b)
 {
@@ -236,7 +241,7 @@ struct Segment {
 // cluster, then the digit rows.
 // Bound by instruction issue and DRAM in about equal parts: magnitudes are
 // compared as integers (one mask and one maximum a value; Inf and NaN order
-// above every number), and two or three digits come out of the low bits of
+// above every number), and three digits come out of the low bits of
 // e * inv + 1.5 * 2^23 without a conversion instruction.
 constexpr int kDigitThreads = 256;
 constexpr uint32_t kInfBits = 0x7F800000u;
@@ -293,17 +298,17 @@ __device__ __forceinline__ void grad_digits(const Params& p, int64_t m, uint32_t
     const float big = __uint_as_float(mx);
     float inv = 0.0f, sc = 0.0f;
     if (mx != 0u && !bad) {
-        if constexpr (D == 2) {
+        if constexpr (D == 3) {
             if (big >= 7.8886091e-31f) {                     // 2^-100
-                inv = __fdiv_rn(32639.0f, big);
-                sc = __fdiv_rn(big, 32639.0f);
+                inv = __fdiv_rn(4194303.0f, big);
+                sc = __fdiv_rn(big, 4194303.0f);
             } else {
-                inv = 2.0769187e34f;                         // 2^114
-                sc = 4.8148249e-35f;
+                inv = 5.316912e36f;                          // 2^122
+                sc = 1.8807910e-37f;
             }
         } else {
             const int ex = (int)(mx >> 23) - 127;            // big < 2^(ex + 1)
-            const int k = min((D == 3 ? 21 : 29) - ex, 126);
+            const int k = min(29 - ex, 126);
             inv = __uint_as_float((uint32_t)(127 + k) << 23);
             sc = __uint_as_float((uint32_t)(127 - k) << 23);
         }
@@ -329,7 +334,7 @@ __device__ __forceinline__ void grad_digits(const Params& p, int64_t m, uint32_t
         for (int k = 0; k < 4; ++k) {
             v[k] = D < 4 ? __float_as_uint(__fmaf_rn(e[k], inv, quant::kRoundMagic))
                          : (uint32_t)__float2int_rn(__fmul_rn(e[k], inv));
-            if (D == 3) v[k] -= __float_as_uint(quant::kRoundMagic);
+            if constexpr (D < 4) v[k] -= __float_as_uint(quant::kRoundMagic);
         }
         // digit d is byte d of v once 128 was added to every byte below it:
         // (v - digit) / 256 is (v + 128) >> 8 for a digit in [-128, 127]

@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
 {
     using C = Cfg<BN, SC, WF, EG>;
     static_assert(EK != kEpPlain || EG == 1, "EG");
-    static_assert(EK == kEpGrad ? D >= 2 && D <= 4 : D == 1, "digits per token");
+    static_assert(EK == kEpGrad ? D == 3 || D == 4 : D == 1, "digits per token");
     // Few tokens and fewer tiles than SMs: the CTAs of a cluster take a share of
     // a tile's chunks each and add their sums into the first one's staging
     // slots over distributed shared memory (M = 16 bf16: K = 4096, N = 4096

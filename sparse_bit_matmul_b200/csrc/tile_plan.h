@@ -43,8 +43,9 @@ struct TilePlan {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// grad: the launch reads the transposed weight (kEpGrad).
-inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, double w, bool grad)
+// grad: the launch reads the transposed weight (kEpGrad).  split_bn: the
+// largest tile that may be split through the workspace.
+inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, double w, bool grad, int split_bn)
 {
     struct Tile {
         int bn, eg;
@@ -77,8 +78,7 @@ inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, doubl
                 best = {t.bn, 1, T * S, 0, S};
             }
         }
-        // split launches stay within the workspace of sherry_reserve(M, ..)
-        if (t.eg == 2 || t.bn > tc_token_tile(M)) continue;
+        if (t.eg == 2 || t.bn > split_bn) continue;
         const double sums = 3.6 + 0.075 * t.bn;
         double split;
         int64_t grid;
@@ -101,6 +101,12 @@ inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, doubl
         }
     }
     return best;
+}
+
+// With split tiles within the workspace of sherry_reserve(M, ..).
+inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, double w, bool grad)
+{
+    return plan_tiles(M, TN, Kc, sms, w, grad, tc_token_tile(M));
 }
 
 }  // namespace sherry
