@@ -268,9 +268,10 @@ int make_out_map(CUtensorMap* map, void* out, int dtype, int64_t Mo, int64_t No,
 }
 
 // One tensor-core launch.  b: int8 rows [p.M][p.K], ld bytes apart.  p holds
-// the problem; tiles, workspace and status are filled in here.
-template <int BN, int SC, int WF, int EK, int D, int EG = 1>
-int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan, cudaStream_t stream)
+// the problem; tiles, workspace and status are filled in here.  `ahead` launches
+// what the product reads, once nothing but a launch can fail any more.
+template <int BN, int SC, int WF, int EK, int D, int EG = 1, class Ahead>
+int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan, cudaStream_t stream, const Ahead& ahead)
 {
     using C = tc::Cfg<BN, SC, WF, EG>;
     DeviceInfo di;
@@ -319,6 +320,8 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (st != SHERRY_OK) return st;
+    st = ahead();
+    if (st != SHERRY_OK) return st;
     return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream,
                                   dim3((unsigned)std::max(1, plan.cluster)), map, maps, p));
 }
@@ -335,45 +338,46 @@ double epilogue_weight(const tc::EpParams& p, bool gated)
     return gated ? 0.75 * w : w;
 }
 
-template <int EK>
-int launch_forward_tc(const int8_t* b, const tc::EpParams& p, int sms, cudaStream_t s)
+template <int EK, class Ahead>
+int launch_forward_tc(const int8_t* b, const tc::EpParams& p, int sms, cudaStream_t s, const Ahead& ahead)
 {
     constexpr int W = tc::kWeightSherry;
     const TilePlan plan = plan_tiles(p.M, sherry_row_tiles(p.N), sherry_k_chunks(p.K), sms,
                                      epilogue_weight(p, EK == tc::kEpGated), false);
-    if (plan.eg == 2) return plan.bn == 64 ? launch_tc<64, 4, W, EK, 1, 2>(b, p.K, p, plan, s)
-                                           : launch_tc<128, 2, W, EK, 1, 2>(b, p.K, p, plan, s);
+    if (plan.eg == 2) return plan.bn == 64 ? launch_tc<64, 4, W, EK, 1, 2>(b, p.K, p, plan, s, ahead)
+                                           : launch_tc<128, 2, W, EK, 1, 2>(b, p.K, p, plan, s, ahead);
     switch (plan.bn) {
-    case 16: return launch_tc<16, 4, W, EK, 1>(b, p.K, p, plan, s);
-    case 32: return launch_tc<32, 4, W, EK, 1>(b, p.K, p, plan, s);
-    case 64: return launch_tc<64, 4, W, EK, 1>(b, p.K, p, plan, s);
-    case 128: return launch_tc<128, 2, W, EK, 1>(b, p.K, p, plan, s);
-    default: return launch_tc<192, 1, W, EK, 1>(b, p.K, p, plan, s);
+    case 16: return launch_tc<16, 4, W, EK, 1>(b, p.K, p, plan, s, ahead);
+    case 32: return launch_tc<32, 4, W, EK, 1>(b, p.K, p, plan, s, ahead);
+    case 64: return launch_tc<64, 4, W, EK, 1>(b, p.K, p, plan, s, ahead);
+    case 128: return launch_tc<128, 2, W, EK, 1>(b, p.K, p, plan, s, ahead);
+    default: return launch_tc<192, 1, W, EK, 1>(b, p.K, p, plan, s, ahead);
     }
 }
 
 // kWeightT2 chunks are 4 KB: two-chunk stages from 64 rows on keep at least
 // three stages in the ring.
-template <int D>
-int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, const TilePlan& plan, cudaStream_t s)
+template <int D, class Ahead>
+int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, const TilePlan& plan, cudaStream_t s,
+                   const Ahead& ahead)
 {
     constexpr int W = tc::kWeightT2, EK = tc::kEpGrad;
-    if (plan.eg == 2) return launch_tc<192, 1, W, EK, D, 2>(b, ld, p, plan, s);
+    if (plan.eg == 2) return launch_tc<192, 1, W, EK, D, 2>(b, ld, p, plan, s, ahead);
     switch (plan.bn) {
-    case 16: return launch_tc<16, 4, W, EK, D>(b, ld, p, plan, s);
-    case 32: return launch_tc<32, 4, W, EK, D>(b, ld, p, plan, s);
-    case 64: return launch_tc<64, 2, W, EK, D>(b, ld, p, plan, s);
-    case 128: return launch_tc<128, 2, W, EK, D>(b, ld, p, plan, s);
-    default: return launch_tc<192, 1, W, EK, D>(b, ld, p, plan, s);
+    case 16: return launch_tc<16, 4, W, EK, D>(b, ld, p, plan, s, ahead);
+    case 32: return launch_tc<32, 4, W, EK, D>(b, ld, p, plan, s, ahead);
+    case 64: return launch_tc<64, 2, W, EK, D>(b, ld, p, plan, s, ahead);
+    case 128: return launch_tc<128, 2, W, EK, D>(b, ld, p, plan, s, ahead);
+    default: return launch_tc<192, 1, W, EK, D>(b, ld, p, plan, s, ahead);
     }
 }
 
-template <int MT, bool FUSED, int RT, class XT>
-int launch_decode_rt(const decode::EpParams& p, const decode::Plan& pl, cudaStream_t stream)
+template <int MT, bool FUSED, int RT, class XT, class Ahead>
+int launch_decode_rt(const decode::EpParams& p, const decode::Plan& pl, cudaStream_t stream, const Ahead& ahead)
 {
     auto kernel = decode::sherry_decode_kernel<MT, FUSED, RT, XT, true>;
     static std::atomic<uint64_t> done{0};
-    const int st = once_per_device(done, [&] {
+    int st = once_per_device(done, [&] {
         // one carveout for every shape, so that the next call's CTAs share the SM
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, decode::kSmemBudgetMax);
         if (e == cudaSuccess)
@@ -382,11 +386,14 @@ int launch_decode_rt(const decode::EpParams& p, const decode::Plan& pl, cudaStre
         return e;
     });
     if (st != SHERRY_OK) return st;
+    st = ahead();
+    if (st != SHERRY_OK) return st;
     return cuda_status(launch_pdl(kernel, dim3((unsigned)pl.G), dim3((unsigned)pl.threads), (size_t)pl.smem, stream, p));
 }
 
-template <int MT, bool FUSED, class XT>
-int launch_decode(decode::EpParams p, const decode::Plan& pl, const DeviceInfo& di, cudaStream_t stream)
+template <int MT, bool FUSED, class XT, class Ahead>
+int launch_decode(decode::EpParams p, const decode::Plan& pl, const DeviceInfo& di, cudaStream_t stream,
+                  const Ahead& ahead)
 {
     p.Kc = sherry_k_chunks(p.K);
     p.G = pl.G;
@@ -397,9 +404,9 @@ int launch_decode(decode::EpParams p, const decode::Plan& pl, const DeviceInfo& 
     p.NS = pl.NS;
     p.S = pl.S;
     if (pl.smem > di.max_smem_optin) return SHERRY_ERR_DEVICE;
-    if (pl.RT == 4) return launch_decode_rt<MT, FUSED, 4, XT>(p, pl, stream);
-    if (pl.RT == 2) return launch_decode_rt<MT, FUSED, 2, XT>(p, pl, stream);
-    return launch_decode_rt<MT, FUSED, 1, XT>(p, pl, stream);
+    if (pl.RT == 4) return launch_decode_rt<MT, FUSED, 4, XT>(p, pl, stream, ahead);
+    if (pl.RT == 2) return launch_decode_rt<MT, FUSED, 2, XT>(p, pl, stream, ahead);
+    return launch_decode_rt<MT, FUSED, 1, XT>(p, pl, stream, ahead);
 }
 
 // Both forward operators: R weight rows, No output columns.
@@ -445,9 +452,10 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
         d.x = static_cast<const float*>(x);
         d.xq_out = x_i8;
         d.xs_out = x_scale;
-        if (dtype == SHERRY_F32) return launch_decode<1, true, float>(d, pl, di, s);
-        if (dtype == SHERRY_BF16) return launch_decode<1, true, __nv_bfloat16>(d, pl, di, s);
-        return launch_decode<1, true, __half>(d, pl, di, s);
+        const auto none = [] { return (int)SHERRY_OK; };
+        if (dtype == SHERRY_F32) return launch_decode<1, true, float>(d, pl, di, s, none);
+        if (dtype == SHERRY_BF16) return launch_decode<1, true, __nv_bfloat16>(d, pl, di, s, none);
+        return launch_decode<1, true, __half>(d, pl, di, s, none);
     }
     if (!x_i8) {
         void* buf = nullptr;
@@ -457,12 +465,11 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
         if (!x_scale)
             x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + (((size_t)M * (size_t)K + 255) & ~size_t(255)));
     }
-    st = sherry_quant_act_dt(x, dtype, M, K, x_i8, x_scale, s);
-    if (st != SHERRY_OK) return st;
+    const auto quantise = [&] { return sherry_quant_act_dt(x, dtype, M, K, x_i8, x_scale, s); };
     if (few) {
         d.xq = x_i8;
         d.x_scale = x_scale;
-        return launch_decode<2, false, float>(d, pl, di, s);
+        return launch_decode<2, false, float>(d, pl, di, s, quantise);
     }
     tc::EpParams p = {};
     p.wnative = static_cast<const uint8_t*>(wn);
@@ -479,8 +486,8 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     p.No = No;
     p.dtype = dtype;
     p.act = act;
-    return gated ? launch_forward_tc<tc::kEpGated>(x_i8, p, di.sms, s)
-                 : launch_forward_tc<tc::kEpLinear>(x_i8, p, di.sms, s);
+    return gated ? launch_forward_tc<tc::kEpGated>(x_i8, p, di.sms, s, quantise)
+                 : launch_forward_tc<tc::kEpLinear>(x_i8, p, di.sms, s, quantise);
 }
 
 // Row stride of the digit rows: whole 128-byte lines, so that a TMA box row is
@@ -540,8 +547,7 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     // split tiles stay within what sherry_reserve(sherry_grad_digits(dtype) M, ..) sets aside
     const TilePlan plan = plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true,
                                      tc_token_tile(sherry_grad_digits(dtype) * M));
-    st = grad::launch_ahead(g, gated, act, dtype, di.sms, s);
-    if (st != SHERRY_OK) return st;
+    const auto digits = [&] { return grad::launch_ahead(g, gated, act, dtype, di.sms, s); };
     tc::EpParams p = {};
     p.wnative = static_cast<const uint8_t*>(wt);
     p.x_scale = g.dscale;
@@ -552,9 +558,9 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     p.Mo = M;
     p.No = K;
     p.dtype = dtype;
-    if (dtype == SHERRY_F32) return launch_grad_tc<grad::kDigits<SHERRY_F32>>(g.dig, g.ld, p, plan, s);
+    if (dtype == SHERRY_F32) return launch_grad_tc<grad::kDigits<SHERRY_F32>>(g.dig, g.ld, p, plan, s, digits);
     static_assert(grad::kDigits<SHERRY_BF16> == grad::kDigits<SHERRY_F16>, "one kernel for the 16-bit types");
-    return launch_grad_tc<grad::kDigits<SHERRY_F16>>(g.dig, g.ld, p, plan, s);
+    return launch_grad_tc<grad::kDigits<SHERRY_F16>>(g.dig, g.ld, p, plan, s, digits);
 }
 
 int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)
