@@ -446,9 +446,17 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  * Inf or NaN gives a dx row of NaN.  Results do not depend on the launch
  * shape or on the order of any sum across blocks: the same call gives the
  * same bits.
- * Tensors are dense row-major.  Workspace, concurrency and errors are those
- * of sherry_linear.  An output that overlaps an input or another output is
- * refused, but for y == residual.
+ * Tensors are dense row-major.  Errors are those of sherry_linear.  An output
+ * that overlaps an input or another output is refused, but for y == residual.
+ * Split-K workspace: a call with many chunks and few tiles sums tiles across
+ * CTAs.  The _ws forms take the memory for that from the caller (`split`, at
+ * least the bytes that the matching _split_bytes function gives on the same
+ * device, 16-byte aligned, any contents, this call's alone until it has
+ * completed; fewer bytes than it needs: SHERRY_ERR_WORKSPACE), so that calls
+ * with buffers of their own may run at the same time.  The other forms, and
+ * split == NULL, use the reserved workspace, and the rule at the top of this
+ * file holds for them: no two at the same time on one device, replays of
+ * captured graphs included.
  * =========================================================================== */
 
 /* sherry_quant_act for x of any element type (x [M][K], 16-byte aligned). */
@@ -482,6 +490,14 @@ int sherry_linear_epilogue(const void* x, int x_dtype, const void* Wnative, cons
                            const float* bias, int act, const void* residual, void* y, int32_t* acc,
                            int8_t* x_i8, float* x_scale, int64_t M, int64_t N, int64_t K, void* stream);
 
+/* The same with the caller's split-K workspace.  residual and acc in the size
+ * query: whether the call has one. */
+size_t sherry_linear_split_bytes(int x_dtype, int act, int residual, int acc, int64_t M, int64_t N, int64_t K);
+int sherry_linear_epilogue_ws(const void* x, int x_dtype, const void* Wnative, const float* alpha,
+                              const float* bias, int act, const void* residual, void* y, int32_t* acc,
+                              int8_t* x_i8, float* x_scale, void* split, size_t split_size, int64_t M,
+                              int64_t N, int64_t K, void* stream);
+
 /*
  * sherry_gated -- device, asynchronous.  Both projections, the activation and
  * the product in one contraction kernel (for one token also the quantiser).
@@ -492,6 +508,12 @@ int sherry_linear_epilogue(const void* x, int x_dtype, const void* Wnative, cons
 int sherry_gated(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias,
                  int act, void* h, int32_t* acc, int8_t* x_i8, float* x_scale, int64_t M, int64_t N,
                  int64_t K, void* stream);
+
+/* The same with the caller's split-K workspace. */
+size_t sherry_gated_split_bytes(int x_dtype, int act, int acc, int64_t M, int64_t N, int64_t K);
+int sherry_gated_ws(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias,
+                    int act, void* h, int32_t* acc, int8_t* x_i8, float* x_scale, void* split, size_t split_size,
+                    int64_t M, int64_t N, int64_t K, void* stream);
 
 /* Bytes of the transposed layout that the gradients read, for an R x K weight
  * (R = 2N for a gated pair): ceil(K/128) * ceil(R/128) * 4096, 2 bits a
@@ -549,6 +571,18 @@ int sherry_linear_grad(const void* dy, int dtype, const int32_t* acc, const floa
 int sherry_gated_grad(const void* dh, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
                       const float* alpha, const float* bias, int act, void* dx, float* dalpha,
                       float* dbias, void* work, int64_t M, int64_t N, int64_t K, void* stream);
+
+/* Both with the caller's split-K workspace, of sherry_grad_split_bytes(dtype,
+ * M, R, K) bytes (R = 2N for sherry_gated_grad_ws; calls without dx use none). */
+size_t sherry_grad_split_bytes(int dtype, int64_t M, int64_t R, int64_t K);
+int sherry_linear_grad_ws(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                          const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
+                          void* work, void* split, size_t split_size, int64_t M, int64_t N, int64_t K,
+                          void* stream);
+int sherry_gated_grad_ws(const void* dh, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                         const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
+                         void* work, void* split, size_t split_size, int64_t M, int64_t N, int64_t K,
+                         void* stream);
 
 /*
  * sherry_selftest_wait -- device, asynchronous.  A check of failure

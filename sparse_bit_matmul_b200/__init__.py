@@ -33,6 +33,8 @@ ABI_SYMBOLS = (
     "sherry_quant_act_dt", "sherry_repack_gated", "sherry_linear_epilogue", "sherry_gated",
     "sherry_transposed_bytes", "sherry_repack_t", "sherry_repack_gated_t", "sherry_grad_work_bytes",
     "sherry_grad_digits", "sherry_linear_grad", "sherry_gated_grad",
+    "sherry_linear_split_bytes", "sherry_linear_epilogue_ws", "sherry_gated_split_bytes", "sherry_gated_ws",
+    "sherry_grad_split_bytes", "sherry_linear_grad_ws", "sherry_gated_grad_ws",
 )
 
 _lib = None
@@ -103,6 +105,14 @@ def load() -> ctypes.CDLL:
     grad = [vp, c_int, vp, vp, vp, vp, vp, c_int, vp, vp, vp, vp, i64, i64, i64, vp]
     L.sherry_linear_grad.argtypes = grad
     L.sherry_gated_grad.argtypes = grad
+    split = [vp, ctypes.c_size_t, i64, i64, i64, vp]           # in place of M, N, K, stream
+    for name in ("sherry_linear_epilogue", "sherry_gated", "sherry_linear_grad", "sherry_gated_grad"):
+        getattr(L, name + "_ws").argtypes = getattr(L, name).argtypes[:-4] + split
+    L.sherry_linear_split_bytes.argtypes = [c_int, c_int, c_int, c_int, i64, i64, i64]
+    L.sherry_gated_split_bytes.argtypes = [c_int, c_int, c_int, i64, i64, i64]
+    L.sherry_grad_split_bytes.argtypes = [c_int, i64, i64, i64]
+    for name in ("linear", "gated", "grad"):
+        getattr(L, f"sherry_{name}_split_bytes").restype = ctypes.c_size_t
     for name in ABI_SYMBOLS:
         getattr(L, name).restype = getattr(L, name).restype or c_int
     _lib = L
@@ -344,9 +354,19 @@ def _activation(act) -> int:
     return a
 
 
-@functools.lru_cache(maxsize=256)
-def _work_bytes(dtype: int, M: int, R: int) -> int:
-    return int(load().sherry_grad_work_bytes(dtype, M, R))
+@functools.lru_cache(maxsize=1024)
+def _forward_split_bytes(idx: int, gated: bool, dtype: int, act: int, res: bool, acc: bool, M: int, N: int, K: int) -> int:
+    """Split-K workspace of a forward call on device idx (the current one)."""
+    if gated:
+        return int(load().sherry_gated_split_bytes(dtype, act, acc, M, N, K))
+    return int(load().sherry_linear_split_bytes(dtype, act, res, acc, M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def _grad_bytes(idx: int, dtype: int, M: int, R: int, K: int):
+    """Work buffer (a multiple of 16) and split-K workspace of a gradient call on device idx."""
+    return ((int(load().sherry_grad_work_bytes(dtype, M, R)) + 15) & ~15,
+            int(load().sherry_grad_split_bytes(dtype, M, R, K)))
 
 
 def _stream_of(idx: int):
@@ -366,10 +386,9 @@ def _on_device(fn):
 
 
 def reserve_split(device=None):
-    """Sets aside, host-synchronously, the split-K workspace (about 15 MB) of every linear_epilogue, gated
-    and gradient call on `device` (default: the current one).  The first such call does it too; do it
-    before capturing a graph.  All calls on the device share it (sherry.h): two that may run at the same
-    time, replays of captured graphs included, need one stream or events between them."""
+    """Sets aside, host-synchronously, the split-K workspace (about 15 MB) of the C entry points that take
+    none from the caller, for any number of tokens on `device` (default: the current one).  Such calls
+    share it (sherry.h); linear_epilogue, gated and the gradients bring their own and need no reserve."""
     _types()
     dev = _torch.device("cuda" if device is None else device) if not isinstance(device, int) else \
         _torch.device("cuda", device)
@@ -446,20 +465,27 @@ def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q,
         op = _ptr(out, "out", x.dtype, (M, N), idx)
     if M == 0:
         return out
-    if qp is None and (M > 1 or K > 65536) or qp is not None and sp is None:
-        # the call's own buffer for the int8 activations and their scales: nothing is shared with other
-        # streams or graphs
-        own = w_native.new_empty(M * K + 4 * M)         # K % 32 == 0: the scales are aligned
+    # the call's own buffer for the int8 activations, their scales and the split-K sums: nothing is shared
+    # with other streams or graphs (one token of up to 65536 needs none)
+    kp, split = None, 0
+    if M > 1 or K > 65536:
+        split = _forward_split_bytes(idx, gated, dt, a, rp is not None, cp is not None, M, N, K)
+        at = (M * K + 4 * M + 15) & ~15                 # K % 32 == 0: the scales are aligned
+        own = w_native.new_empty(at + split)
         if qp is None:
             qp = own.data_ptr()
         if sp is None:
             sp = own.data_ptr() + M * K
-    if idx not in _split_reserved:
-        reserve_split(idx)
+        if split:
+            kp = own.data_ptr() + at
+    elif qp is not None and sp is None:
+        own = w_native.new_empty(4)
+        sp = own.data_ptr()
     if gated:
-        rc = _lib.sherry_gated(x.data_ptr(), dt, wp, ap, bp, a, op, cp, qp, sp, M, N, K, _stream_of(idx))
+        rc = _lib.sherry_gated_ws(x.data_ptr(), dt, wp, ap, bp, a, op, cp, qp, sp, kp, split, M, N, K, _stream_of(idx))
     else:
-        rc = _lib.sherry_linear_epilogue(x.data_ptr(), dt, wp, ap, bp, a, rp, op, cp, qp, sp, M, N, K, _stream_of(idx))
+        rc = _lib.sherry_linear_epilogue_ws(x.data_ptr(), dt, wp, ap, bp, a, rp, op, cp, qp, sp, kp, split, M, N, K,
+                                            _stream_of(idx))
     if rc != OK:
         _check(rc, "sherry_gated" if gated else "sherry_linear_epilogue")
     return out
@@ -506,7 +532,8 @@ def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, w
     bp = None if bias is None else _ptr(bias, "bias", f32, (R,), idx)
     cp = None if acc is None else _ptr(acc, "acc", _torch.int32, (M, R), idx)
     sp = None if x_scale is None else _ptr(x_scale, "x_scale", f32, (M,), idx)
-    dx = dalpha = dbias = wp = xp = kp = dap = dbp = None
+    dx = dalpha = dbias = wp = xp = kp = dap = dbp = lp = None
+    split = 0
     if want_dx:
         wp = _ptr(w_t, "w_t", _torch.uint8, (-(-R // 128) * -(-K // 128) * 4096,), idx)
         dx = dy.new_empty(M, K) if out is None else out
@@ -518,12 +545,13 @@ def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, w
     if M == 0:
         return dx, dalpha, dbias
     if want_dx:
-        work = w_t.new_empty(_work_bytes(dt, M, R))
+        digits, split = _grad_bytes(idx, dt, M, R, K)
+        work = w_t.new_empty(digits + split)            # nothing is shared with other streams or graphs
         kp = work.data_ptr()
-        if idx not in _split_reserved:
-            reserve_split(idx)
-    fn = _lib.sherry_gated_grad if gated else _lib.sherry_linear_grad
-    rc = fn(dy.data_ptr(), dt, cp, sp, wp, ap, bp, a, xp, dap, dbp, kp, M, N, K, _stream_of(idx))
+        if split:
+            lp = kp + digits
+    fn = _lib.sherry_gated_grad_ws if gated else _lib.sherry_linear_grad_ws
+    rc = fn(dy.data_ptr(), dt, cp, sp, wp, ap, bp, a, xp, dap, dbp, kp, lp, split, M, N, K, _stream_of(idx))
     if rc != OK:
         _check(rc, "sherry_gated_grad" if gated else "sherry_linear_grad")
     return dx, dalpha, dbias

@@ -45,6 +45,12 @@ int quant_threads(int64_t M, int64_t units, int sms)
     return (int)std::min<int64_t>(kQuantThreads, (t + 31) & ~int64_t(31));
 }
 
+// Memory that a launch clears for the next one.
+struct Zero {
+    uint4* p;
+    int64_t n;
+};
+
 // The largest magnitude of 16-byte pieces of a row (NaN: ignored), two values
 // at a time where they are 16-bit.
 template <class XT>
@@ -96,7 +102,8 @@ __device__ __forceinline__ void quantise16(int8_t* row, int unit, const uint4& w
 
 template <class XT, int XV>
 __global__ void __launch_bounds__(kQuantThreads, XV == kQuantLoads ? 3 : 2)
-    quant_rows_kernel(const XT* __restrict__ x, int64_t K, int8_t* __restrict__ q, float* __restrict__ scale)
+    quant_rows_kernel(const XT* __restrict__ x, int64_t K, int8_t* __restrict__ q, float* __restrict__ scale,
+                      uint4* __restrict__ zero, int64_t zero_n)
 {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
@@ -140,16 +147,26 @@ __global__ void __launch_bounds__(kQuantThreads, XV == kQuantLoads ? 3 : 2)
 #pragma unroll 4
         for (int i = tid; i < U; i += nthr) quantise16<XT>(qr, i, xr[i], sc);
     }
+    // the split-K workspace of the launch behind
+    for (int64_t i = m * nthr + tid; i < zero_n; i += (int64_t)gridDim.x * nthr) zero[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <class XT>
-int launch_quant(const void* x, int64_t M, int64_t K, int8_t* q, float* scale, int sms, cudaStream_t s)
+int launch_quant(const void* x, int64_t M, int64_t K, int8_t* q, float* scale, Zero zero, int sms, cudaStream_t s)
 {
     const int64_t units = K * (int64_t)sizeof(XT) / 16;
     auto kernel = units <= kQuantLoads * kQuantThreads ? quant_rows_kernel<XT, kQuantLoads>
                                                        : quant_rows_kernel<XT, kQuantLoadsMax>;
     return cuda_status(launch_pdl(kernel, dim3((unsigned)M), dim3((unsigned)quant_threads(M, units, sms)), 0, s,
-                                  static_cast<const XT*>(x), K, q, scale));
+                                  static_cast<const XT*>(x), K, q, scale, zero.p, zero.n));
+}
+
+int launch_quant(const void* x, int dtype, int64_t M, int64_t K, int8_t* q, float* scale, Zero zero, int sms,
+                 cudaStream_t s)
+{
+    if (dtype == SHERRY_F32) return launch_quant<float>(x, M, K, q, scale, zero, sms, s);
+    if (dtype == SHERRY_BF16) return launch_quant<__nv_bfloat16>(x, M, K, q, scale, zero, sms, s);
+    return launch_quant<__half>(x, M, K, q, scale, zero, sms, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -267,11 +284,28 @@ int make_out_map(CUtensorMap* map, void* out, int dtype, int64_t Mo, int64_t No,
                : SHERRY_ERR_CUDA;
 }
 
+// A call's split-K workspace: the caller's (any contents; cleared by the launch
+// ahead of the product), or with a null p the reserved one (all zero between
+// calls).
+struct Split {
+    void* p;
+    size_t bytes;
+};
+
+// What launch_tc needs of it: the slots of the split tiles, and their counters.
+size_t split_bytes(const TilePlan& plan, int64_t M, int64_t TN)
+{
+    const int64_t n = split_tiles(plan, ceil_div(M, plan.bn) * TN);
+    return (size_t)(n * plan.bn * SHERRY_TILE_ROWS * 4 + ((4 * n + 15) & ~int64_t(15)));
+}
+
 // One tensor-core launch.  b: int8 rows [p.M][p.K], ld bytes apart.  p holds
 // the problem; tiles, workspace and status are filled in here.  `ahead` launches
-// what the product reads, once nothing but a launch can fail any more.
+// what the product reads, once nothing but a launch can fail any more, and
+// clears the workspace it is given.
 template <int BN, int SC, int WF, int EK, int D, int EG = 1, class Ahead>
-int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan, cudaStream_t stream, const Ahead& ahead)
+int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan, Split split, cudaStream_t stream,
+              const Ahead& ahead)
 {
     using C = tc::Cfg<BN, SC, WF, EG>;
     DeviceInfo di;
@@ -287,13 +321,17 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
     p.cluster = plan.cluster;
     p.ws = nullptr;
     p.counters = nullptr;
-    if (!p.whole && !p.cluster) {
-        void* ws = nullptr;
-        const size_t ws_acc = (size_t)grid * BN * SHERRY_TILE_ROWS * sizeof(int32_t);
-        st = get_workspace(ws_acc + (size_t)grid * sizeof(uint32_t), &ws);
-        if (st != SHERRY_OK) return st;
-        p.ws = static_cast<int32_t*>(ws);
-        p.counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + ws_acc);
+    Zero zero = {nullptr, 0};
+    if (const size_t need = split_bytes(plan, p.M, p.TN)) {
+        if (split.p) {
+            if (split.bytes < need) return SHERRY_ERR_WORKSPACE;
+            zero = {static_cast<uint4*>(split.p), (int64_t)(need / 16)};
+        } else {
+            st = get_workspace(need, &split.p);
+            if (st != SHERRY_OK) return st;
+        }
+        p.ws = static_cast<int32_t*>(split.p);
+        p.counters = reinterpret_cast<uint32_t*>(p.ws + split_tiles(plan, p.TM * p.TN) * BN * SHERRY_TILE_ROWS);
     }
     p.status = device_status_ptr();
     if (!p.status) return SHERRY_ERR_CUDA;
@@ -320,7 +358,7 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (st != SHERRY_OK) return st;
-    st = ahead();
+    st = ahead(zero);
     if (st != SHERRY_OK) return st;
     return cuda_status(launch_pdl(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)smem, stream,
                                   dim3((unsigned)std::max(1, plan.cluster)), map, maps, p));
@@ -328,47 +366,58 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
 
 // Weight of an epilogue for plan_tiles, beside a bare linear layer's: the
 // activation's instructions, the residual, fp32 stores, kept sums.
-double epilogue_weight(const tc::EpParams& p, bool gated)
+double epilogue_weight(int dtype, int act, bool res, bool acc, bool gated)
 {
-    const double act = p.act == SHERRY_ACT_NONE                                  ? 0.0
-                       : p.act == SHERRY_ACT_RELU || p.act == SHERRY_ACT_RELU2   ? 0.1
-                       : p.act == SHERRY_ACT_GELU                                ? 0.7
-                                                                                 : 0.55;
-    const double w = 1.0 + act + (p.res ? 0.5 : 0.0) + (p.dtype == SHERRY_F32 ? 0.3 : 0.0) + (p.acc ? 0.4 : 0.0);
+    const double a = act == SHERRY_ACT_NONE                              ? 0.0
+                     : act == SHERRY_ACT_RELU || act == SHERRY_ACT_RELU2 ? 0.1
+                     : act == SHERRY_ACT_GELU                            ? 0.7
+                                                                         : 0.55;
+    const double w = 1.0 + a + (res ? 0.5 : 0.0) + (dtype == SHERRY_F32 ? 0.3 : 0.0) + (acc ? 0.4 : 0.0);
     return gated ? 0.75 * w : w;
 }
 
+TilePlan forward_plan(int dtype, int act, bool res, bool acc, bool gated, int64_t M, int64_t R, int64_t K, int sms)
+{
+    return plan_tiles(M, sherry_row_tiles(R), sherry_k_chunks(K), sms, epilogue_weight(dtype, act, res, acc, gated), false);
+}
+
+// Few tokens: the decode kernel, when it has a plan for the shape.
+bool forward_few(int64_t M, int64_t R, int64_t K, int sms, decode::Plan* pl)
+{
+    return M <= SHERRY_GEMM_DECODE_AUTO_MAX_M &&
+           decode::plan(R, sherry_k_chunks(K), M, sms, pl, decode::ep_rt_first(R, M, sms));
+}
+
 template <int EK, class Ahead>
-int launch_forward_tc(const int8_t* b, const tc::EpParams& p, int sms, cudaStream_t s, const Ahead& ahead)
+int launch_forward_tc(const int8_t* b, const tc::EpParams& p, Split split, int sms, cudaStream_t s, const Ahead& ahead)
 {
     constexpr int W = tc::kWeightSherry;
-    const TilePlan plan = plan_tiles(p.M, sherry_row_tiles(p.N), sherry_k_chunks(p.K), sms,
-                                     epilogue_weight(p, EK == tc::kEpGated), false);
-    if (plan.eg == 2) return plan.bn == 64 ? launch_tc<64, 4, W, EK, 1, 2>(b, p.K, p, plan, s, ahead)
-                                           : launch_tc<128, 2, W, EK, 1, 2>(b, p.K, p, plan, s, ahead);
+    const TilePlan plan = forward_plan(p.dtype, p.act, p.res, p.acc, EK == tc::kEpGated, p.M, p.N, p.K, sms);
+    if (plan.eg == 2) return plan.bn == 64 ? launch_tc<64, 4, W, EK, 1, 2>(b, p.K, p, plan, split, s, ahead)
+                                           : launch_tc<128, 2, W, EK, 1, 2>(b, p.K, p, plan, split, s, ahead);
     switch (plan.bn) {
-    case 16: return launch_tc<16, 4, W, EK, 1>(b, p.K, p, plan, s, ahead);
-    case 32: return launch_tc<32, 4, W, EK, 1>(b, p.K, p, plan, s, ahead);
-    case 64: return launch_tc<64, 4, W, EK, 1>(b, p.K, p, plan, s, ahead);
-    case 128: return launch_tc<128, 2, W, EK, 1>(b, p.K, p, plan, s, ahead);
-    default: return launch_tc<192, 1, W, EK, 1>(b, p.K, p, plan, s, ahead);
+    case 16: return launch_tc<16, 4, W, EK, 1>(b, p.K, p, plan, split, s, ahead);
+    case 32: return launch_tc<32, 4, W, EK, 1>(b, p.K, p, plan, split, s, ahead);
+    case 64: return launch_tc<64, 4, W, EK, 1>(b, p.K, p, plan, split, s, ahead);
+    case 128: return launch_tc<128, 2, W, EK, 1>(b, p.K, p, plan, split, s, ahead);
+    default: return launch_tc<192, 1, W, EK, 1>(b, p.K, p, plan, split, s, ahead);
     }
 }
 
 // kWeightT2 chunks are 4 KB: two-chunk stages from 64 rows on keep at least
 // three stages in the ring.
 template <int D, class Ahead>
-int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, const TilePlan& plan, cudaStream_t s,
+int launch_grad_tc(const int8_t* b, int64_t ld, const tc::EpParams& p, const TilePlan& plan, Split split, cudaStream_t s,
                    const Ahead& ahead)
 {
     constexpr int W = tc::kWeightT2, EK = tc::kEpGrad;
-    if (plan.eg == 2) return launch_tc<192, 1, W, EK, D, 2>(b, ld, p, plan, s, ahead);
+    if (plan.eg == 2) return launch_tc<192, 1, W, EK, D, 2>(b, ld, p, plan, split, s, ahead);
     switch (plan.bn) {
-    case 16: return launch_tc<16, 4, W, EK, D>(b, ld, p, plan, s, ahead);
-    case 32: return launch_tc<32, 4, W, EK, D>(b, ld, p, plan, s, ahead);
-    case 64: return launch_tc<64, 2, W, EK, D>(b, ld, p, plan, s, ahead);
-    case 128: return launch_tc<128, 2, W, EK, D>(b, ld, p, plan, s, ahead);
-    default: return launch_tc<192, 1, W, EK, D>(b, ld, p, plan, s, ahead);
+    case 16: return launch_tc<16, 4, W, EK, D>(b, ld, p, plan, split, s, ahead);
+    case 32: return launch_tc<32, 4, W, EK, D>(b, ld, p, plan, split, s, ahead);
+    case 64: return launch_tc<64, 2, W, EK, D>(b, ld, p, plan, split, s, ahead);
+    case 128: return launch_tc<128, 2, W, EK, D>(b, ld, p, plan, split, s, ahead);
+    default: return launch_tc<192, 1, W, EK, D>(b, ld, p, plan, split, s, ahead);
     }
 }
 
@@ -386,7 +435,7 @@ int launch_decode_rt(const decode::EpParams& p, const decode::Plan& pl, cudaStre
         return e;
     });
     if (st != SHERRY_OK) return st;
-    st = ahead();
+    st = ahead(Zero{nullptr, 0});
     if (st != SHERRY_OK) return st;
     return cuda_status(launch_pdl(kernel, dim3((unsigned)pl.G), dim3((unsigned)pl.threads), (size_t)pl.smem, stream, p));
 }
@@ -411,17 +460,18 @@ int launch_decode(decode::EpParams p, const decode::Plan& pl, const DeviceInfo& 
 
 // Both forward operators: R weight rows, No output columns.
 int forward(const void* x, int dtype, const void* wn, const float* alpha, const float* bias, int act,
-            const void* res, void* out, int32_t* acc, int8_t* x_i8, float* x_scale, int64_t M, int64_t R, int64_t No,
-            int64_t K, bool gated, cudaStream_t s)
+            const void* res, void* out, int32_t* acc, int8_t* x_i8, float* x_scale, Split split, int64_t M, int64_t R,
+            int64_t No, int64_t K, bool gated, cudaStream_t s)
 {
     if (!dtype_ok(dtype) || !act_ok(act)) return SHERRY_ERR_INVALID_ARG;
     if (!x || !wn || !alpha || !out || (x_i8 && !x_scale)) return SHERRY_ERR_INVALID_ARG;
     if (M <= 0 || No <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
     if (!sherry_shape_ok(M, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(x) || !aligned16(wn) || (x_i8 && !aligned16(x_i8))) return SHERRY_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(wn) || (x_i8 && !aligned16(x_i8)) || !aligned16(split.p)) return SHERRY_ERR_INVALID_ARG;
     if (!aligned_elem(out, dtype) || (res && !aligned_elem(res, dtype))) return SHERRY_ERR_INVALID_ARG;
     const int64_t es = ep::elem_size(dtype), rb = 4 * R;
-    const Span outs[] = {{out, M * No * es}, {acc, M * rb}, {x_i8, M * K}, {x_scale, 4 * M}};
+    const Span outs[] = {{out, M * No * es}, {acc, M * rb}, {x_i8, M * K}, {x_scale, 4 * M},
+                         {split.p, (int64_t)split.bytes}};
     const Span ins[] = {{x, M * K * es}, {wn, (int64_t)sherry_native_bytes(R, K)}, {alpha, rb}, {bias, rb},
                         {res == out ? nullptr : res, M * No * es}};
     if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
@@ -430,8 +480,7 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     if (st != SHERRY_OK) return st;
 
     decode::Plan pl;
-    const bool few = M <= SHERRY_GEMM_DECODE_AUTO_MAX_M && decode::plan(R, sherry_k_chunks(K), M, di.sms, &pl,
-                                                                           decode::ep_rt_first(R, M, di.sms));
+    const bool few = forward_few(M, R, K, di.sms, &pl);
     decode::EpParams d = {};
     if (few) {
         d.wnative = static_cast<const uint8_t*>(wn);
@@ -452,7 +501,7 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
         d.x = static_cast<const float*>(x);
         d.xq_out = x_i8;
         d.xs_out = x_scale;
-        const auto none = [] { return (int)SHERRY_OK; };
+        const auto none = [](Zero) { return (int)SHERRY_OK; };
         if (dtype == SHERRY_F32) return launch_decode<1, true, float>(d, pl, di, s, none);
         if (dtype == SHERRY_BF16) return launch_decode<1, true, __nv_bfloat16>(d, pl, di, s, none);
         return launch_decode<1, true, __half>(d, pl, di, s, none);
@@ -465,7 +514,7 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
         if (!x_scale)
             x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + (((size_t)M * (size_t)K + 255) & ~size_t(255)));
     }
-    const auto quantise = [&] { return sherry_quant_act_dt(x, dtype, M, K, x_i8, x_scale, s); };
+    const auto quantise = [&](Zero zero) { return launch_quant(x, dtype, M, K, x_i8, x_scale, zero, di.sms, s); };
     if (few) {
         d.xq = x_i8;
         d.x_scale = x_scale;
@@ -486,8 +535,17 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     p.No = No;
     p.dtype = dtype;
     p.act = act;
-    return gated ? launch_forward_tc<tc::kEpGated>(x_i8, p, di.sms, s, quantise)
-                 : launch_forward_tc<tc::kEpLinear>(x_i8, p, di.sms, s, quantise);
+    return gated ? launch_forward_tc<tc::kEpGated>(x_i8, p, split, di.sms, s, quantise)
+                 : launch_forward_tc<tc::kEpLinear>(x_i8, p, split, di.sms, s, quantise);
+}
+
+size_t forward_split_bytes(int dtype, int act, bool res, bool acc, bool gated, int64_t M, int64_t R, int64_t K)
+{
+    DeviceInfo di;
+    decode::Plan pl;
+    if (!dtype_ok(dtype) || !act_ok(act) || !sherry_shape_ok(M, R, K) || device_info(&di) != SHERRY_OK) return 0;
+    if (forward_few(M, R, K, di.sms, &pl)) return 0;
+    return split_bytes(forward_plan(dtype, act, res, acc, gated, M, R, K, di.sms), M, sherry_row_tiles(R));
 }
 
 // Row stride of the digit rows: whole 128-byte lines, so that a TMA box row is
@@ -506,9 +564,21 @@ int64_t digit_bytes(int dtype, int64_t M, int64_t R)
 
 constexpr int64_t kGradMaxRows = (int64_t(1) << 24) - 1;
 
+bool grad_shape_ok(int64_t M, int64_t R, int64_t K)
+{
+    return sherry_shape_ok(M, R, K) && R <= kGradMaxRows && M <= SHERRY_MAX_DIM / 4;
+}
+
+// Split tiles stay within what sherry_reserve(sherry_grad_digits(dtype) M, ..) sets aside.
+TilePlan grad_plan(int dtype, int64_t M, int64_t R, int64_t K, int sms)
+{
+    return plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), sms, 0.3, true,
+                      tc_token_tile(sherry_grad_digits(dtype) * M));
+}
+
 int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* wt, const float* alpha,
-             const float* bias, int act, void* dx, float* dalpha, float* dbias, void* work, int64_t M, int64_t R,
-             int64_t No, int64_t K, bool gated, cudaStream_t s)
+             const float* bias, int act, void* dx, float* dalpha, float* dbias, void* work, Split split, int64_t M,
+             int64_t R, int64_t No, int64_t K, bool gated, cudaStream_t s)
 {
     if (!dtype_ok(dtype) || !act_ok(act)) return SHERRY_ERR_INVALID_ARG;
     if (!dy || !alpha || (!dx && !dalpha && !dbias)) return SHERRY_ERR_INVALID_ARG;
@@ -516,11 +586,12 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     if (!acc && (gated || act != SHERRY_ACT_NONE || dalpha)) return SHERRY_ERR_INVALID_ARG;
     if (acc && !x_scale) return SHERRY_ERR_INVALID_ARG;
     if (M <= 0 || No <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
-    if (!sherry_shape_ok(M, R, K) || R > kGradMaxRows || M > SHERRY_MAX_DIM / 4) return SHERRY_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned_elem(dy, dtype) || (reinterpret_cast<uintptr_t>(acc) & 7u)) return SHERRY_ERR_INVALID_ARG;
+    if (!grad_shape_ok(M, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(split.p) || !aligned_elem(dy, dtype) || (reinterpret_cast<uintptr_t>(acc) & 7u)) return SHERRY_ERR_INVALID_ARG;
     if (dx && (!aligned16(wt) || !aligned16(work) || !aligned_elem(dx, dtype))) return SHERRY_ERR_INVALID_ARG;
     const int64_t es = ep::elem_size(dtype), rb = 4 * R;
-    const Span outs[] = {{dx, M * K * es}, {dalpha, rb}, {dbias, rb}, {dx ? work : nullptr, digit_bytes(dtype, M, R) + 4 * M}};
+    const Span outs[] = {{dx, M * K * es}, {dalpha, rb}, {dbias, rb}, {dx ? work : nullptr, digit_bytes(dtype, M, R) + 4 * M},
+                         {dx ? split.p : nullptr, (int64_t)split.bytes}};
     const Span ins[] = {{dy, M * No * es}, {acc, M * rb}, {x_scale, 4 * M}, {alpha, rb}, {bias, rb},
                         {dx ? wt : nullptr, (int64_t)sherry_transposed_bytes(R, K)}};
     if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
@@ -544,10 +615,12 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     g.dalpha = dalpha;
     g.dbias = dbias;
     if (!dx) return grad::launch_columns(g, gated, act, dtype, di.sms, s);
-    // split tiles stay within what sherry_reserve(sherry_grad_digits(dtype) M, ..) sets aside
-    const TilePlan plan = plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), di.sms, 0.3, true,
-                                     tc_token_tile(sherry_grad_digits(dtype) * M));
-    const auto digits = [&] { return grad::launch_ahead(g, gated, act, dtype, di.sms, s); };
+    const TilePlan plan = grad_plan(dtype, M, R, K, di.sms);
+    const auto digits = [&](Zero zero) {
+        g.zero = zero.p;
+        g.zero_n = zero.n;
+        return grad::launch_ahead(g, gated, act, dtype, di.sms, s);
+    };
     tc::EpParams p = {};
     p.wnative = static_cast<const uint8_t*>(wt);
     p.x_scale = g.dscale;
@@ -558,9 +631,9 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     p.Mo = M;
     p.No = K;
     p.dtype = dtype;
-    if (dtype == SHERRY_F32) return launch_grad_tc<grad::kDigits<SHERRY_F32>>(g.dig, g.ld, p, plan, s, digits);
+    if (dtype == SHERRY_F32) return launch_grad_tc<grad::kDigits<SHERRY_F32>>(g.dig, g.ld, p, plan, split, s, digits);
     static_assert(grad::kDigits<SHERRY_BF16> == grad::kDigits<SHERRY_F16>, "one kernel for the 16-bit types");
-    return launch_grad_tc<grad::kDigits<SHERRY_F16>>(g.dig, g.ld, p, plan, s, digits);
+    return launch_grad_tc<grad::kDigits<SHERRY_F16>>(g.dig, g.ld, p, plan, split, s, digits);
 }
 
 int repack(bool transposed, const uint8_t* a, const uint8_t* b, int64_t N, int64_t R, int64_t K, void* out, void* stream)
@@ -600,10 +673,7 @@ int sherry_quant_act_dt(const void* x, int x_dtype, int64_t M, int64_t K, int8_t
     DeviceInfo di;
     const int st = device_info(&di);
     if (st != SHERRY_OK) return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (x_dtype == SHERRY_F32) return launch_quant<float>(x, M, K, x_i8, x_scale, di.sms, s);
-    if (x_dtype == SHERRY_BF16) return launch_quant<__nv_bfloat16>(x, M, K, x_i8, x_scale, di.sms, s);
-    return launch_quant<__half>(x, M, K, x_i8, x_scale, di.sms, s);
+    return launch_quant(x, x_dtype, M, K, x_i8, x_scale, Zero{nullptr, 0}, di.sms, static_cast<cudaStream_t>(stream));
 }
 
 int sherry_repack_gated(const uint8_t* gate_dev, const uint8_t* up_dev, int64_t N, int64_t K, void* native_dev,
@@ -627,20 +697,45 @@ int sherry_repack_gated_t(const uint8_t* gate_dev, const uint8_t* up_dev, int64_
     return repack(true, gate_dev, up_dev, N, 2 * N, K, out_dev, stream);
 }
 
+size_t sherry_linear_split_bytes(int x_dtype, int act, int residual, int acc, int64_t M, int64_t N, int64_t K)
+{
+    return forward_split_bytes(x_dtype, act, residual != 0, acc != 0, false, M, N, K);
+}
+
+size_t sherry_gated_split_bytes(int x_dtype, int act, int acc, int64_t M, int64_t N, int64_t K)
+{
+    return N < 1 || N > SHERRY_MAX_DIM / 2 ? 0 : forward_split_bytes(x_dtype, act, false, acc != 0, true, M, 2 * N, K);
+}
+
+int sherry_linear_epilogue_ws(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias,
+                              int act, const void* residual, void* y, int32_t* acc, int8_t* x_i8, float* x_scale,
+                              void* split, size_t split_size, int64_t M, int64_t N, int64_t K, void* stream)
+{
+    return forward(x, x_dtype, Wnative, alpha, bias, act, residual, y, acc, x_i8, x_scale, Split{split, split_size}, M, N,
+                   N, K, false, static_cast<cudaStream_t>(stream));
+}
+
 int sherry_linear_epilogue(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias,
                            int act, const void* residual, void* y, int32_t* acc, int8_t* x_i8, float* x_scale,
                            int64_t M, int64_t N, int64_t K, void* stream)
 {
-    return forward(x, x_dtype, Wnative, alpha, bias, act, residual, y, acc, x_i8, x_scale, M, N, N, K, false,
-                   static_cast<cudaStream_t>(stream));
+    return sherry_linear_epilogue_ws(x, x_dtype, Wnative, alpha, bias, act, residual, y, acc, x_i8, x_scale, nullptr, 0, M,
+                                     N, K, stream);
+}
+
+int sherry_gated_ws(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias, int act,
+                    void* h, int32_t* acc, int8_t* x_i8, float* x_scale, void* split, size_t split_size, int64_t M,
+                    int64_t N, int64_t K, void* stream)
+{
+    if (N > SHERRY_MAX_DIM / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    return forward(x, x_dtype, Wnative, alpha, bias, act, nullptr, h, acc, x_i8, x_scale, Split{split, split_size}, M,
+                   2 * N, N, K, true, static_cast<cudaStream_t>(stream));
 }
 
 int sherry_gated(const void* x, int x_dtype, const void* Wnative, const float* alpha, const float* bias, int act,
                  void* h, int32_t* acc, int8_t* x_i8, float* x_scale, int64_t M, int64_t N, int64_t K, void* stream)
 {
-    if (N > SHERRY_MAX_DIM / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
-    return forward(x, x_dtype, Wnative, alpha, bias, act, nullptr, h, acc, x_i8, x_scale, M, 2 * N, N, K, true,
-                   static_cast<cudaStream_t>(stream));
+    return sherry_gated_ws(x, x_dtype, Wnative, alpha, bias, act, h, acc, x_i8, x_scale, nullptr, 0, M, N, K, stream);
 }
 
 size_t sherry_transposed_bytes(int64_t R, int64_t K)
@@ -657,21 +752,44 @@ size_t sherry_grad_work_bytes(int dtype, int64_t M, int64_t R)
     return (size_t)digit_bytes(dtype, M, R) + 4 * (size_t)M;
 }
 
+size_t sherry_grad_split_bytes(int dtype, int64_t M, int64_t R, int64_t K)
+{
+    DeviceInfo di;
+    if (!dtype_ok(dtype) || !grad_shape_ok(M, R, K) || device_info(&di) != SHERRY_OK) return 0;
+    return split_bytes(grad_plan(dtype, M, R, K, di.sms), digit_rows(dtype, M), sherry_row_tiles(K));
+}
+
+int sherry_linear_grad_ws(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                          const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
+                          void* work, void* split, size_t split_size, int64_t M, int64_t N, int64_t K, void* stream)
+{
+    return backward(dy, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, Split{split, split_size}, M, N,
+                    N, K, false, static_cast<cudaStream_t>(stream));
+}
+
 int sherry_linear_grad(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
                        const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
                        void* work, int64_t M, int64_t N, int64_t K, void* stream)
 {
-    return backward(dy, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, M, N, N, K, false,
-                    static_cast<cudaStream_t>(stream));
+    return sherry_linear_grad_ws(dy, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, nullptr, 0, M, N,
+                                 K, stream);
+}
+
+int sherry_gated_grad_ws(const void* dh, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
+                         const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
+                         void* work, void* split, size_t split_size, int64_t M, int64_t N, int64_t K, void* stream)
+{
+    if (N > kGradMaxRows / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
+    return backward(dh, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, Split{split, split_size}, M,
+                    2 * N, N, K, true, static_cast<cudaStream_t>(stream));
 }
 
 int sherry_gated_grad(const void* dh, int dtype, const int32_t* acc, const float* x_scale, const void* Wt,
                       const float* alpha, const float* bias, int act, void* dx, float* dalpha, float* dbias,
                       void* work, int64_t M, int64_t N, int64_t K, void* stream)
 {
-    if (N > kGradMaxRows / 2) return SHERRY_ERR_UNSUPPORTED_SHAPE;
-    return backward(dh, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, M, 2 * N, N, K, true,
-                    static_cast<cudaStream_t>(stream));
+    return sherry_gated_grad_ws(dh, dtype, acc, x_scale, Wt, alpha, bias, act, dx, dalpha, dbias, work, nullptr, 0, M, N,
+                                K, stream);
 }
 
 }  // extern "C"

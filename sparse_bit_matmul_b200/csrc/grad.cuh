@@ -51,7 +51,16 @@ struct Params {
     int vec;                    // rows and bases allow 16-byte loads of four rows' values
     float* dalpha;              // [R] or null
     float* dbias;               // [R] or null
+    uint4* zero;                // split-K workspace that the digits' launch clears
+    int64_t zero_n;
 };
+
+// Block `block` of `blocks` clears its share of p.zero.
+__device__ __forceinline__ void clear_split(const Params& p, int64_t block, int64_t blocks)
+{
+    for (int64_t i = block * blockDim.x + threadIdx.x; i < p.zero_n; i += blocks * blockDim.x)
+        p.zero[i] = make_uint4(0u, 0u, 0u, 0u);
+}
 
 template <int DT>
 struct Elem {
@@ -366,6 +375,7 @@ __global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params
 {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
+    clear_split(p, (int64_t)blockIdx.y * gridDim.x + blockIdx.x, (int64_t)gridDim.x * gridDim.y);
     digits_block<GATED, ACT, DT>(p, blockIdx.y, blockIdx.x, gridDim.x);
 }
 
@@ -546,6 +556,7 @@ __global__ void __launch_bounds__(kDigitThreads, kBothBlocks)
 {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
+    clear_split(p, blockIdx.x, gridDim.x);
     const uint32_t id = blockIdx.x / cluster, rank = blockIdx.x - id * cluster;
     // what 64 registers hold
     constexpr int kBatch = ACT == SHERRY_ACT_GELU ? 1 : 2;

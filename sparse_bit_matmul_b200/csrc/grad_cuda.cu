@@ -88,6 +88,7 @@ int digits(Params p, int sms, cudaStream_t stream)
         const cudaError_t e = launch_pdl(kernel, dim3((unsigned)cx, (unsigned)n), dim3(kDigitThreads), (size_t)smem, stream,
                                          dim3((unsigned)cx), q);
         if (e != cudaSuccess) return cuda_status(e);
+        q.zero_n = 0;                                        // cleared by the first
     }
     return SHERRY_OK;
 }

@@ -70,7 +70,7 @@ const char* sherry_status_string(int status)
     }
 }
 
-int sherry_version(void) { return 10100; }
+int sherry_version(void) { return 10200; }
 
 size_t sherry_packed_bytes(int64_t N, int64_t K)
 {

@@ -184,8 +184,8 @@ struct Params {
     const float* x_scale;       // [M]
     float* y;                   // [M][N] or null
     int32_t* acc;               // [M][N] or null
-    int32_t* ws;                // split-K slots [grid][BN][128]
-    uint32_t* counters;         // [grid]
+    int32_t* ws;                // split-K slots [grid][BN][128] (kEpPlain), else [split tiles][BN][128]
+    uint32_t* counters;         // one per slot
     unsigned* status;           // device status word
     int64_t M, N, K;
     int64_t TM, TN, Kc;         // token tiles, row tiles, K chunks
@@ -1024,6 +1024,8 @@ __global__ void __launch_bounds__(Cfg<BN, SC, WF, EG>::kThreads, 1)
                 int64_t bf = 0, bl = 0;
                 split_owners(p, tile, G, &bf, &bl);
                 slot = bf;
+                // the feed-forward launches' slots are as many as their split tiles
+                if constexpr (EK != kEpPlain) slot = tile - p.TM * p.TN / G * G;
                 nparts = bl - bf + 1;
             }
             int32_t* wsl = p.ws + slot * (int64_t)BN * SHERRY_TILE_ROWS;

@@ -103,6 +103,13 @@ inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, doubl
     return best;
 }
 
+// Tiles of a launch of T that are summed through the workspace, a slot of BN x
+// 128 sums and a counter each.
+inline int64_t split_tiles(const TilePlan& plan, int64_t T)
+{
+    return plan.whole || plan.cluster ? 0 : T - T / plan.grid * plan.grid;
+}
+
 // With split tiles within the workspace of sherry_reserve(M, ..).
 inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, double w, bool grad)
 {
