@@ -600,7 +600,8 @@ int sherry_selftest_wait(uint64_t limit_ns, void* stream);
  * max_K) sets aside on the current device: the tensor-core kernel's split-K
  * slots (one per SM, the token tile of max_M tokens x 128 rows of int32)
  * and counters, plus max_M x max_K int8 activations and max_M scales for
- * sherry_linear.  0 for non-positive sizes or an unsupported device.
+ * sherry_linear; smaller split-K workspaces set aside before come on top.
+ * 0 for non-positive sizes or an unsupported device.
  */
 size_t sherry_workspace_bytes(int64_t max_M, int64_t max_K);
 
@@ -611,12 +612,13 @@ size_t sherry_workspace_bytes(int64_t max_M, int64_t max_K);
  * W4A8 tensor-core entry points.  Grows what an earlier call reserved (never
  * shrinks it).  When the activation buffer grows, it first waits for the
  * device to be idle and frees the old one; the split-K workspace's older
- * buffers stay (captured graphs may hold their address).  Call it before
- * capturing a stream into a CUDA graph and before timing.  The asynchronous
- * entry points never allocate: without enough workspace they return
- * SHERRY_ERR_WORKSPACE.  Calls whose tensor-core launch splits no tile over
- * several CTAs, the decode kernel (M <= SHERRY_DECODE_MAX_M), the fused
- * sherry_linear launch and sherry_gemm_noalloc need no workspace.
+ * buffers stay, since captured graphs may hold their address (four at most,
+ * 33 MB in all).  Call it before capturing a stream into a CUDA graph and
+ * before timing.  The asynchronous entry points never allocate: without
+ * enough workspace they return SHERRY_ERR_WORKSPACE.  Calls whose tensor-core
+ * launch splits no tile over several CTAs, the decode kernel (M <=
+ * SHERRY_DECODE_MAX_M), the fused sherry_linear launch and
+ * sherry_gemm_noalloc need no workspace.
  */
 int sherry_reserve(int64_t max_M, int64_t max_K);
 
@@ -625,9 +627,9 @@ int sherry_reserve(int64_t max_M, int64_t max_K);
  * current device).  0 when no kernel of this library has reported a bounded
  * wait running out since the last reset; otherwise a nonzero code naming the
  * wait.  reset != 0 clears it; when the word was nonzero the reset also waits
- * for the device to be idle and zero-fills the reserved workspace again,
- * since a launch that gave up may have left partial sums and arrival
- * counters in it.  After a nonzero status, reset it before the next call.
+ * for the device to be idle and zero-fills the reserved workspace again, and
+ * the smaller ones that it grew from, since a launch that gave up may have
+ * left partial sums and arrival counters in them.  After a nonzero status, reset it before the next call.
  */
 int sherry_last_device_status(int reset);
 

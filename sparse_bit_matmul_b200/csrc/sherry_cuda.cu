@@ -17,6 +17,7 @@
 #include "gemv.cuh"
 #include "decode.cuh"
 #include "quant.cuh"
+#include "reserve.h"
 #include "tc_gemm.cuh"
 #include "tile_plan.h"
 #include "w4a8_gemv.cuh"
@@ -231,10 +232,6 @@ namespace {
 std::mutex g_mutex;
 std::vector<DeviceInfo> g_dev;
 
-struct Workspace {
-    void* ptr = nullptr;
-    size_t bytes = 0;
-};
 std::vector<Workspace> g_ws;
 
 }  // namespace
@@ -556,29 +553,15 @@ int get_act_buffer(size_t bytes, void** out)
 
 namespace {
 
-// Grow one per-device buffer to at least `bytes` (host-synchronous; the
-// device is idle before an older, smaller buffer is freed), zero-filled.
-// keep_old: the older buffer stays allocated, since captured graphs may hold
-// its address (the split-K workspace: it grows at most four times, with the
-// token tile, and all its sizes together are 33 MB).
+// grow_reserved in device memory.
 int grow_buffer(Workspace& w, size_t bytes, bool keep_old)
 {
-    if (w.bytes >= bytes) return SHERRY_OK;
-    if (w.ptr && !keep_old) {
-        if (cudaDeviceSynchronize() != cudaSuccess) return SHERRY_ERR_CUDA;
-        cudaFree(w.ptr);
-        w.ptr = nullptr;
-        w.bytes = 0;
-    }
-    void* ptr = nullptr;
-    if (cudaMalloc(&ptr, bytes) != cudaSuccess) return SHERRY_ERR_CUDA;
-    if (cudaMemset(ptr, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
-        cudaFree(ptr);
-        return SHERRY_ERR_CUDA;
-    }
-    w.ptr = ptr;
-    w.bytes = bytes;
-    return SHERRY_OK;
+    return grow_reserved(
+               w, bytes, keep_old, [](void** p, size_t n) { return cudaMalloc(p, n) == cudaSuccess; },
+               [](void* p) { cudaFree(p); }, [](void* p, size_t n) { return cudaMemset(p, 0, n) == cudaSuccess; },
+               [] { return cudaDeviceSynchronize() == cudaSuccess; })
+               ? SHERRY_OK
+               : SHERRY_ERR_CUDA;
 }
 
 int check_gemm_args(const int8_t* x, const float* xs, const void* wn, const float* alpha, const float* y,
@@ -979,14 +962,17 @@ int sherry_last_device_status(int reset)
     if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(v)) != cudaSuccess) return -1;
     if (reset) {
         // A launch whose bounded wait ran out may have left split-K partial
-        // sums and arrival counters behind: the workspace of this device is
-        // zeroed again before the next call can use it.
+        // sums and arrival counters behind: the workspace of this device, and
+        // the smaller ones that captured graphs may use, are zeroed again
+        // before the next call can use them.
         if (v != 0) {
             int dev = 0;
             if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return -1;
             std::lock_guard<std::mutex> lk(g_mutex);
-            if ((int)g_ws.size() > dev && g_ws[dev].ptr &&
-                (cudaMemset(g_ws[dev].ptr, 0, g_ws[dev].bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
+            if ((int)g_ws.size() > dev &&
+                !clear_reserved(
+                    g_ws[dev], [](void* p, size_t n) { return cudaMemset(p, 0, n) == cudaSuccess; },
+                    [] { return cudaDeviceSynchronize() == cudaSuccess; }))
                 return -1;
         }
         unsigned z = 0;
