@@ -427,7 +427,9 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  *   gated    h[m][n] = act(z[m][2n]) * z[m][2n + 1]: row 2n of the weight is
  *            row n of the gate projection, row 2n + 1 row n of the up
  *            projection, and alpha, bias and acc are interleaved the same way
- * in fp32, rounded once to the output's type.  acc, x_i8 and x_scale are
+ * in fp32, rounded once to the output's type.  A token with a NaN or an Inf
+ * has a NaN or Inf scale (its acc and x_i8 are unspecified) and a row of NaN;
+ * no other token's row changes.  acc, x_i8 and x_scale are
  * bit-identical to sherry_linear_ex's for the same fp32 activations.
  * Gradients pass through the quantiser as through the identity (its rounding
  * has slope 0 almost everywhere): with dz the gradient of z,
@@ -459,7 +461,8 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  * captured graphs included.
  * =========================================================================== */
 
-/* sherry_quant_act for x of any element type (x [M][K], 16-byte aligned). */
+/* sherry_quant_act for x of any element type (x [M][K], 16-byte aligned).  A
+ * token with a NaN has x_scale NaN, one with an Inf and no NaN x_scale Inf. */
 int sherry_quant_act_dt(const void* x, int x_dtype, int64_t M, int64_t K, int8_t* x_i8,
                         float* x_scale, void* stream);
 

@@ -502,8 +502,8 @@ __device__ __forceinline__ void cp_async_wait_pending(int n)
 // byte m * QK + c * S), scales into scale_s.  XV float4 slots per thread hold
 // the row in registers (all loads in flight at once); XV = 0 streams it from
 // global memory twice.  Whether the row is in registers is a compile-time
-// property of each instantiation.
-template <int XV, class XT = float>
+// property of each instantiation.  NANS: a NaN in the row makes its scale NaN.
+template <int XV, class XT = float, bool NANS = false>
 __device__ __forceinline__ void fused_activations(const Params& p, int8_t* qbuf, int QK, int S, float* scale_s,
                                                   float* warp_max, int M, int K4)
 {
@@ -527,20 +527,20 @@ __device__ __forceinline__ void fused_activations(const Params& p, int8_t* qbuf,
                 if (u < nsl) v[u] = load_x4<XT>(xr, tid + u * nthr);
 #pragma unroll
             for (int u = 0; u < XV; ++u)
-                if (u < nsl) mx = fmaxf(mx, quant::absmax4(v[u]));
+                if (u < nsl) mx = quant::larger<NANS>(mx, quant::absmax4<NANS>(v[u]));
         } else {
 #pragma unroll 4
-            for (int i = tid; i < K4; i += nthr) mx = fmaxf(mx, quant::absmax4(load_x4<XT>(xr, i)));
+            for (int i = tid; i < K4; i += nthr) mx = quant::larger<NANS>(mx, quant::absmax4<NANS>(load_x4<XT>(xr, i)));
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int o = 16; o > 0; o >>= 1) mx = quant::larger<NANS>(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (lane == 0) warp_max[(m & 1) * 16 + warp] = mx;
         __syncthreads();
         // every warp combines the (at most 16) warp maxima: one load per
         // lane and a shuffle tree, not a chain of dependent loads
         float a = lane < nwarps ? warp_max[(m & 1) * 16 + lane] : 0.0f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        for (int o = 16; o > 0; o >>= 1) a = quant::larger<NANS>(a, __shfl_xor_sync(0xffffffffu, a, o));
         const quant::Scale sc = quant::make_scale(a);
         if (tid == 0) {
             scale_s[m] = sc.s;
@@ -640,8 +640,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
         // rows of up to kXV float4s per thread are held in registers; longer
         // rows stream from global memory (XV = 0)
         float* warp_max = reinterpret_cast<float*>(smem + kOffWarpMax);
-        if (K4 <= kXV * nthr) fused_activations<kXV, XT>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
-        else fused_activations<0, XT>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
+        if (K4 <= kXV * nthr) fused_activations<kXV, XT, EP>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
+        else fused_activations<0, XT, EP>(p, qbuf, QK, S, scale_s, warp_max, M, K4);
     } else {
         // plain 16-byte loads, so that the copy groups in flight are the code steps only
         const int K16 = (int)(p.K >> 4);

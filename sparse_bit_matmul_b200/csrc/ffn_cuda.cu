@@ -51,8 +51,8 @@ struct Zero {
     int64_t n;
 };
 
-// The largest magnitude of 16-byte pieces of a row (NaN: ignored), two values
-// at a time where they are 16-bit.
+// The largest magnitude of 16-byte pieces of a row (NaN if there is one), two
+// values at a time where they are 16-bit.
 template <class XT>
 struct AbsMax {
     using Pair = std::conditional_t<std::is_same_v<XT, __half>, __half2, __nv_bfloat162>;
@@ -70,19 +70,19 @@ struct AbsMax {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (kWide) {
-                a = fmaxf(a, fabsf(__uint_as_float(u[i])));
+                a = quant::larger<true>(a, fabsf(__uint_as_float(u[i])));
             } else {
                 Pair p;
                 memcpy(&p, &u[i], 4);
-                a = __hmax2(a, __habs2(p));
+                a = __hmax2_nan(a, __habs2(p));
             }
         }
     }
     __device__ __forceinline__ float get() const
     {
         if constexpr (kWide) return a;
-        else if constexpr (std::is_same_v<XT, __half>) return fmaxf(__low2float(a), __high2float(a));
-        else return fmaxf(__bfloat162float(a.x), __bfloat162float(a.y));
+        else if constexpr (std::is_same_v<XT, __half>) return quant::larger<true>(__low2float(a), __high2float(a));
+        else return quant::larger<true>(__bfloat162float(a.x), __bfloat162float(a.y));
     }
 };
 
@@ -129,13 +129,13 @@ __global__ void __launch_bounds__(kQuantThreads, XV == kQuantLoads ? 3 : 2)
     }
     float a = mx.get();
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (int o = 16; o > 0; o >>= 1) a = quant::larger<true>(a, __shfl_xor_sync(0xffffffffu, a, o));
     __shared__ float warp_max[kQuantThreads / 32];
     if (lane == 0) warp_max[warp] = a;
     __syncthreads();
     a = lane < nthr / 32 ? warp_max[lane] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (int o = 16; o > 0; o >>= 1) a = quant::larger<true>(a, __shfl_xor_sync(0xffffffffu, a, o));
 
     const quant::Scale sc = quant::make_scale(a);
     if (tid == 0) scale[m] = sc.s;

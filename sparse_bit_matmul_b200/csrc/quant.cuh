@@ -4,7 +4,9 @@
 // Rule (the Sherry page, pnsm.cn/news/1195499, sec. 2.2 step 1 leaves it
 // open; this is symmetric absmax/127): s = a / 127 with a = max |x| (IEEE
 // fp32 division), q = clamp(rint(fl(x / s)), -127, 127), round half to even;
-// a == 0 gives s = 0 and q = 0.
+// a == 0 gives s = 0 and q = 0.  A token with an Inf has s = Inf and q = 0, and
+// so acc * alpha * s = NaN; one with a NaN has s = NaN where the maximum keeps
+// it (the feed-forward entry points), else its NaN counts as 0.
 //
 // q is computed without a division for almost every element: r is the
 // hardware reciprocal approximation of s (rcp.approx, at most 1 ulp off:
@@ -93,9 +95,20 @@ __device__ __forceinline__ uint32_t quantise4(const float4& v, const Scale& sc)
     return near ? quantise4_exact(v, sc.s) : packed;
 }
 
+// The larger of two values; NANS: NaN if either is (else NaN is passed over).
+template <bool NANS>
+__device__ __forceinline__ float larger(float a, float b)
+{
+    if constexpr (!NANS) return fmaxf(a, b);
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+template <bool NANS = false>
 __device__ __forceinline__ float absmax4(const float4& v)
 {
-    return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+    return larger<NANS>(larger<NANS>(fabsf(v.x), fabsf(v.y)), larger<NANS>(fabsf(v.z), fabsf(v.w)));
 }
 
 }  // namespace quant
