@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "epilogue.cuh"
+#include "grad_plan.h"
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "sherry_internal.h"
@@ -252,7 +253,6 @@ struct Segment {
 // compared as integers (one mask and one maximum a value; Inf and NaN order
 // above every number), and three digits come out of the low bits of
 // e * inv + 1.5 * 2^23 without a conversion instruction.
-constexpr int kDigitThreads = 256;
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 template <bool GATED, int ACT, int DT, bool VEC>
@@ -382,12 +382,6 @@ __global__ void __launch_bounds__(kDigitThreads) grad_digits_kernel(const Params
 // Column sums: a block owns the rows of 32 lanes x 4 weight rows, its warps
 // (and the blocks of its cluster, which share the columns) take the tokens in
 // turn, and the partial sums meet in a fixed order.
-constexpr int kColWarps = 4;
-constexpr int kColBlocks = 6;                                // resident per SM (registers)
-// Many tokens and so few rows that clusters of eight blocks leave SMs idle:
-// blocks of 16 warps.
-constexpr int kColWarpsWide = 16;
-constexpr int kColRows = 128;                                // weight rows per block
 
 // One lane's sums over the tokens m0, m0 + step, ..: the loads of B tokens are
 // issued before their arithmetic, without a branch between them; advances m
@@ -547,9 +541,6 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 
 // the digits of other tokens hide a token's two passes; the column sums load
 // fewer tokens at once for it (M=300 K=2080, gated to 5001, f16: 48.1 -> 44.0 us;
 // M=380 K=1056 N=10001 f32 gelu 64 -> 56).
-constexpr int64_t kBothMaxTokens = 1024;
-constexpr int kBothBlocks = 4;
-
 template <bool GATED, int ACT, int DT>
 __global__ void __launch_bounds__(kDigitThreads, kBothBlocks)
     grad_both_kernel(const Params p, uint32_t ahead, uint32_t cluster, int whole)

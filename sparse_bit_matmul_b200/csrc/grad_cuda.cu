@@ -13,49 +13,12 @@ namespace grad {
 namespace {
 
 constexpr int kCacheMax = 200 * 1024;       // bytes of e a block may hold
-constexpr int kSegMin = 1024;               // weight rows worth a block of their own
-constexpr int kSegMax = 8192;               // above, a block's 32 KB keep its neighbours off the SM
-constexpr int kClusterMax = 8;
-
-// Blocks that share the columns: of the cluster sizes that leave every warp
-// four tokens, the one whose last round of resident blocks is fullest; the
-// smallest such.
-int columns_cluster(int64_t R, int64_t M, int sms)
+// The segments of cx blocks per token; returns the block's shared memory for e.
+int64_t split_rows(Params& p, int cx)
 {
-    const int64_t bx = (R + kColRows - 1) / kColRows, slots = (int64_t)kColBlocks * sms;
-    int cy = 1;
-    double best = 0.0;
-    for (int y = 1; y <= kClusterMax && (y == 1 || M >= (int64_t)y * kColWarps * 4); ++y) {
-        const int64_t blocks = bx * y, rounds = (blocks + slots - 1) / slots;
-        const double full = (double)blocks / (double)(rounds * slots);
-        if (full > best + 0.02) {
-            best = full;
-            cy = y;
-        }
-    }
-    return cy;
-}
-
-int64_t row_blocks(int64_t R) { return (R + kColRows - 1) / kColRows; }
-
-bool columns_wide(int64_t R, int64_t M, int sms)
-{
-    return M >= 4 * kColWarpsWide * 2 && row_blocks(R) * kClusterMax < sms;
-}
-
-// Blocks per token: so many that a block holds at most kSegMax rows, and more
-// while the grid leaves SMs without `per` blocks.  Fills in p's segments;
-// returns the block's shared memory for e.
-int64_t split_rows(Params& p, int sms, int per, int* blocks)
-{
-    int cx = 1;
-    while (cx < kClusterMax &&
-           (p.R > (int64_t)cx * kSegMax || (p.M * cx < per * (int64_t)sms && p.R >= (int64_t)cx * 2 * kSegMin)))
-        cx *= 2;
     p.seg = (int)(((p.R + cx - 1) / cx + 15) & ~int64_t(15));
     const int64_t need = 4 * std::min<int64_t>(p.seg, (p.R + 3) & ~int64_t(3));
     p.cached = need <= kCacheMax;
-    *blocks = cx;
     return p.cached ? need : 0;
 }
 
@@ -74,8 +37,8 @@ int digits(Params p, int sms, cudaStream_t stream)
     static std::atomic<uint64_t> done{0};
     const int st = allow_cache(kernel, done);
     if (st != SHERRY_OK) return st;
-    int cx = 1;
-    const int64_t smem = split_rows(p, sms, 4, &cx);
+    const int cx = token_blocks(p.M, p.R, sms, 4);
+    const int64_t smem = split_rows(p, cx);
     // tokens in grid.y: at most 65535 a launch (whole groups of 16 digit rows)
     Params q = p;
     for (int64_t m0 = 0; m0 < p.M; m0 += 65535) {
@@ -101,15 +64,9 @@ int both(Params p, bool dx, int sms, cudaStream_t stream)
     static std::atomic<uint64_t> done{0};
     const int st = allow_cache(kernel, done);
     if (st != SHERRY_OK) return st;
-    int c = 1;
-    const int64_t smem = split_rows(p, sms, 2, &c), rb = row_blocks(p.R);
-    const bool whole = c == 1;
-    // short rows: clusters for the column sums alone, four tokens a warp, while
-    // they leave half the blocks of a round to the digits (M=300 K=512 N=203:
-    // 15.7 -> 9.7 us)
-    if (whole)
-        while (c < kClusterMax && p.M >= 2 * c * (kDigitThreads / 32) * 4 && 2 * c * rb <= kBothBlocks / 2 * (int64_t)sms)
-            c *= 2;
+    bool whole = false;
+    const int c = both_cluster(p.M, p.R, sms, &whole);
+    const int64_t smem = split_rows(p, whole ? 1 : c), rb = row_blocks(p.R);
     const int64_t ahead = !dx ? 0 : whole ? (p.M + c - 1) / c : p.M;
     return cuda_status(launch_pdl(kernel, dim3((unsigned)(c * (ahead + rb))), dim3(kDigitThreads), (size_t)smem, stream,
                                   dim3((unsigned)c), p, (uint32_t)ahead, (uint32_t)c, (int)whole));
@@ -119,13 +76,11 @@ template <bool GATED, int ACT, int DT>
 int columns(const Params& p, int sms, cudaStream_t stream)
 {
     if (p.M <= kBothMaxTokens) return both<GATED, ACT, DT>(p, false, sms, stream);
-    const unsigned bx = (unsigned)row_blocks(p.R);
-    if (columns_wide(p.R, p.M, sms)) {
-        const unsigned cy = (unsigned)std::min<int64_t>(kClusterMax, p.M / (4 * kColWarpsWide));
+    const Columns shape = columns_shape(p.R, sms);
+    const unsigned bx = (unsigned)row_blocks(p.R), cy = (unsigned)shape.cluster;
+    if (shape.warps == kColWarpsWide)
         return cuda_status(launch_pdl(grad_columns_kernel<GATED, ACT, DT, kColWarpsWide>, dim3(bx, cy),
                                       dim3(32 * kColWarpsWide), 0, stream, dim3(1, cy), p));
-    }
-    const unsigned cy = (unsigned)columns_cluster(p.R, p.M, sms);
     return cuda_status(launch_pdl(grad_columns_kernel<GATED, ACT, DT, kColWarps>, dim3(bx, cy), dim3(32 * kColWarps), 0,
                                   stream, dim3(1, cy), p));
 }
