@@ -448,7 +448,9 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  * Inf or NaN gives a dx row of NaN.  Results do not depend on the launch
  * shape or on the order of any sum across blocks: the same call gives the
  * same bits.
- * Tensors are dense row-major.  Errors are those of sherry_linear.  An output
+ * Tensors are dense row-major and start at a multiple of their element size
+ * (x, x_i8, the weights and the buffers of bytes: of 16; the acc of a gradient:
+ * of 8), or the call is refused.  Errors are those of sherry_linear.  An output
  * that overlaps an input or another output is refused, but for y == residual.
  * Split-K workspace: a call with many chunks and few tiles sums tiles across
  * CTAs.  The _ws forms take the memory for that from the caller (`split`, at

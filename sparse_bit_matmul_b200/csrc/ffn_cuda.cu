@@ -242,6 +242,13 @@ bool aligned_elem(const void* p, int dtype)
     return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(ep::elem_size(dtype) - 1)) == 0;
 }
 
+// fp32 and int32 arrays (null counts as aligned)
+template <class... P>
+bool aligned4(const P*... p)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
+
 struct Span {
     const void* p;              // or null: empty
     int64_t bytes;
@@ -469,6 +476,7 @@ int forward(const void* x, int dtype, const void* wn, const float* alpha, const 
     if (!sherry_shape_ok(M, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x) || !aligned16(wn) || (x_i8 && !aligned16(x_i8)) || !aligned16(split.p)) return SHERRY_ERR_INVALID_ARG;
     if (!aligned_elem(out, dtype) || (res && !aligned_elem(res, dtype))) return SHERRY_ERR_INVALID_ARG;
+    if (!aligned4(alpha, bias, acc, x_scale)) return SHERRY_ERR_INVALID_ARG;
     const int64_t es = ep::elem_size(dtype), rb = 4 * R;
     const Span outs[] = {{out, M * No * es}, {acc, M * rb}, {x_i8, M * K}, {x_scale, 4 * M},
                          {split.p, (int64_t)split.bytes}};
@@ -588,6 +596,7 @@ int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale
     if (M <= 0 || No <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
     if (!grad_shape_ok(M, R, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(split.p) || !aligned_elem(dy, dtype) || (reinterpret_cast<uintptr_t>(acc) & 7u)) return SHERRY_ERR_INVALID_ARG;
+    if (!aligned4(x_scale, alpha, bias, dalpha, dbias)) return SHERRY_ERR_INVALID_ARG;
     if (dx && (!aligned16(wt) || !aligned16(work) || !aligned_elem(dx, dtype))) return SHERRY_ERR_INVALID_ARG;
     const int64_t es = ep::elem_size(dtype), rb = 4 * R;
     const Span outs[] = {{dx, M * K * es}, {dalpha, rb}, {dbias, rb}, {dx ? work : nullptr, digit_bytes(dtype, M, R) + 4 * M},
@@ -667,7 +676,7 @@ int sherry_quant_act_dt(const void* x, int x_dtype, int64_t M, int64_t K, int8_t
     if (!x || !x_i8 || !x_scale) return SHERRY_ERR_INVALID_ARG;
     if (M <= 0 || K <= 0) return SHERRY_ERR_INVALID_ARG;
     if (!sherry_shape_ok(M, 1, K)) return SHERRY_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(x) || !aligned16(x_i8)) return SHERRY_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(x_i8) || !aligned4(x_scale)) return SHERRY_ERR_INVALID_ARG;
     const Span outs[] = {{x_i8, M * K}, {x_scale, 4 * M}}, ins[] = {{x, M * K * ep::elem_size(x_dtype)}};
     if (overlaps(outs, ins)) return SHERRY_ERR_INVALID_ARG;
     DeviceInfo di;

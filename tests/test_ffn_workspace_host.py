@@ -1,4 +1,4 @@
-"""The caller's split-K workspace of the feed-forward calls: what is refused before anything is launched."""
+"""Buffers of the feed-forward calls: what is refused before anything is launched."""
 import ctypes
 
 import sparse_bit_matmul_b200 as sbm
@@ -34,3 +34,23 @@ def test_size_queries_of_bad_arguments(lib):
     assert L.sherry_gated_split_bytes(0, 0, 0, 8, 1 << 62, 32) == 0
     for bad in ((3, 8, 8, 32), (0, 0, 8, 32), (0, 8, 1 << 24, 32), (0, 8, 8, 33), (0, 1 << 30, 8, 32)):
         assert L.sherry_grad_split_bytes(*bad) == 0
+
+
+def test_arrays_off_their_elements_are_refused(lib):
+    """fp32 and int32 arguments at addresses that are no multiple of 4."""
+    L = sbm.load()
+    far = 1 << 24
+    for off in (1, 2, 3):
+        for i in (3, 4, 8, 10):                       # alpha, bias, acc, x_scale
+            a = [at(0), 1, at(far), at(2 * far), at(3 * far), 0, None, at(4 * far), at(5 * far), at(6 * far), at(7 * far)]
+            a[i] = at((20 + i) * far + off)
+            assert L.sherry_linear_epilogue(*a, 2, 4, 32, None) == INVALID, (i, off)
+            del a[6]
+            assert L.sherry_gated(*a, 2, 4, 32, None) == INVALID, (i, off)
+        for i in (3, 5, 6, 9, 10):                    # x_scale, alpha, bias, dalpha, dbias
+            a = [at(0), 1, at(far), at(2 * far), at(3 * far), at(4 * far), at(5 * far), 3, at(6 * far), at(7 * far),
+                 at(8 * far), at(9 * far)]
+            a[i] = at((20 + i) * far + off)
+            assert L.sherry_linear_grad(*a, 2, 4, 32, None) == INVALID, (i, off)
+            assert L.sherry_gated_grad(*a, 2, 4, 32, None) == INVALID, (i, off)
+        assert L.sherry_quant_act_dt(at(0), 1, 2, 32, at(far), at(2 * far + off), None) == INVALID
