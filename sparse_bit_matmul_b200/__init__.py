@@ -303,7 +303,7 @@ def selftest_wait(limit_ns: int, stream=None):
 
 # --------------------------------------------------- feed-forward operators
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}   # sherry_act
-_torch = None
+_torch = _is_grad_enabled = None
 _DTYPES = {}            # torch dtype -> sherry_dtype, filled on first use
 _split_reserved = set()  # devices whose split-K workspace covers every call
 SPLIT_MAX_M = 1536      # from this many tokens on the split-K workspace no longer grows
@@ -311,10 +311,11 @@ SPLIT_MAX_M = 1536      # from this many tokens on the split-K workspace no long
 
 def _types():
     """Imports torch on first use: sherry_dtype by torch dtype."""
-    global _torch
+    global _torch, _is_grad_enabled
     if _torch is None:
         import torch
         load()
+        _is_grad_enabled = torch.is_grad_enabled
         _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
         _torch = torch
     return _DTYPES
@@ -345,6 +346,14 @@ def _matrix(t, name: str):
     if code is None or len(shape) != 2 or idx < 0 or not t.is_contiguous():
         _refuse(name, t, "[M][.] of float32, bfloat16 or float16")
     return shape[0], shape[1], code, idx
+
+
+def _no_history(what: str, *tensors):
+    """Refuses tensors that autograd would follow through a call: its results carry no history."""
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{what} is not recorded by autograd and an argument requires a gradient: call it under "
+                             "torch.no_grad(), or in a torch.autograd.Function with the *_backward call as its backward")
 
 
 def _activation(act) -> int:
@@ -441,6 +450,8 @@ def repack_gated_t(gate_dev, up_dev, N: int, K: int, out=None):
 
 def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s):
     M, K, dt, idx = _matrix(x, "x")
+    if _is_grad_enabled():
+        _no_history("gated" if gated else "linear_epilogue", x, alpha, bias, residual, out)
     if idx != _torch._C._cuda_getDevice():
         with _torch.cuda.device(idx):
             return _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s)
@@ -498,7 +509,7 @@ def linear_epilogue(x, w_native, alpha, N: int, bias=None, act: str = "none", re
     x, residual and y are float32, bfloat16 or float16 (one type per call); bias fp32 [N]; act a key of
     ACTIVATIONS.  out may be residual itself.  acc int32 [M][N], out_q int8 [M][K] and out_s fp32 [M]
     receive the exact sums, the quantised activations and their scales (linear_backward needs acc and
-    out_s)."""
+    out_s).  Not recorded by autograd: with gradients enabled, arguments that require one are refused."""
     return _forward(False, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s)
 
 
@@ -506,12 +517,14 @@ def gated(x, w_native, alpha, N: int, bias=None, act: str = "silu", out=None, ac
     """h [M][N] = act(gate(x)) * up(x) in one contraction (sherry_gated).
 
     w_native from repack_gated; alpha, bias fp32 [2N] and acc int32 [M][2N] interleave gate and up
-    (entries 2n, 2n + 1).  Other arguments as linear_epilogue."""
+    (entries 2n, 2n + 1).  Other arguments, and autograd, as linear_epilogue."""
     return _forward(True, x, w_native, alpha, N, bias, act, None, out, acc, out_q, out_s)
 
 
 def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales):
     M, N, dt, idx = _matrix(dy, "dy")
+    if _is_grad_enabled():
+        _no_history("gated_backward" if gated else "linear_backward", dy, alpha, bias, out)
     if idx != _torch._C._cuda_getDevice():
         with _torch.cuda.device(idx):
             return _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales)
