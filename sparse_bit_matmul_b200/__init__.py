@@ -348,12 +348,9 @@ def _matrix(t, name: str):
     return shape[0], shape[1], code, idx
 
 
-def _no_history(what: str, *tensors):
-    """Refuses tensors that autograd would follow through a call: its results carry no history."""
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            raise ValueError(f"{what} is not recorded by autograd and an argument requires a gradient: call it under "
-                             "torch.no_grad(), or in a torch.autograd.Function with the *_backward call as its backward")
+def _no_history(what: str):
+    raise ValueError(f"{what} is not recorded by autograd and an argument requires a gradient: call it under "
+                     "torch.no_grad(), or in a torch.autograd.Function with the *_backward call as its backward")
 
 
 def _activation(act) -> int:
@@ -450,8 +447,10 @@ def repack_gated_t(gate_dev, up_dev, N: int, K: int, out=None):
 
 def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s):
     M, K, dt, idx = _matrix(x, "x")
-    if _is_grad_enabled():
-        _no_history("gated" if gated else "linear_epilogue", x, alpha, bias, residual, out)
+    if _is_grad_enabled() and (
+            x.requires_grad or alpha is not None and alpha.requires_grad or bias is not None and bias.requires_grad or
+            residual is not None and residual.requires_grad or out is not None and out.requires_grad):
+        _no_history("gated" if gated else "linear_epilogue")
     if idx != _torch._C._cuda_getDevice():
         with _torch.cuda.device(idx):
             return _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q, out_s)
@@ -481,14 +480,16 @@ def _forward(gated, x, w_native, alpha, N, bias, act, residual, out, acc, out_q,
     kp, split = None, 0
     if M > 1 or K > 65536:
         split = _forward_split_bytes(idx, gated, dt, a, rp is not None, cp is not None, M, N, K)
-        at = (M * K + 4 * M + 15) & ~15                 # K % 32 == 0: the scales are aligned
-        own = w_native.new_empty(at + split)
-        if qp is None:
-            qp = own.data_ptr()
-        if sp is None:
-            sp = own.data_ptr() + M * K
-        if split:
-            kp = own.data_ptr() + at
+        # K % 32 == 0: the scales are aligned
+        at = (M * K + 4 * M + 15) & ~15 if qp is None or sp is None else 0
+        if at or split:
+            own = w_native.new_empty(at + split)
+            kp = own.data_ptr()
+            if qp is None:
+                qp = kp
+            if sp is None:
+                sp = kp + M * K
+            kp = kp + at if split else None
     elif qp is not None and sp is None:
         own = w_native.new_empty(4)
         sp = own.data_ptr()
@@ -523,8 +524,10 @@ def gated(x, w_native, alpha, N: int, bias=None, act: str = "silu", out=None, ac
 
 def _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales):
     M, N, dt, idx = _matrix(dy, "dy")
-    if _is_grad_enabled():
-        _no_history("gated_backward" if gated else "linear_backward", dy, alpha, bias, out)
+    if _is_grad_enabled() and (
+            dy.requires_grad or alpha is not None and alpha.requires_grad or bias is not None and bias.requires_grad or
+            out is not None and out.requires_grad):
+        _no_history("gated_backward" if gated else "linear_backward")
     if idx != _torch._C._cuda_getDevice():
         with _torch.cuda.device(idx):
             return _backward(gated, dy, w_t, alpha, K, acc, x_scale, bias, act, out, want_dx, want_scales)
