@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
             const float s = scale_s[m];
             float z0 = __fmul_rn(__fmul_rn((float)a0, alpha_sm[i0]), s);
             if (p.bias) z0 = __fadd_rn(z0, first_out ? pre_b0 : p.bias[n]);
-            float y = ep::act_one(z0, p.act);
+            float y = ep::act_one(z0, p.act, p.dtype);
             if (p.gated) {
                 float z1 = __fmul_rn(__fmul_rn((float)a1, alpha_sm[i0 + 1]), s);
                 if (p.bias) z1 = __fadd_rn(z1, first_out ? pre_b1 : p.bias[n + 1]);

@@ -8,12 +8,13 @@
 //   t(z) = 2 sqrt(2/pi) (z + 0.044715 z^3), S the logistic function
 //   (z/2 (1 + tanh(t/2)) = z S(t)).
 // silu and gelu_tanh share one body.
-// S(t) = 1 / (1 + e^-t) with the hardware's approximate power of two and
-// reciprocal (two special-function instructions a value: the epilogue has one
-// warp per scheduler).  e^-t overflows to infinity for t < -88, where S is 0
-// to fp32 either way; its relative error (2 ulp and the rounding of t log2 e)
-// reaches the result scaled by 1 - S(t), so the larger half of the values
-// hardly sees it.
+// S(t) = 1 / (1 + e^-t) with the hardware's approximate reciprocal (1 ulp).
+// e^-t overflows to infinity for t < -88, where S is 0 to fp32 either way.  For
+// 16-bit tensors it is the hardware's approximate power of two of -t log2 e (two
+// special-function instructions a value: the epilogue has one warp per
+// scheduler), whose relative error, 2 ulp and |t| half steps of the rounded
+// argument, is far below the output's rounding; for fp32 tensors it is expf (2
+// ulp at any t).
 #pragma once
 
 #include <cstdint>
@@ -71,10 +72,12 @@ constexpr float kGeluC3 = 0.0713548162726009f;       // 2 sqrt(2 / pi) 0.044715
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
+template <bool FULL>
 __device__ __forceinline__ float logistic(float t)
 {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(t, -1.4426950408889634f)));
+    if constexpr (FULL) e = expf(-t);
+    else asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(t, -1.4426950408889634f)));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
     return r;
 }
@@ -88,15 +91,21 @@ __device__ __forceinline__ float sigmoid_arg(float z, bool silu)
 // max(z, 0); NaN stays NaN
 __device__ __forceinline__ float relu(float z) { return z < 0.0f ? 0.0f : z; }
 
-// act over an array held in registers: one switch for the whole array
+// act over an array held in registers: one switch for the whole array.  dtype:
+// that of the tensors.
 template <int N>
-__device__ __forceinline__ void apply_act(float (&v)[N], int act)
+__device__ __forceinline__ void apply_act(float (&v)[N], int act, int dtype)
 {
     if (act == SHERRY_ACT_NONE) return;
     if (act == SHERRY_ACT_SILU || act == SHERRY_ACT_GELU_TANH) {
         const bool silu = act == SHERRY_ACT_SILU;
+        if (dtype == SHERRY_F32) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __fmul_rn(v[i], logistic(sigmoid_arg(v[i], silu)));
+            for (int i = 0; i < N; ++i) v[i] = __fmul_rn(v[i], logistic<true>(sigmoid_arg(v[i], silu)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __fmul_rn(v[i], logistic<false>(sigmoid_arg(v[i], silu)));
+        }
     } else if (act == SHERRY_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -110,14 +119,15 @@ __device__ __forceinline__ void apply_act(float (&v)[N], int act)
     }
 }
 
-__device__ __forceinline__ float act_one(float z, int act)
+__device__ __forceinline__ float act_one(float z, int act, int dtype)
 {
     float v[1] = {z};
-    apply_act<1>(v, act);
+    apply_act<1>(v, act, dtype);
     return v[0];
 }
 
-// act(z) and its derivative (0 at the corner of relu)
+// act(z) and its derivative (0 at the corner of relu).  FULL: for fp32 tensors.
+template <bool FULL>
 __device__ __forceinline__ void act_slope(float z, int act, float& f, float& d)
 {
     if (act == SHERRY_ACT_NONE) {
@@ -125,13 +135,13 @@ __device__ __forceinline__ void act_slope(float z, int act, float& f, float& d)
         d = 1.0f;
     } else if (act == SHERRY_ACT_SILU) {
         // d/dz [z S(z)] = S + z S (1 - S)
-        const float s = logistic(z);
+        const float s = logistic<FULL>(z);
         f = __fmul_rn(z, s);
         d = __fmaf_rn(f, __fsub_rn(1.0f, s), s);
     } else if (act == SHERRY_ACT_GELU_TANH) {
         // d/dz [z S(t)] = S + z S (1 - S) t',  t' = c1 + 3 c3 z^2; a far z:
         // z^2 may overflow where S (1 - S) is 0
-        const float s = logistic(sigmoid_arg(z, false));
+        const float s = logistic<FULL>(sigmoid_arg(z, false));
         const float t1 = __fmaf_rn(__fmul_rn(z, z), 3.0f * kGeluC3, kGeluC1);
         f = __fmul_rn(z, s);
         const float w = __fmul_rn(f, __fsub_rn(1.0f, s));

@@ -187,7 +187,7 @@ __device__ __forceinline__ Rows4 load_rows(const float* alpha, const float* bias
 
 // dz of a unit of one token, from its sums a and the
 // token's dy (two columns when gated)
-template <bool GATED, int ACT, int C>
+template <bool GATED, int ACT, int DT, int C>
 __device__ __forceinline__ void dz4(const int32_t (&a)[4], const float (&g)[C], const Rows4& w, bool hb, float s,
                                     float (&dz)[4])
 {
@@ -195,7 +195,7 @@ __device__ __forceinline__ void dz4(const int32_t (&a)[4], const float (&g)[C], 
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             float f, d;
-            ep::act_slope(pre_act(a[2 * k], w.al[2 * k], s, hb, w.b[2 * k]), ACT, f, d);
+            ep::act_slope<DT == SHERRY_F32>(pre_act(a[2 * k], w.al[2 * k], s, hb, w.b[2 * k]), ACT, f, d);
             const float up = pre_act(a[2 * k + 1], w.al[2 * k + 1], s, hb, w.b[2 * k + 1]);
             dz[2 * k] = __fmul_rn(__fmul_rn(g[k], up), d);
             dz[2 * k + 1] = __fmul_rn(g[k], f);
@@ -204,7 +204,7 @@ __device__ __forceinline__ void dz4(const int32_t (&a)[4], const float (&g)[C], 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float f, d;
-            ep::act_slope(pre_act(a[k], w.al[k], s, hb, w.b[k]), ACT, f, d);
+            ep::act_slope<DT == SHERRY_F32>(pre_act(a[k], w.al[k], s, hb, w.b[k]), ACT, f, d);
             dz[k] = __fmul_rn(g[k], d);
         }
     }
@@ -240,7 +240,7 @@ struct Segment {
         load_dy<DT, C>(dy + at, cols - at, VEC, step, g);
         if (acc) load_acc<GATED>(acc + r, rows - r, VEC, step, a);
         const Rows4 w = load_rows<GATED, VEC>(alpha + r, bias ? bias + r : nullptr, rows - r, step);
-        dz4<GATED, ACT, C>(a, g, w, bias != nullptr, s, dz);
+        dz4<GATED, ACT, DT, C>(a, g, w, bias != nullptr, s, dz);
 #pragma unroll
         for (int k = 0; k < 4; ++k) e[k] = __fmul_rn(dz[k], w.al[k]);
     }
@@ -422,7 +422,7 @@ struct Column {
 #pragma unroll
             for (int i = 0; i < B; ++i) {
                 float dz[4];
-                dz4<GATED, ACT, C>(a[i], g[i], w, hb, sc[i], dz);
+                dz4<GATED, ACT, DT, C>(a[i], g[i], w, hb, sc[i], dz);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     sa[k] = __fmaf_rn(dz[k], __fmul_rn((float)a[i][k], sc[i]), sa[k]);

@@ -251,7 +251,7 @@ __device__ __forceinline__ void ep_values(const EpParams& p, const uint32_t (&v)
 #pragma unroll
             for (int i = 0; i < O; ++i) o[i] = __fadd_rn(o[i], bi);
         }
-        ep::apply_act<O>(o, p.act);
+        ep::apply_act<O>(o, p.act, p.dtype);
     } else {
         static_assert(2 * O == S, "one value per pair of sums");
         const bool odd = lane & 1;
@@ -268,7 +268,7 @@ __device__ __forceinline__ void ep_values(const EpParams& p, const uint32_t (&v)
             o[i] = odd ? got : z0;
             up[i] = odd ? z1 : got;
         }
-        ep::apply_act<O>(o, p.act);
+        ep::apply_act<O>(o, p.act, p.dtype);
 #pragma unroll
         for (int i = 0; i < O; ++i) o[i] = __fmul_rn(o[i], up[i]);
     }
