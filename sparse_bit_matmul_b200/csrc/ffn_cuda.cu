@@ -371,23 +371,6 @@ int launch_tc(const int8_t* b, int64_t ld, tc::EpParams p, const TilePlan& plan,
                                   dim3((unsigned)std::max(1, plan.cluster)), map, maps, p));
 }
 
-// Weight of an epilogue for plan_tiles, beside a bare linear layer's: the
-// activation's instructions, the residual, fp32 stores, kept sums.
-double epilogue_weight(int dtype, int act, bool res, bool acc, bool gated)
-{
-    const double a = act == SHERRY_ACT_NONE                              ? 0.0
-                     : act == SHERRY_ACT_RELU || act == SHERRY_ACT_RELU2 ? 0.1
-                     : act == SHERRY_ACT_GELU                            ? 0.7
-                                                                         : 0.55;
-    const double w = 1.0 + a + (res ? 0.5 : 0.0) + (dtype == SHERRY_F32 ? 0.3 : 0.0) + (acc ? 0.4 : 0.0);
-    return gated ? 0.75 * w : w;
-}
-
-TilePlan forward_plan(int dtype, int act, bool res, bool acc, bool gated, int64_t M, int64_t R, int64_t K, int sms)
-{
-    return plan_tiles(M, sherry_row_tiles(R), sherry_k_chunks(K), sms, epilogue_weight(dtype, act, res, acc, gated), false);
-}
-
 // Few tokens: the decode kernel, when it has a plan for the shape.
 bool forward_few(int64_t M, int64_t R, int64_t K, int sms, decode::Plan* pl)
 {
@@ -560,11 +543,6 @@ size_t forward_split_bytes(int dtype, int act, bool res, bool acc, bool gated, i
 // one of them and not parts of two.
 int64_t digit_ld(int64_t R) { return (R + 127) & ~int64_t(127); }
 
-int64_t digit_rows(int dtype, int64_t M)
-{
-    return dtype == SHERRY_F32 ? 4 * M : (M + 4) / 5 * 16;
-}
-
 int64_t digit_bytes(int dtype, int64_t M, int64_t R)
 {
     return (digit_rows(dtype, M) * digit_ld(R) + 255) & ~int64_t(255);
@@ -575,13 +553,6 @@ constexpr int64_t kGradMaxRows = (int64_t(1) << 24) - 1;
 bool grad_shape_ok(int64_t M, int64_t R, int64_t K)
 {
     return sherry_shape_ok(M, R, K) && R <= kGradMaxRows && M <= SHERRY_MAX_DIM / 4;
-}
-
-// Split tiles stay within what sherry_reserve(sherry_grad_digits(dtype) M, ..) sets aside.
-TilePlan grad_plan(int dtype, int64_t M, int64_t R, int64_t K, int sms)
-{
-    return plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), sms, 0.3, true,
-                      tc_token_tile(sherry_grad_digits(dtype) * M));
 }
 
 int backward(const void* dy, int dtype, const int32_t* acc, const float* x_scale, const void* wt, const float* alpha,
@@ -753,7 +724,7 @@ size_t sherry_transposed_bytes(int64_t R, int64_t K)
     return (size_t)sherry_row_tiles(R) * (size_t)sherry_k_chunks(K) * SHERRY_T2_CHUNK_BYTES;
 }
 
-int sherry_grad_digits(int dtype) { return dtype == SHERRY_BF16 ? 2 : dtype == SHERRY_F32 || dtype == SHERRY_F16 ? 4 : 0; }
+int sherry_grad_digits(int dtype) { return grad_digits(dtype); }
 
 size_t sherry_grad_work_bytes(int dtype, int64_t M, int64_t R)
 {

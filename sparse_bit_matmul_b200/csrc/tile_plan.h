@@ -4,6 +4,9 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "sherry.h"
+#include "sherry_internal.h"
+
 namespace sherry {
 
 // Token tile of the tensor-core kernel for M tokens (the dispatch of
@@ -114,6 +117,39 @@ inline int64_t split_tiles(const TilePlan& plan, int64_t T)
 inline TilePlan plan_tiles(int64_t M, int64_t TN, int64_t Kc, int64_t sms, double w, bool grad)
 {
     return plan_tiles(M, TN, Kc, sms, w, grad, tc_token_tile(M));
+}
+
+// Weight of an epilogue for plan_tiles, beside a bare linear layer's: the
+// activation's instructions, the residual, fp32 stores, kept sums.
+inline double epilogue_weight(int dtype, int act, bool res, bool acc, bool gated)
+{
+    const double a = act == SHERRY_ACT_NONE                              ? 0.0
+                     : act == SHERRY_ACT_RELU || act == SHERRY_ACT_RELU2 ? 0.1
+                     : act == SHERRY_ACT_GELU                            ? 0.7
+                                                                         : 0.55;
+    const double w = 1.0 + a + (res ? 0.5 : 0.0) + (dtype == SHERRY_F32 ? 0.3 : 0.0) + (acc ? 0.4 : 0.0);
+    return gated ? 0.75 * w : w;
+}
+
+inline TilePlan forward_plan(int dtype, int act, bool res, bool acc, bool gated, int64_t M, int64_t R, int64_t K, int sms)
+{
+    return plan_tiles(M, sherry_row_tiles(R), sherry_k_chunks(K), sms, epilogue_weight(dtype, act, res, acc, gated), false);
+}
+
+// Rows of int8 digits of M tokens' gradients: four a token, or 16 for five.
+inline int64_t digit_rows(int dtype, int64_t M)
+{
+    return dtype == SHERRY_F32 ? 4 * M : (M + 4) / 5 * 16;
+}
+
+// sherry_grad_digits
+inline int grad_digits(int dtype) { return dtype == SHERRY_BF16 ? 2 : dtype == SHERRY_F32 || dtype == SHERRY_F16 ? 4 : 0; }
+
+// Split tiles stay within what sherry_reserve(sherry_grad_digits(dtype) M, ..) sets aside.
+inline TilePlan grad_plan(int dtype, int64_t M, int64_t R, int64_t K, int sms)
+{
+    return plan_tiles(digit_rows(dtype, M), sherry_row_tiles(K), sherry_k_chunks(R), sms, 0.3, true,
+                      tc_token_tile(grad_digits(dtype) * M));
 }
 
 }  // namespace sherry
