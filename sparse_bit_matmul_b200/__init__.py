@@ -677,7 +677,7 @@ class GatedFFN:
     def backward(self, dy, kept, want_dx: bool = True, want_scales: bool = True):
         """(dx, dalpha fp32 [2F] interleaved, dalpha of the down projection fp32 [K2]); the gradient of the
         residual is dy itself."""
-        _need(self.w_t is not None, "backward: the block was made without trainable=True")
+        _need(self.w_t is not None or not want_dx, "backward: the block was made without trainable=True")
         acc, s, acc_d, s_d = kept
         dh, dalpha_d, _ = self.down.backward(dy, acc_d, s_d, want_scales=want_scales)
         dx, dalpha, _ = gated_backward(dh, self.w_t, self.alpha, self.K, acc, s, act=self.act, want_dx=want_dx,

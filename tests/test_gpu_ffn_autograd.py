@@ -62,3 +62,16 @@ def test_block_inside_an_autograd_function():
         want, kept = b.forward(x, residual=x, keep=True)
         dx, dalpha, _ = b.backward(dy, kept)
     assert torch.equal(y, want) and torch.equal(x.grad, dx + dy) and torch.equal(alpha.grad, dalpha)
+
+
+def test_scales_alone_need_no_transposed_gate():
+    """backward(want_dx=False) reads the down projection's transposed weight only."""
+    b = _block()
+    lean = sbm.GatedFFN(b.w_native, b.alpha, b.down, b.F, b.K, b.act)
+    x, dy = torch.randn(9, 96, device="cuda"), torch.randn(9, 96, device="cuda")
+    _, kept = lean.forward(x, keep=True)
+    want = b.backward(dy, kept)
+    got = lean.backward(dy, kept, want_dx=False)
+    assert got[0] is None and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    with pytest.raises(ValueError, match="trainable"):
+        lean.backward(dy, kept)
