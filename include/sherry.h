@@ -444,10 +444,11 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  * token's others, the columns of dx whose weight in that row is 0 are off by
  * about 7e-8 r (SHERRY_F32: 5e-10 r) of themselves, above the rounding of the
  * type from r = 20000 (SHERRY_BF16), 3000 (SHERRY_F16) or 100 (SHERRY_F32)
- * on.  A token whose dz * alpha holds an
- * Inf or NaN gives a dx row of NaN.  Results do not depend on the launch
- * shape or on the order of any sum across blocks: the same call gives the
- * same bits.
+ * on.  A token whose dz * alpha holds an Inf or NaN gives a dx row of NaN.
+ * dx does not depend on how the work is split; dalpha and dbias are fp32 sums
+ * over the tokens, grouped by the sizes and the device's number of SMs, in
+ * chains of at most M / 16 + 20 additions.  No sum depends on the order in
+ * which blocks run: the same call gives the same bits.
  * Tensors are dense row-major and start at a multiple of their element size
  * (x, x_i8, the weights and the buffers of bytes: of 16; the acc of a gradient:
  * of 8), or the call is refused.  Errors are those of sherry_linear.  An output

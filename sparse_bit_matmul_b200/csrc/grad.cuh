@@ -532,12 +532,12 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kColWarps ? kColBlocks : 
 }
 
 // Both in one launch, for few tokens, where a launch costs more than the work
-// (M=5 K=1024, gated to 2816, bf16: 13.6 -> 11.3 us for the call, 21.9 -> 19.2 us with the host): clusters of
+// (M=5 K=1024, gated to 2816, bf16: 12.4 -> 9.6 us for the call): clusters of
 // `cluster` blocks, the first `ahead` of them the tokens' digits (a cluster per
 // token, or with `whole` a block), the others column sums, whose order does not
 // depend on whether the digits are wanted.  In two launches and in one: M=750
-// K=640, gated to 1197, bf16 29.0 and 22.0 us, M=1000, 4096 x 4096, bf16 47.5 and
-// 44.2; M=2048 K=4096, gated to 14336, 511 and 536.  Four blocks an SM, so that
+// K=640, gated to 1197, bf16 30.9 and 23.1 us, M=1000, 4096 x 4096, bf16 64.5 and
+// 61.7; M=2048 K=4096, gated to 14336, 754 and 795.  Four blocks an SM, so that
 // the digits of other tokens hide a token's two passes; the column sums load
 // fewer tokens at once for it (M=300 K=2080, gated to 5001, f16: 48.1 -> 44.0 us;
 // M=380 K=1056 N=10001 f32 gelu 64 -> 56).

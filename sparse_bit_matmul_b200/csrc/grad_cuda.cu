@@ -91,8 +91,8 @@ int ahead(const Params& p, int sms, cudaStream_t stream)
     const bool sums = p.dalpha || p.dbias;
     if (sums && p.M <= kBothMaxTokens) return both<GATED, ACT, DT>(p, true, sms, stream);
     // the digits first: the column sums then find their inputs in the second-level
-    // cache (M=2048 K=14336 N=4096 bf16: 199 us for the call, 210 the other way
-    // round; with the column sums after the product 212)
+    // cache (M=2048 K=14336 N=4096 bf16: 295 us for the call, 305 the other way
+    // round; gated M=1386 K=1504 N=14319 f16: 333 and 352)
     const int st = digits<GATED, ACT, DT>(p, sms, stream);
     return st != SHERRY_OK || !sums ? st : columns<GATED, ACT, DT>(p, sms, stream);
 }
