@@ -458,10 +458,10 @@ int sherry_w4a8_gemm(const int8_t* x_i8, const float* x_scale, const void* W4nat
  * least the bytes that the matching _split_bytes function gives on the same
  * device, 16-byte aligned, any contents, this call's alone until it has
  * completed; fewer bytes than it needs: SHERRY_ERR_WORKSPACE), so that calls
- * with buffers of their own may run at the same time.  The other forms, and
- * split == NULL, use the reserved workspace, and the rule at the top of this
- * file holds for them: no two at the same time on one device, replays of
- * captured graphs included.
+ * with buffers of their own, x_i8 and x_scale included, may run at the same
+ * time.  The other forms, split == NULL and x_i8 == NULL use the reserved
+ * workspace, and the rule at the top of this file holds for them: no two at the
+ * same time on one device, replays of captured graphs included.
  * =========================================================================== */
 
 /* sherry_quant_act for x of any element type (x [M][K], 16-byte aligned).  A

@@ -641,7 +641,8 @@ class GatedFFN:
     ``GatedFFN.from_weights(W_gate, W_up, W_down)`` (fp32 [F][K], [F][K], [K2][F]) packs on the host;
     ``forward(x, residual)`` is two contractions, each with its epilogue.  With ``trainable=True``,
     ``forward(x, residual, keep=True)`` also returns what ``backward(dy, kept)`` needs for the gradients
-    of x and of the scales (the packed weights themselves stay as they are).
+    of x and of the scales (the packed weights themselves stay as they are).  Autograd does not record
+    them: see linear_epilogue.
     """
 
     def __init__(self, w_native, alpha, down: PackedLinear, F: int, K: int, act: str = "silu", w_t=None):
