@@ -21,7 +21,7 @@ st = torch.cuda.current_stream().cuda_stream
 seven = lambda *shape, dtype=torch.float32: torch.full(shape, 7, dtype=dtype, device="cuda")
 refused = 0
 bf16 = torch.bfloat16
-for M, N, K in ((3, 128, 10240), (17, 768, 30720), (65, 3200, 20480)):
+for M, N, K in ((3, 128, 10240), (17, 768, 30688), (65, 3200, 20480)):
     w, alpha = torch.zeros(sbm.native_bytes(N, K), dtype=torch.uint8, device="cuda"), torch.ones(N, device="cuda")
     x, y = torch.ones(M, K, device="cuda", dtype=bf16), seven(M, N, dtype=bf16)
     q, s, acc = seven(M, K, dtype=torch.int8), seven(M), seven(M, N, dtype=torch.int32)
@@ -62,9 +62,9 @@ def test_refused_for_want_of_workspace_leaves_outputs_alone():
 
 # (gated, M, K, N): launches that split tiles of 16, 32, 64, 128 and 192 tokens through the workspace
 SPLIT_FORWARD = [(False, 3, 10240, 128), (True, 17, 51200, 256), (False, 33, 20480, 2432), (False, 65, 20480, 3200),
-                 (True, 1537, 30720, 256), (False, 1537, 14336, 2176)]
+                 (True, 1537, 30688, 256), (False, 1537, 14336, 2176)]
 # (M, K, R) of gradients
-SPLIT_GRADIENT = [(3, 128, 10240), (16, 512, 20480), (31, 2176, 10240), (33, 3200, 20480), (1000, 256, 30720)]
+SPLIT_GRADIENT = [(3, 128, 10240), (16, 512, 20480), (31, 2176, 10240), (33, 3200, 20480), (1000, 256, 30688)]
 
 
 def _bytes(n, seed):
